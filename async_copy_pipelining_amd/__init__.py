@@ -37,8 +37,9 @@ _lib = ctypes.CDLL(LIB_PATH)
 ACP_OK, ACP_ERR_INVALID, ACP_ERR_DECLINED, ACP_ERR_UNSUPPORTED, ACP_ERR_LDS, ACP_ERR_HIP = range(6)
 STATUS_NAMES = {0: "OK", 1: "INVALID", 2: "DECLINED", 3: "UNSUPPORTED", 4: "LDS", 5: "HIP"}
 # acp_dtype
-ACP_U8, ACP_U16, ACP_U32, ACP_U64, ACP_F16, ACP_F32 = range(6)
-DTYPES = {"u8": ACP_U8, "u16": ACP_U16, "u32": ACP_U32, "u64": ACP_U64, "f16": ACP_F16, "f32": ACP_F32}
+ACP_U8, ACP_U16, ACP_U32, ACP_U64, ACP_F16, ACP_F32, ACP_BF16 = range(7)
+DTYPES = {"u8": ACP_U8, "u16": ACP_U16, "u32": ACP_U32, "u64": ACP_U64, "f16": ACP_F16, "f32": ACP_F32,
+          "bf16": ACP_BF16}
 # acp_swizzle / acp_oob
 ACP_SWIZZLE_NONE, ACP_SWIZZLE_32B, ACP_SWIZZLE_64B, ACP_SWIZZLE_128B = 0, 1, 2, 3
 ACP_OOB_ZERO = 0
@@ -46,6 +47,11 @@ ACP_OOB_ZERO = 0
 ACP_OP_ZERO, ACP_OP_SQRT, ACP_OP_EXP, ACP_OP_ADD, ACP_OP_MUL, ACP_OP_FMA, ACP_OP_COPY = range(7)
 OPS = {"zero": ACP_OP_ZERO, "sqrt": ACP_OP_SQRT, "exp": ACP_OP_EXP, "add": ACP_OP_ADD,
        "mul": ACP_OP_MUL, "fma": ACP_OP_FMA, "copy": ACP_OP_COPY}
+# acp_pack_format / acp_activation
+ACP_PACK_I8, ACP_PACK_E4M3 = range(2)
+FORMATS = {"i8": ACP_PACK_I8, "e4m3": ACP_PACK_E4M3}
+ACP_ACT_NONE, ACP_ACT_SILU, ACP_ACT_GELU = range(3)
+ACTIVATIONS = {"none": ACP_ACT_NONE, "silu": ACP_ACT_SILU, "gelu": ACP_ACT_GELU}
 ACP_MAX_RANK = 5
 
 
@@ -76,6 +82,18 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _DESC_P = ctypes.POINTER(acp_tile_desc)
 
+
+class acp_packed8(ctypes.Structure):
+    """A tensor in 8 bits: descriptor of its codes, float32 scales, format, block."""
+    _fields_ = [("codes", _DESC_P), ("scales", _P), ("format", ctypes.c_int32), ("block", ctypes.c_int32)]
+
+    def __init__(self, codes: acp_tile_desc, scales, fmt, block: int):
+        super().__init__(ctypes.pointer(codes), _ptr(scales),
+                         FORMATS[fmt] if isinstance(fmt, str) else int(fmt), int(block))
+
+
+_PACKED_P = ctypes.POINTER(acp_packed8)
+
 _SIGS = {
     "acp_abi_version": ([], _I),
     "acp_last_error": ([], ctypes.c_char_p),
@@ -89,6 +107,15 @@ _SIGS = {
     "acp_tile_reduce": ([_I, _DESC_P, _DESC_P, _I, _P], _I),
     "acp_stream_reduce_rows": ([_I, _P, _DESC_P, ctypes.POINTER(ctypes.c_int32), _I, _I, _I, _P], _I),
     "acp_stream_binary": ([_I, _DESC_P, _DESC_P, _DESC_P, ctypes.POINTER(ctypes.c_int32), _I, _I, _I, _I, _P], _I),
+    "acp_pack8": ([_PACKED_P, _DESC_P, _P], _I),
+    "acp_unpack8": ([_DESC_P, _PACKED_P, _P], _I),
+    "acp_act_forward": ([_I, _DESC_P, _DESC_P, _DESC_P, _PACKED_P, _PACKED_P, _P], _I),
+    "acp_act_backward": ([_I, _DESC_P, _DESC_P, _DESC_P, _PACKED_P, _PACKED_P, _P], _I),
+    "acp_group_norm_workspace": ([_DESC_P, _I, ctypes.POINTER(ctypes.c_int64)], _I),
+    "acp_group_norm": ([_DESC_P, _DESC_P, _P, _P, _I, ctypes.c_float, _I, _P, _P, _PACKED_P, _P, ctypes.c_int64, _P],
+                       _I),
+    "acp_group_norm_backward": ([_DESC_P, _P, _P, _DESC_P, _DESC_P, _PACKED_P, _P, _P, _P, _P, _I, _I, _P,
+                                 ctypes.c_int64, _P], _I),
     "acp_debug_lds_image": ([_DESC_P, ctypes.c_int64, _I, _P, _P], _I),
     "acp_debug_ring_trace": ([_I, _I, _I, _I, _P, _P], _I),
     "acp_debug_stream_copy": ([_P, _P, ctypes.c_int64, _I, _P], _I),
@@ -204,6 +231,55 @@ def acp_stream_binary(op, out: acp_tile_desc, x: acp_tile_desc, z: acp_tile_desc
     sb = (ctypes.c_int32 * len(stage_box))(*stage_box)
     _check(_lib.acp_stream_binary(opc, ctypes.byref(out), ctypes.byref(x), ctypes.byref(z), sb, int(stages),
                                   int(threads), int(workgroups), stg, _stream(stream)))
+
+
+def _ref(x):
+    return None if x is None else ctypes.byref(x)
+
+
+def _act(act) -> int:
+    return ACTIVATIONS[act] if isinstance(act, str) else int(act)
+
+
+def acp_pack8(out: acp_packed8, x: acp_tile_desc, stream=None) -> None:
+    _check(_lib.acp_pack8(_ref(out), _ref(x), _stream(stream)))
+
+
+def acp_unpack8(out: acp_tile_desc, src: acp_packed8, stream=None) -> None:
+    _check(_lib.acp_unpack8(_ref(out), _ref(src), _stream(stream)))
+
+
+def acp_act_forward(act, out: acp_tile_desc, x: acp_tile_desc, z: acp_tile_desc | None = None,
+                    save_x: acp_packed8 | None = None, save_z: acp_packed8 | None = None, stream=None) -> None:
+    _check(_lib.acp_act_forward(_act(act), _ref(out), _ref(x), _ref(z), _ref(save_x), _ref(save_z), _stream(stream)))
+
+
+def acp_act_backward(act, dx: acp_tile_desc, dz: acp_tile_desc | None, dy: acp_tile_desc, x: acp_packed8,
+                     z: acp_packed8 | None = None, stream=None) -> None:
+    _check(_lib.acp_act_backward(_act(act), _ref(dx), _ref(dz), _ref(dy), _ref(x), _ref(z), _stream(stream)))
+
+
+def acp_group_norm_workspace(x: acp_tile_desc, groups: int) -> int:
+    n = ctypes.c_int64()
+    _check(_lib.acp_group_norm_workspace(_ref(x), int(groups), ctypes.byref(n)))
+    return n.value
+
+
+def acp_group_norm(y: acp_tile_desc, x: acp_tile_desc, gamma, beta, groups: int, eps: float, act="none", mean=None,
+                   rstd=None, save: acp_packed8 | None = None, workspace=None, workspace_bytes: int = 0,
+                   stream=None) -> None:
+    _check(_lib.acp_group_norm(_ref(y), _ref(x), _ptr(gamma), _ptr(beta), int(groups), float(eps), _act(act),
+                               _ptr(mean), _ptr(rstd), _ref(save), _ptr(workspace), int(workspace_bytes),
+                               _stream(stream)))
+
+
+def acp_group_norm_backward(dx: acp_tile_desc, dgamma, dbeta, dy: acp_tile_desc, x: acp_tile_desc | acp_packed8,
+                            mean, rstd, gamma, beta, groups: int, act="none", workspace=None,
+                            workspace_bytes: int = 0, stream=None) -> None:
+    plain, saved = (None, x) if isinstance(x, acp_packed8) else (x, None)
+    _check(_lib.acp_group_norm_backward(_ref(dx), _ptr(dgamma), _ptr(dbeta), _ref(dy), _ref(plain), _ref(saved),
+                                        _ptr(mean), _ptr(rstd), _ptr(gamma), _ptr(beta), int(groups), _act(act),
+                                        _ptr(workspace), int(workspace_bytes), _stream(stream)))
 
 
 def acp_debug_lds_image(src: acp_tile_desc, tile_index: int, threads: int, out_bytes, stream=None) -> None:

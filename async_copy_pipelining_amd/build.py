@@ -27,7 +27,7 @@ DEVICE = ["--offload-arch=gfx950", "-Xclang", "-target-feature", "-Xclang", "-pa
 
 SOURCES = [
     ("acp_plan.cpp", False),
-    ("acp_api.cpp", False),
+    ("acp_entry.cpp", False),
     ("acp_engine.hip", True),
     ("acp_k_copy.hip", True),
     ("acp_k_tile.hip", True),
@@ -36,6 +36,8 @@ SOURCES = [
     ("acp_k_stream_f32.hip", True),
     ("acp_k_stream_f16.hip", True),
     ("acp_k_ref.hip", True),
+    ("acp_k_pack8.hip", True),
+    ("acp_k_norm.hip", True),
 ]
 
 

@@ -1,0 +1,346 @@
+// Device side of the row operators: chunk loads and stores, the activations,
+// and the 8-bit forms.
+#pragma once
+
+#include <type_traits>
+
+#include "acp_engine.hpp"
+#include "acp_rows.hpp"
+
+namespace acp {
+namespace dev {
+
+typedef unsigned rw4 __attribute__((ext_vector_type(4)));
+typedef unsigned rw2 __attribute__((ext_vector_type(2)));
+// the same at any byte address
+typedef rw4 rw4_any __attribute__((aligned(1)));
+typedef rw2 rw2_any __attribute__((aligned(1)));
+typedef unsigned rw1_any __attribute__((aligned(1)));
+typedef float rf2 __attribute__((ext_vector_type(2)));
+
+struct bf16_t {
+  uint16_t bits;
+};
+
+__device__ __forceinline__ uint32_t divide(uint32_t n, const Div& d) {
+  return static_cast<uint32_t>((static_cast<uint64_t>(n) * d.mag) >> (31 + d.sh));
+}
+
+__device__ __forceinline__ float as_float(uint32_t u) { return __builtin_bit_cast(float, u); }
+__device__ __forceinline__ uint32_t as_bits(float f) { return __builtin_bit_cast(uint32_t, f); }
+
+// ---------------------------------------------------------------- 16-byte chunks
+
+template <class T>
+constexpr int kChunk = 16 / static_cast<int>(sizeof(T));
+
+__device__ __forceinline__ void widen(const rw4& r, float (&f)[8], const _Float16*) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+    const uint32_t w = r[k];  // a scalar: a bit cast of the vector's element would read element 0
+    const h2 h = __builtin_bit_cast(h2, w);
+    f[2 * k] = static_cast<float>(h[0]);
+    f[2 * k + 1] = static_cast<float>(h[1]);
+  }
+}
+__device__ __forceinline__ void widen(const rw4& r, float (&f)[8], const bf16_t*) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    f[2 * k] = as_float(r[k] << 16);
+    f[2 * k + 1] = as_float(r[k] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void widen(const rw4& r, float (&f)[4], const float*) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) f[k] = as_float(r[k]);
+}
+
+// One rounding to nearest, ties to even, from the float32 result.
+__device__ __forceinline__ rw4 narrow(const float (&f)[8], const _Float16*) {
+  rw4 r;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+    const h2 h = {static_cast<_Float16>(f[2 * k]), static_cast<_Float16>(f[2 * k + 1])};
+    r[k] = __builtin_bit_cast(uint32_t, h);
+  }
+  return r;
+}
+__device__ __forceinline__ rw4 narrow(const float (&f)[8], const bf16_t*) {
+  rw4 r;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    const b2 h = {static_cast<__bf16>(f[2 * k]), static_cast<__bf16>(f[2 * k + 1])};
+    r[k] = __builtin_bit_cast(uint32_t, h);
+  }
+  return r;
+}
+__device__ __forceinline__ rw4 narrow(const float (&f)[4], const float*) {
+  rw4 r;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) r[k] = as_bits(f[k]);
+  return r;
+}
+
+// `n` channels at p (all of a chunk, or fewer at a row's end; none for n <= 0);
+// channels past n read as zero.
+template <class T>
+__device__ __forceinline__ rw4 load_chunk(const char* p, int n) {
+  constexpr int V = kChunk<T>;
+  if (n >= V) return __builtin_nontemporal_load(reinterpret_cast<const rw4_any*>(p));
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int k = 0; k < V - 1; ++k)
+    if (k < n) {
+      if constexpr (sizeof(T) == 2)
+        w[k / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[k]) << (16 * (k & 1));
+      else
+        w[k] = reinterpret_cast<const uint32_t*>(p)[k];
+    }
+  return rw4{w[0], w[1], w[2], w[3]};
+}
+
+template <class T>
+__device__ __forceinline__ void store_chunk_n(char* p, int n, const rw4& r) {
+  constexpr int V = kChunk<T>;
+  if (n >= V) {
+    __builtin_nontemporal_store(r, reinterpret_cast<rw4_any*>(p));
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < V - 1; ++k)
+    if (k < n) {
+      if constexpr (sizeof(T) == 2)
+        reinterpret_cast<uint16_t*>(p)[k] = static_cast<uint16_t>(r[k / 2] >> (16 * (k & 1)));
+      else
+        reinterpret_cast<uint32_t*>(p)[k] = r[k];
+    }
+}
+
+// The codes of a chunk: V bytes in V / 4 words.
+template <int V>
+struct Codes {
+  uint32_t w[V / 4];
+};
+
+template <int V>
+__device__ __forceinline__ Codes<V> load_codes(const char* p, int n) {
+  Codes<V> c;
+  if (n >= V) {
+    if constexpr (V == 8) {
+      const rw2 r = __builtin_nontemporal_load(reinterpret_cast<const rw2_any*>(p));
+      c.w[0] = r[0];
+      c.w[1] = r[1];
+    } else {
+      c.w[0] = __builtin_nontemporal_load(reinterpret_cast<const rw1_any*>(p));
+    }
+    return c;
+  }
+#pragma unroll
+  for (int k = 0; k < V / 4; ++k) c.w[k] = 0u;
+#pragma unroll
+  for (int k = 0; k < V - 1; ++k)
+    if (k < n) c.w[k / 4] |= static_cast<uint32_t>(reinterpret_cast<const uint8_t*>(p)[k]) << (8 * (k & 3));
+  return c;
+}
+
+template <int V>
+__device__ __forceinline__ void store_codes(char* p, int n, const Codes<V>& c) {
+  if (n >= V) {
+    if constexpr (V == 8) {
+      __builtin_nontemporal_store(rw2{c.w[0], c.w[1]}, reinterpret_cast<rw2_any*>(p));
+    } else {
+      __builtin_nontemporal_store(c.w[0], reinterpret_cast<rw1_any*>(p));
+    }
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < V - 1; ++k)
+    if (k < n) reinterpret_cast<uint8_t*>(p)[k] = static_cast<uint8_t>(c.w[k / 4] >> (8 * (k & 3)));
+}
+
+// ---------------------------------------------------------------- 8-bit forms
+
+// Scale of a block from the bits of its largest |x| (an unsigned maximum of
+// the sign-less bits, which puts NaN above infinity above every number).
+//   i8:   max(fl(amax / 127), 2^-126), at most the largest float32 whose
+//         127-fold is finite
+//   e4m3: the smallest power of two >= 2^-126 with amax <= 448 * scale
+//   a NaN or an infinity in the block: NaN, so all of it unpacks to NaN
+__device__ __forceinline__ float block_scale(int format, uint32_t amax) {
+  if (amax >= 0x7F800000u) return as_float(0x7FC00000u);
+  if (format == 0) {
+    const float s = as_float(amax) / 127.0f;
+    return __builtin_fminf(__builtin_fmaxf(s, 0x1p-126f), 0x1.020406p+121f);
+  }
+  // amax = m 2^k with 1 <= m < 2, and 448 = 1.75 * 2^8
+  const int e = static_cast<int>(amax >> 23) - 8 + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return as_float(static_cast<uint32_t>(e < 1 ? 1 : e) << 23);
+}
+
+// Codes of x in a block of scale s.
+//
+// i8: round-half-even of the exact quotient x / s.  t = x * (1/s) is within
+// 127 * 2^-21 of it, so its rounding q can only be wrong where t lies within
+// 2^-13 of a half; there the remainder x - q s decides, which one fma gives
+// exactly (it is a multiple of half an ulp of s and at most about s / 2).
+// Adding 1.5 * 2^23 rounds t and leaves the two's complement code in the low
+// byte.
+// e4m3: x / s is exact (s is a power of two); the conversion rounds to
+// nearest even, and |x / s| <= 448 is the format's largest value.  Under the
+// scale of T's own largest values, 256 s would be past them: those that would
+// round to it take 240 s.
+template <class T>
+constexpr float kTopScale = std::is_same_v<T, _Float16> ? 0x1p8f : 0x1p120f;
+
+template <class T, int V>
+__device__ __forceinline__ Codes<V> encode(int format, float (&x)[V], float s) {
+  Codes<V> c;
+  if (format == 0) {
+    constexpr float kRound = 12582912.0f;
+    const float inv = __builtin_amdgcn_rcpf(s);
+    float u[V], off = 0.0f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const float t = x[k] * inv;
+      u[k] = t + kRound;
+      off = __builtin_fmaxf(off, __builtin_fabsf(t - (u[k] - kRound)));
+    }
+    if (off > 0.4998f) {
+      const float half = 0.5f * s;
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const float q = u[k] - kRound;
+        const float r = __builtin_fmaf(-q, s, x[k]);
+        const float a = __builtin_fabsf(r);
+        if (a > half || (a == half && (as_bits(u[k]) & 1u))) u[k] += __builtin_copysignf(1.0f, r);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < V / 4; ++k) {
+      const uint32_t lo = __builtin_amdgcn_perm(as_bits(u[4 * k + 1]), as_bits(u[4 * k]), 0x0C0C0400u);
+      const uint32_t hi = __builtin_amdgcn_perm(as_bits(u[4 * k + 3]), as_bits(u[4 * k + 2]), 0x04000C0Cu);
+      c.w[k] = lo | hi;
+    }
+  } else {
+    const float inv = as_float((254u << 23) - as_bits(s));
+    if (s >= kTopScale<T>) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) x[k] = __builtin_fminf(__builtin_fmaxf(x[k], -240.0f * s), 240.0f * s);
+    }
+#pragma unroll
+    for (int k = 0; k < V / 4; ++k) {
+      int w = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * k] * inv, x[4 * k + 1] * inv, 0, false);
+      w = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * k + 2] * inv, x[4 * k + 3] * inv, w, true);
+      c.w[k] = static_cast<uint32_t>(w);
+    }
+  }
+  return c;
+}
+
+// The values that codes stand for: code * s, rounded once to float32.
+template <int V>
+__device__ __forceinline__ void decode(int format, const Codes<V>& c, float s, float (&x)[V]) {
+  if (format == 0) {
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      x[k] = static_cast<float>(static_cast<int8_t>(c.w[k / 4] >> (8 * (k & 3)))) * s;
+  } else {
+#pragma unroll
+    for (int k = 0; k < V / 4; ++k) {
+      const rf2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(c.w[k]), false);
+      const rf2 b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(c.w[k]), true);
+      x[4 * k] = a[0] * s;
+      x[4 * k + 1] = a[1] * s;
+      x[4 * k + 2] = b[0] * s;
+      x[4 * k + 3] = b[1] * s;
+    }
+  }
+}
+
+// Largest |x| of the 2^lb lanes that share a scale block, as bits.  The lanes
+// of a block are aligned to 2^lb within their wave.
+template <int V>
+__device__ __forceinline__ uint32_t block_amax(const float (&x)[V], int lb) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const uint32_t b = as_bits(x[k]) & 0x7FFFFFFFu;
+    m = b > m ? b : m;
+  }
+  for (int k = 0; k < lb; ++k) {
+    const uint32_t o = static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 1 << k));
+    m = o > m ? o : m;
+  }
+  return m;
+}
+
+// ---------------------------------------------------------------- activations
+
+constexpr int kActNone = 0, kActSilu = 1, kActGelu = 2;
+
+// 1 / (1 + e^-u): the hardware exponential and reciprocal, each within an
+// ulp; the argument's rounding adds |u| 2^-24 relative, under 2^-20 where the
+// result is not negligible.
+__device__ __forceinline__ float sigmoid(float u) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u * -1.44269504088896341f));
+}
+
+__device__ __forceinline__ float normal_cdf(float u) { return 0.5f + 0.5f * erff(u * 0.70710678118654752f); }
+
+// act(u)
+template <int ACT>
+__device__ __forceinline__ float act_value(float u) {
+  if constexpr (ACT == kActSilu) return u * sigmoid(u);
+  if constexpr (ACT == kActGelu) return u * normal_cdf(u);
+  return u;
+}
+
+// act(u) and act'(u)
+template <int ACT>
+__device__ __forceinline__ void act_both(float u, float* value, float* slope) {
+  if constexpr (ACT == kActSilu) {
+    const float s = sigmoid(u);
+    *value = u * s;
+    *slope = s * (1.0f + u * (1.0f - s));
+  } else if constexpr (ACT == kActGelu) {
+    const float p = normal_cdf(u);
+    *value = u * p;
+    *slope = p + u * (0.398942280401432678f * __builtin_amdgcn_exp2f(u * u * -0.721347520444481704f));
+  } else {
+    *value = u;
+    *slope = 1.0f;
+  }
+}
+
+template <int ACT, int V>
+__device__ __forceinline__ void act_values(float (&u)[V]) {
+#pragma unroll
+  for (int k = 0; k < V; ++k) u[k] = act_value<ACT>(u[k]);
+}
+
+template <int V>
+__device__ __forceinline__ void act_values(int act, float (&u)[V]) {
+  if (act == kActSilu) act_values<kActSilu, V>(u);
+  else if (act == kActGelu) act_values<kActGelu, V>(u);
+}
+
+// value = act(u) and slope = act'(u), channel by channel
+template <int V>
+__device__ __forceinline__ void act_pairs(int act, const float (&u)[V], float (&value)[V], float (&slope)[V]) {
+  if (act == kActSilu) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) act_both<kActSilu>(u[k], &value[k], &slope[k]);
+  } else if (act == kActGelu) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) act_both<kActGelu>(u[k], &value[k], &slope[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k) act_both<kActNone>(u[k], &value[k], &slope[k]);
+  }
+}
+
+}  // namespace dev
+}  // namespace acp

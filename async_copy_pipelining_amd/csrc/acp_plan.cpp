@@ -48,6 +48,7 @@ int dtype_size(int dtype) {
     case 3: return 8;  // u64
     case 4: return 2;  // f16
     case 5: return 4;  // f32
+    case 6: return 2;  // bf16
     default: return -1;
   }
 }

@@ -1,0 +1,645 @@
+// Entry points of the row operators: 8-bit checkpoints, activations, group
+// norm.  Included by acp_entry.cpp after acp_api.cpp, whose helpers it uses.
+// Host code: checks, the collapse of the tensors' outer dims, and the split of
+// the work; one to three kernels on the caller's stream.
+#include <algorithm>
+#include <cmath>
+
+#include "acp_rows.hpp"
+
+namespace {
+
+int row_dtype(int dtype) {
+  return dtype == ACP_F16 ? acp::kRowF16 : dtype == ACP_BF16 ? acp::kRowBF16 : dtype == ACP_F32 ? acp::kRowF32 : -1;
+}
+
+acp::Div div_by(uint64_t d) {
+  acp::Div r;
+  r.d = static_cast<uint32_t>(d);
+  acp::magic_for(r.d, &r.mag, &r.sh);
+  return r;
+}
+
+bool same_shape(const acp::DescData& a, const acp::DescData& b) {
+  if (a.rank != b.rank) return false;
+  for (int d = 0; d < a.rank; ++d)
+    if (a.shape[d] != b.shape[d]) return false;
+  return true;
+}
+
+// Whether two elements of a tensor lie at one address.  Taken from the
+// strides in ascending order, each has to reach past everything inside it.
+bool self_overlap(const acp::DescData& t) {
+  int order[acp::kMaxInputRank];
+  int n = 0;
+  for (int d = 0; d < t.rank; ++d)
+    if (t.shape[d] > 1) order[n++] = d;
+  std::sort(order, order + n, [&](int a, int b) { return t.strides[a] < t.strides[b]; });
+  uint64_t span = 0;
+  for (int k = 0; k < n; ++k) {
+    if (static_cast<uint64_t>(t.strides[order[k]]) <= span) return true;
+    span += static_cast<uint64_t>(t.shape[order[k]] - 1) * static_cast<uint64_t>(t.strides[order[k]]);
+  }
+  return false;
+}
+
+int64_t elements(const acp::DescData& t) {
+  int64_t n = 1;
+  for (int d = 0; d < t.rank; ++d) n *= t.shape[d];
+  return n;
+}
+
+// A byte range that a call reads or writes.
+struct Range {
+  uint64_t at, bytes;
+  const char* what;
+};
+
+Range range_of(const acp::DescData& t, const char* what) { return {t.gbase, tensor_span(t), what}; }
+Range range_of(const void* p, int64_t bytes, const char* what) {
+  return {reinterpret_cast<uint64_t>(p), p ? static_cast<uint64_t>(bytes) : 0u, what};
+}
+
+// Written ranges share no byte with each other or with what is read.
+acp_status check_ranges(const Range* out, int n_out, const Range* in, int n_in) {
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = i + 1; j < n_out; ++j)
+      if (overlap(out[i].at, out[i].bytes, out[j].at, out[j].bytes))
+        return ret(ACP_ERR_INVALID, std::string(out[i].what) + " and " + out[j].what + " share memory");
+    for (int j = 0; j < n_in; ++j)
+      if (overlap(out[i].at, out[i].bytes, in[j].at, in[j].bytes))
+        return ret(ACP_ERR_INVALID, std::string(out[i].what) + " and " + in[j].what + " share memory");
+  }
+  return ACP_OK;
+}
+
+// A float tensor of a row operator.
+acp_status load_float(const acp_tile_desc* d, const char* what, acp::DescData* out) {
+  if (!load_desc(d, out)) return ret(ACP_ERR_INVALID, std::string(what) + " is not an encoded descriptor");
+  if (row_dtype(out->dtype) < 0) return ret(ACP_ERR_UNSUPPORTED, std::string(what) + " must be f16, bf16 or f32");
+  if (out->gbase % out->esize) return ret(ACP_ERR_INVALID, std::string(what) + " is not aligned to its element");
+  return ACP_OK;
+}
+
+acp_status load_packed(const acp_packed8* p, const acp::DescData& like, const char* what, acp::DescData* out) {
+  if (!p || !load_desc(p->codes, out))
+    return ret(ACP_ERR_INVALID, std::string(what) + " has no encoded descriptor of its codes");
+  if (out->dtype != ACP_U8) return ret(ACP_ERR_INVALID, std::string(what) + " holds u8 codes");
+  if (!p->scales || reinterpret_cast<uint64_t>(p->scales) % 4)
+    return ret(ACP_ERR_INVALID, std::string(what) + " needs 4-byte aligned scales");
+  if (p->format != ACP_PACK_I8 && p->format != ACP_PACK_E4M3)
+    return ret(ACP_ERR_INVALID, std::string(what) + " has an unknown 8-bit format");
+  if (p->block != 32 && p->block != 64 && p->block != 128 && p->block != 256)
+    return ret(ACP_ERR_INVALID, std::string(what) + " needs a block of 32, 64, 128 or 256");
+  if (!same_shape(*out, like)) return ret(ACP_ERR_INVALID, std::string(what) + " has another shape");
+  return ACP_OK;
+}
+
+int64_t scale_bytes(const acp::DescData& codes, int block) {
+  const int64_t c = codes.shape[codes.rank - 1];
+  return c ? elements(codes) / c * ((c + block - 1) / block) * 4 : 0;
+}
+
+// The outer dims [lo, rank - 1) of tensors of one shape as at most `most`
+// dims, outermost first: dims that all tensors hold without a gap become one.
+struct Collapsed {
+  int n = 0;
+  int64_t ext[acp::kMaxInputRank];
+  int64_t stride[8][acp::kMaxInputRank];  // bytes, by tensor
+};
+
+bool collapse(const acp::DescData* const* t, int nt, int lo, int most, Collapsed* out) {
+  const int r = t[0]->rank;
+  for (int d = lo; d + 1 < r; ++d) {
+    if (t[0]->shape[d] == 1) continue;
+    bool join = out->n > 0;
+    for (int k = 0; join && k < nt; ++k)
+      join = out->stride[k][out->n - 1] == t[k]->shape[d] * t[k]->strides[d] * t[k]->esize;
+    if (join) out->ext[out->n - 1] *= t[0]->shape[d];
+    else out->ext[out->n++] = t[0]->shape[d];
+    for (int k = 0; k < nt; ++k) out->stride[k][out->n - 1] = t[k]->strides[d] * t[k]->esize;
+  }
+  return out->n <= most;
+}
+
+int log2_of(int64_t v) { return log2i(static_cast<int>(v)); }
+
+constexpr int64_t kRowLimit = (int64_t(1) << 31) - 4096;  // rows and chunks the kernels index
+
+// Elementwise row operators: the geometry of `t` (all of one shape) in chunks
+// of v channels, scale blocks of `block` channels (0: none).  Rows that all
+// tensors hold without a gap, in whole scale blocks, become one long row.
+acp_status row_geometry(const acp::DescData* const* t, acp::RowTensor* const* rt, int nt, int v, int block,
+                        acp::RowsArgs* A) {
+  const int r = t[0]->rank;
+  Collapsed o;
+  if (!collapse(t, nt, 0, 3, &o))
+    return ret(ACP_ERR_UNSUPPORTED, "the outer dims of these strides do not join into three");
+  const int unit = block ? block : v;
+  int64_t c = t[0]->shape[r - 1], rows = 1;
+  for (int d = 0; d < o.n; ++d) rows *= o.ext[d];
+  bool flat = o.n == 1 && c % unit == 0;
+  for (int k = 0; flat && k < nt; ++k) flat = o.stride[k][0] == c * t[k]->esize;
+  if (flat) {
+    c *= rows;
+    rows = 1;
+    o.n = 0;
+  }
+  const int64_t cpr = (c + unit - 1) / unit * (unit / v);
+  if (rows >= kRowLimit || cpr >= kRowLimit || rows * cpr >= kRowLimit)
+    return ret(ACP_ERR_UNSUPPORTED, "more than 2^31 chunks of 16 bytes");
+  const int64_t n1 = o.n >= 2 ? o.ext[o.n - 2] : 1, n2 = o.n >= 1 ? o.ext[o.n - 1] : 1;
+  A->c = c;
+  A->total = static_cast<uint32_t>(rows * cpr);
+  A->cpr = div_by(static_cast<uint64_t>(cpr));
+  A->n1 = div_by(static_cast<uint64_t>(n1));
+  A->n2 = div_by(static_cast<uint64_t>(n2));
+  A->lb_log2 = log2_of(unit / v);
+  for (int k = 0; k < nt; ++k) {
+    rt[k]->p = reinterpret_cast<char*>(t[k]->gbase);
+    for (int d = 0; d < 3; ++d) rt[k]->s[d] = 0;
+    for (int d = 0; d < o.n; ++d) rt[k]->s[3 - o.n + d] = o.stride[k][d];
+  }
+  return ACP_OK;
+}
+
+// The kernels run on the current device: a stream of another one is refused.
+acp_status check_stream(void* stream) {
+  hipDevice_t dev = 0;
+  if (stream && hipStreamGetDevice(static_cast<hipStream_t>(stream), &dev) == hipSuccess && dev != current_device())
+    return ret(ACP_ERR_INVALID, "the stream is of another device than the current one");
+  return ACP_OK;
+}
+
+acp_status launched(hipError_t e, const std::string& what) {
+  if (e != hipSuccess) {
+    g_last_kernel = "none";
+    return ret(ACP_ERR_HIP, std::string("kernel launch failed: ") + hipGetErrorString(e));
+  }
+  g_last_kernel = what;
+  return ret(ACP_OK);
+}
+
+acp_status launched_nothing() {
+  g_last_kernel = "none";
+  return ret(ACP_OK);
+}
+
+bool known_act(int act) { return act == ACP_ACT_NONE || act == ACP_ACT_SILU || act == ACP_ACT_GELU; }
+
+acp_status pack8(const acp_packed8* out, const acp_tile_desc* x, void* stream) {
+  acp::DescData xd, cd;
+  acp_status st = load_float(x, "x", &xd);
+  if (st == ACP_OK) st = load_packed(out, xd, "the packed output", &cd);
+  if (st != ACP_OK) return st;
+  if (self_overlap(cd)) return ret(ACP_ERR_INVALID, "the codes overlap themselves");
+  const Range w[] = {range_of(cd, "the codes"), range_of(out->scales, scale_bytes(cd, out->block), "the scales")};
+  const Range r[] = {range_of(xd, "x")};
+  if ((st = check_ranges(w, 2, r, 1)) != ACP_OK) return st;
+  if (elements(xd) == 0) return launched_nothing();
+  if ((st = check_stream(stream)) != ACP_OK) return st;
+  acp::RowsArgs A{};
+  const acp::DescData* t[] = {&xd, &cd};
+  acp::RowTensor* rt[] = {&A.x, &A.px.codes};
+  const int v = 16 / xd.esize;
+  if ((st = row_geometry(t, rt, 2, v, out->block, &A)) != ACP_OK) return st;
+  A.px.scales = out->scales;
+  A.format = out->format;
+  return launched(acp::pack8_launch(row_dtype(xd.dtype), A, static_cast<hipStream_t>(stream)),
+                  "pack8 chunks " + std::to_string(A.total));
+}
+
+acp_status unpack8(const acp_tile_desc* out, const acp_packed8* in, void* stream) {
+  acp::DescData od, cd;
+  acp_status st = load_float(out, "the output", &od);
+  if (st == ACP_OK) st = load_packed(in, od, "the packed input", &cd);
+  if (st != ACP_OK) return st;
+  if (self_overlap(od)) return ret(ACP_ERR_INVALID, "the output overlaps itself");
+  const Range w[] = {range_of(od, "the output")};
+  const Range r[] = {range_of(cd, "the codes"), range_of(in->scales, scale_bytes(cd, in->block), "the scales")};
+  if ((st = check_ranges(w, 1, r, 2)) != ACP_OK) return st;
+  if (elements(od) == 0) return launched_nothing();
+  if ((st = check_stream(stream)) != ACP_OK) return st;
+  acp::RowsArgs A{};
+  const acp::DescData* t[] = {&od, &cd};
+  acp::RowTensor* rt[] = {&A.y, &A.px.codes};
+  const int v = 16 / od.esize;
+  if ((st = row_geometry(t, rt, 2, v, in->block, &A)) != ACP_OK) return st;
+  A.px.scales = in->scales;
+  A.format = in->format;
+  return launched(acp::unpack8_launch(row_dtype(od.dtype), A, static_cast<hipStream_t>(stream)),
+                  "unpack8 chunks " + std::to_string(A.total));
+}
+
+acp_status act_forward(acp_activation act, const acp_tile_desc* out, const acp_tile_desc* x, const acp_tile_desc* z,
+                       const acp_packed8* save_x, const acp_packed8* save_z, void* stream) {
+  acp::DescData od, xd, zd, cxd, czd;
+  if (!known_act(act)) return ret(ACP_ERR_INVALID, "unknown activation");
+  acp_status st = load_float(out, "the output", &od);
+  if (st == ACP_OK) st = load_float(x, "x", &xd);
+  if (st == ACP_OK && z) st = load_float(z, "z", &zd);
+  if (st != ACP_OK) return st;
+  const bool gated = z != nullptr, save = save_x != nullptr;
+  if (save_z && !gated) return ret(ACP_ERR_INVALID, "a saved z without z");
+  if (gated && (save_x != nullptr) != (save_z != nullptr))
+    return ret(ACP_ERR_INVALID, "x and z are saved together or not at all");
+  if (!same_shape(od, xd) || od.dtype != xd.dtype || (gated && (!same_shape(zd, xd) || zd.dtype != xd.dtype)))
+    return ret(ACP_ERR_INVALID, "the operands differ in shape or dtype");
+  if (save && (st = load_packed(save_x, xd, "the saved x", &cxd)) != ACP_OK) return st;
+  if (save && gated) {
+    if ((st = load_packed(save_z, xd, "the saved z", &czd)) != ACP_OK) return st;
+    if (save_z->format != save_x->format || save_z->block != save_x->block)
+      return ret(ACP_ERR_INVALID, "x and z are saved in one format and block");
+  }
+  if (self_overlap(od) || (save && self_overlap(cxd)) || (save && gated && self_overlap(czd)))
+    return ret(ACP_ERR_INVALID, "an output overlaps itself");
+  Range w[5], r[2];
+  int nw = 0, nr = 0;
+  w[nw++] = range_of(od, "the output");
+  r[nr++] = range_of(xd, "x");
+  if (gated) r[nr++] = range_of(zd, "z");
+  acp::RowsArgs A{};
+  const acp::DescData* t[5] = {&xd, &od};
+  acp::RowTensor* rt[5] = {&A.x, &A.y};
+  int nt = 2;
+  if (gated) {
+    t[nt] = &zd;
+    rt[nt++] = &A.z;
+  }
+  if (save) {
+    w[nw++] = range_of(cxd, "the codes of x");
+    w[nw++] = range_of(save_x->scales, scale_bytes(cxd, save_x->block), "the scales of x");
+    t[nt] = &cxd;
+    rt[nt++] = &A.px.codes;
+    A.px.scales = save_x->scales;
+    A.format = save_x->format;
+    if (gated) {
+      w[nw++] = range_of(czd, "the codes of z");
+      w[nw++] = range_of(save_z->scales, scale_bytes(czd, save_z->block), "the scales of z");
+      t[nt] = &czd;
+      rt[nt++] = &A.pz.codes;
+      A.pz.scales = save_z->scales;
+    }
+  }
+  if ((st = check_ranges(w, nw, r, nr)) != ACP_OK) return st;
+  if (elements(xd) == 0) return launched_nothing();
+  if ((st = check_stream(stream)) != ACP_OK) return st;
+  if ((st = row_geometry(t, rt, nt, 16 / xd.esize, save ? save_x->block : 0, &A)) != ACP_OK) return st;
+  A.act = act;
+  return launched(acp::act_forward_launch(row_dtype(xd.dtype), gated, save, A, static_cast<hipStream_t>(stream)),
+                  std::string("activation") + (gated ? " gated" : "") + (save ? " saved" : "") + " chunks " +
+                      std::to_string(A.total));
+}
+
+acp_status act_backward(acp_activation act, const acp_tile_desc* dx, const acp_tile_desc* dz, const acp_tile_desc* dy,
+                        const acp_packed8* x, const acp_packed8* z, void* stream) {
+  acp::DescData dxd, dzd, dyd, cxd, czd;
+  if (!known_act(act)) return ret(ACP_ERR_INVALID, "unknown activation");
+  const bool gated = z != nullptr;
+  if (gated != (dz != nullptr)) return ret(ACP_ERR_INVALID, "z and dz are given together or not at all");
+  acp_status st = load_float(dy, "dy", &dyd);
+  if (st == ACP_OK) st = load_float(dx, "dx", &dxd);
+  if (st == ACP_OK && gated) st = load_float(dz, "dz", &dzd);
+  if (st == ACP_OK) st = load_packed(x, dyd, "the saved x", &cxd);
+  if (st == ACP_OK && gated) st = load_packed(z, dyd, "the saved z", &czd);
+  if (st != ACP_OK) return st;
+  if (!same_shape(dxd, dyd) || dxd.dtype != dyd.dtype || (gated && (!same_shape(dzd, dyd) || dzd.dtype != dyd.dtype)))
+    return ret(ACP_ERR_INVALID, "the gradients differ in shape or dtype");
+  if (gated && (z->format != x->format || z->block != x->block))
+    return ret(ACP_ERR_INVALID, "x and z are saved in one format and block");
+  if (self_overlap(dxd) || (gated && self_overlap(dzd))) return ret(ACP_ERR_INVALID, "an output overlaps itself");
+  Range w[2], r[5];
+  int nw = 0, nr = 0;
+  acp::RowsArgs A{};
+  const acp::DescData* t[5] = {&dyd, &dxd, &cxd};
+  acp::RowTensor* rt[5] = {&A.dy, &A.dx, &A.px.codes};
+  int nt = 3;
+  w[nw++] = range_of(dxd, "dx");
+  r[nr++] = range_of(dyd, "dy");
+  r[nr++] = range_of(cxd, "the codes of x");
+  r[nr++] = range_of(x->scales, scale_bytes(cxd, x->block), "the scales of x");
+  if (gated) {
+    w[nw++] = range_of(dzd, "dz");
+    r[nr++] = range_of(czd, "the codes of z");
+    r[nr++] = range_of(z->scales, scale_bytes(czd, z->block), "the scales of z");
+    t[nt] = &dzd;
+    rt[nt++] = &A.dz;
+    t[nt] = &czd;
+    rt[nt++] = &A.pz.codes;
+    A.pz.scales = z->scales;
+  }
+  if ((st = check_ranges(w, nw, r, nr)) != ACP_OK) return st;
+  if (elements(dyd) == 0) return launched_nothing();
+  if ((st = check_stream(stream)) != ACP_OK) return st;
+  if ((st = row_geometry(t, rt, nt, 16 / dyd.esize, x->block, &A)) != ACP_OK) return st;
+  A.px.scales = x->scales;
+  A.format = x->format;
+  A.act = act;
+  return launched(acp::act_backward_launch(row_dtype(dyd.dtype), gated, A, static_cast<hipStream_t>(stream)),
+                  std::string("activation backward") + (gated ? " gated" : "") + " chunks " + std::to_string(A.total));
+}
+
+// ---------------------------------------------------------------- group norm
+
+// Workgroups that a pass over the data is split into.  By parts: enough to
+// fill 256 CUs several times over; each joins its sample's parts first, so no
+// more than 512 runs a sample.  Per row with sums of columns to leave behind:
+// two a CU, since each leaves 8 bytes for every channel.
+constexpr int64_t kNormGroups = 2048;
+constexpr int64_t kNormGroupsColumns = 512;
+constexpr int64_t kNormRuns = 512;
+
+// Sizes, split and workspace of a group norm of `t`; tensors and pointers
+// are filled in by the caller.
+struct NormPlan {
+  acp::NormArgs A{};
+  int dt = 0, v = 0;
+  bool per_row = false;
+  int64_t forward_bytes = 0, backward_bytes = 0;  // workspace
+  int64_t coef_at = 0;                            // of the backward pass
+};
+
+acp_status norm_plan(const acp::DescData& t, int groups, int block, bool backward, NormPlan* P) {
+  const int r = t.rank;
+  if (r < 2) return ret(ACP_ERR_INVALID, "group norm needs a sample dim and a channel dim");
+  const int64_t samples = t.shape[0], c = t.shape[r - 1];
+  int64_t rows = 1;
+  for (int d = 1; d + 1 < r; ++d) rows *= t.shape[d];
+  if (c < 1 || rows < 1) return ret(ACP_ERR_INVALID, "group norm needs at least one row and one channel");
+  if (groups < 1 || c % groups) return ret(ACP_ERR_INVALID, "the groups must divide the channels");
+  if (samples >= kRowLimit || rows >= kRowLimit || c >= kRowLimit / 2)
+    return ret(ACP_ERR_UNSUPPORTED, "group norm extents go up to 2^31");
+  acp::NormArgs& A = P->A;
+  P->dt = row_dtype(t.dtype);
+  P->v = 16 / t.esize;
+  const int64_t v = P->v, per = c / groups;
+  const int64_t gl = per / v;  // lanes of a group
+  P->per_row = rows == 1 && per % v == 0 && gl <= 64 && (gl & (gl - 1)) == 0;
+  // lanes: the row's chunks in equal channel blocks, in whole scale blocks
+  // and (per row) whole groups
+  const int64_t unit = std::max<int64_t>(block ? block / v : 1, P->per_row ? gl : 1);
+  const int64_t cpr = (c + v - 1) / v;
+  int64_t blocks = (cpr + acp::kRowThreads - 1) / acp::kRowThreads;
+  int64_t lanes = ((cpr + blocks - 1) / blocks + unit - 1) / unit * unit;
+  blocks = (cpr + lanes - 1) / lanes;
+  const int64_t row_lanes = acp::kRowThreads / lanes;
+  const int64_t n = P->per_row ? 1 : samples;
+  if (P->per_row) rows = samples;
+  const int64_t target = P->per_row && backward ? kNormGroupsColumns : kNormGroups;
+  const int64_t want = std::min(P->per_row ? target : kNormRuns, std::max<int64_t>(1, target / std::max<int64_t>(1, n * blocks)));
+  int64_t rpc = std::max<int64_t>((rows + want - 1) / want, row_lanes * (P->per_row ? 1 : acp::kRowUnroll));
+  rpc = (rpc + row_lanes - 1) / row_lanes * row_lanes;
+  const int64_t chunks = rows ? (rows + rpc - 1) / rpc : 1;
+  if (n * blocks * chunks + 2 * c / 32 + 1 >= kRowLimit || n * groups >= kRowLimit * 128)
+    return ret(ACP_ERR_UNSUPPORTED, "more than 2^31 workgroups");
+  A.samples = static_cast<uint32_t>(n);
+  A.rows = static_cast<uint32_t>(rows);
+  A.c = static_cast<uint32_t>(c);
+  A.groups = static_cast<uint32_t>(groups);
+  A.per_group = static_cast<uint32_t>(per);
+  A.lanes = div_by(static_cast<uint64_t>(lanes));
+  A.row_lanes = static_cast<uint32_t>(row_lanes);
+  A.blocks = static_cast<uint32_t>(blocks);
+  A.chunks = static_cast<uint32_t>(chunks);
+  A.rpc = static_cast<uint32_t>(rpc);
+  const int64_t width = lanes * v;
+  A.pieces = static_cast<uint32_t>(std::min(blocks, (per + width - 2) / width + 1));
+  A.lb_log2 = block ? log2_of(block / v) : 0;
+  A.group_lanes_log2 = P->per_row ? log2_of(gl) : 0;
+  A.col_rows = static_cast<uint32_t>(P->per_row ? (rows ? chunks : 0) : n);
+  P->forward_bytes = P->per_row ? 0 : n * groups * chunks * A.pieces * 8;
+  P->coef_at = align_up(n * chunks * 2 * c * 4, 16);
+  P->backward_bytes = P->coef_at + (P->per_row ? 0 : n * groups * 8);
+  return ACP_OK;
+}
+
+// Rows of the tensors: s[0] per sample, (s[1], s[2]) per row of a sample.
+acp_status norm_rows(const acp::DescData* const* t, acp::RowTensor* const* rt, int nt, NormPlan* P) {
+  Collapsed o;
+  if (P->per_row) {
+    P->A.row2 = div_by(1);
+    for (int k = 0; k < nt; ++k) {
+      rt[k]->p = reinterpret_cast<char*>(t[k]->gbase);
+      rt[k]->s[0] = rt[k]->s[2] = 0;
+      rt[k]->s[1] = t[k]->strides[0] * t[k]->esize;
+    }
+    return ACP_OK;
+  }
+  if (!collapse(t, nt, 1, 2, &o))
+    return ret(ACP_ERR_UNSUPPORTED, "the inner row dims of these strides do not join into two");
+  P->A.row2 = div_by(static_cast<uint64_t>(o.n >= 1 ? o.ext[o.n - 1] : 1));
+  for (int k = 0; k < nt; ++k) {
+    rt[k]->p = reinterpret_cast<char*>(t[k]->gbase);
+    rt[k]->s[0] = t[k]->strides[0] * t[k]->esize;
+    rt[k]->s[1] = o.n >= 2 ? o.stride[k][0] : 0;
+    rt[k]->s[2] = o.n >= 1 ? o.stride[k][o.n - 1] : 0;
+  }
+  return ACP_OK;
+}
+
+bool misaligned4(const void* p) { return reinterpret_cast<uint64_t>(p) % 4 != 0; }
+
+acp_status check_workspace(const void* workspace, int64_t bytes, int64_t need) {
+  if (need == 0) return ACP_OK;
+  if (!workspace || bytes < need)
+    return ret(ACP_ERR_INVALID, "the workspace is smaller than acp_group_norm_workspace says");
+  if (reinterpret_cast<uint64_t>(workspace) % 16) return ret(ACP_ERR_INVALID, "the workspace is not 16-byte aligned");
+  return ACP_OK;
+}
+
+std::string norm_text(const char* what, const NormPlan& P) {
+  return std::string(what) + (P.per_row ? " per row" : " by parts") + " lanes " + std::to_string(P.A.lanes.d) + "x" +
+         std::to_string(P.A.row_lanes) + " blocks " + std::to_string(P.A.blocks) + " runs " +
+         std::to_string(P.A.chunks);
+}
+
+acp_status group_norm_workspace(const acp_tile_desc* x, int groups, int64_t* bytes) {
+  acp::DescData xd;
+  if (!bytes) return ret(ACP_ERR_INVALID, "null argument");
+  const acp_status st = load_float(x, "x", &xd);
+  if (st != ACP_OK) return st;
+  int64_t need = 0;
+  for (int block : {0, 32, 64, 128, 256})
+    for (int backward = 0; backward < 2; ++backward) {
+      NormPlan P;
+      const acp_status sp = norm_plan(xd, groups, block, backward != 0, &P);
+      if (sp != ACP_OK) return sp;
+      need = std::max(need, backward ? P.backward_bytes : P.forward_bytes);
+    }
+  *bytes = need;
+  return ret(ACP_OK);
+}
+
+acp_status group_norm(const acp_tile_desc* y, const acp_tile_desc* x, const float* gamma, const float* beta,
+                      int groups, float eps, acp_activation act, float* mean, float* rstd, const acp_packed8* save,
+                      void* workspace, int64_t workspace_bytes, void* stream) {
+  acp::DescData xd, yd, cd;
+  acp_status st = load_float(x, "x", &xd);
+  if (st == ACP_OK) st = load_float(y, "y", &yd);
+  if (st != ACP_OK) return st;
+  if (!known_act(act)) return ret(ACP_ERR_INVALID, "unknown activation");
+  if (!(eps >= 0.0f) || std::isinf(eps)) return ret(ACP_ERR_INVALID, "eps must be a finite number >= 0");
+  if (!same_shape(xd, yd) || xd.dtype != yd.dtype) return ret(ACP_ERR_INVALID, "x and y differ in shape or dtype");
+  if (save && (st = load_packed(save, xd, "the saved x", &cd)) != ACP_OK) return st;
+  if (misaligned4(gamma) || misaligned4(beta) || misaligned4(mean) || misaligned4(rstd))
+    return ret(ACP_ERR_INVALID, "a float32 array is not 4-byte aligned");
+  NormPlan P;
+  if ((st = norm_plan(xd, groups, save ? save->block : 0, false, &P)) != ACP_OK) return st;
+  if ((st = check_workspace(workspace, workspace_bytes, P.forward_bytes)) != ACP_OK) return st;
+  if (self_overlap(yd) || (save && self_overlap(cd))) return ret(ACP_ERR_INVALID, "an output overlaps itself");
+  const int64_t c = xd.shape[xd.rank - 1], stat = xd.shape[0] * groups * 4;
+  Range w[6] = {range_of(yd, "y"), range_of(mean, stat, "mean"), range_of(rstd, stat, "rstd"),
+                range_of(workspace, P.forward_bytes, "the workspace")};
+  int nw = 4;
+  if (save) {
+    w[nw++] = range_of(cd, "the codes");
+    w[nw++] = range_of(save->scales, scale_bytes(cd, save->block), "the scales");
+  }
+  const Range r[] = {range_of(xd, "x"), range_of(gamma, c * 4, "gamma"), range_of(beta, c * 4, "beta")};
+  if ((st = check_ranges(w, nw, r, 3)) != ACP_OK) return st;
+  if (elements(xd) == 0) return launched_nothing();
+  if ((st = check_stream(stream)) != ACP_OK) return st;
+  acp::NormArgs& A = P.A;
+  const acp::DescData* t[] = {&xd, &yd, &cd};
+  acp::RowTensor* rt[] = {&A.x, &A.y, &A.px.codes};
+  if ((st = norm_rows(t, rt, save ? 3 : 2, &P)) != ACP_OK) return st;
+  A.px.scales = save ? save->scales : nullptr;
+  A.format = save ? save->format : 0;
+  A.gamma = gamma;
+  A.beta = beta;
+  A.mean = mean;
+  A.rstd = rstd;
+  A.part = static_cast<float*>(workspace);
+  A.act = act;
+  A.eps = eps;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = hipSuccess;
+  if (!P.per_row) e = acp::norm_stats_launch(P.dt, A, s);
+  if (e == hipSuccess) e = acp::norm_apply_launch(P.dt, P.per_row, save != nullptr, A, s);
+  return launched(e, norm_text(save ? "group norm saved" : "group norm", P));
+}
+
+acp_status group_norm_backward(const acp_tile_desc* dx, float* dgamma, float* dbeta, const acp_tile_desc* dy,
+                               const acp_tile_desc* x, const acp_packed8* saved, const float* mean, const float* rstd,
+                               const float* gamma, const float* beta, int groups, acp_activation act, void* workspace,
+                               int64_t workspace_bytes, void* stream) {
+  acp::DescData dxd, dyd, xd, cd;
+  if ((x != nullptr) == (saved != nullptr)) return ret(ACP_ERR_INVALID, "give x or its saved form, and not both");
+  acp_status st = load_float(dy, "dy", &dyd);
+  if (st == ACP_OK) st = load_float(dx, "dx", &dxd);
+  if (st == ACP_OK && x) st = load_float(x, "x", &xd);
+  if (st == ACP_OK && saved) st = load_packed(saved, dyd, "the saved x", &cd);
+  if (st != ACP_OK) return st;
+  if (!known_act(act)) return ret(ACP_ERR_INVALID, "unknown activation");
+  if (!mean || !rstd) return ret(ACP_ERR_INVALID, "the backward pass needs mean and rstd");
+  if (!same_shape(dxd, dyd) || dxd.dtype != dyd.dtype || (x && (!same_shape(xd, dyd) || xd.dtype != dyd.dtype)))
+    return ret(ACP_ERR_INVALID, "x, dy and dx differ in shape or dtype");
+  if (misaligned4(gamma) || misaligned4(beta) || misaligned4(mean) || misaligned4(rstd) || misaligned4(dgamma) ||
+      misaligned4(dbeta))
+    return ret(ACP_ERR_INVALID, "a float32 array is not 4-byte aligned");
+  NormPlan P;
+  if ((st = norm_plan(dyd, groups, saved ? saved->block : 0, true, &P)) != ACP_OK) return st;
+  if ((st = check_workspace(workspace, workspace_bytes, P.backward_bytes)) != ACP_OK) return st;
+  if (self_overlap(dxd)) return ret(ACP_ERR_INVALID, "an output overlaps itself");
+  const int64_t c = dyd.shape[dyd.rank - 1], stat = dyd.shape[0] * groups * 4;
+  const Range w[] = {range_of(dxd, "dx"), range_of(dgamma, c * 4, "dgamma"), range_of(dbeta, c * 4, "dbeta"),
+                     range_of(workspace, P.backward_bytes, "the workspace")};
+  Range r[7] = {range_of(dyd, "dy"), range_of(mean, stat, "mean"), range_of(rstd, stat, "rstd"),
+                range_of(gamma, c * 4, "gamma"), range_of(beta, c * 4, "beta")};
+  int nr = 5;
+  if (x) r[nr++] = range_of(xd, "x");
+  if (saved) {
+    r[nr++] = range_of(cd, "the codes");
+    r[nr++] = range_of(saved->scales, scale_bytes(cd, saved->block), "the scales");
+  }
+  if ((st = check_ranges(w, 4, r, nr)) != ACP_OK) return st;
+  acp::NormArgs& A = P.A;
+  const acp::DescData* t[] = {&dyd, &dxd, x ? &xd : &cd};
+  acp::RowTensor* rt[] = {&A.dy, &A.dx, x ? &A.x : &A.px.codes};
+  if ((st = norm_rows(t, rt, 3, &P)) != ACP_OK) return st;
+  A.px.scales = saved ? saved->scales : nullptr;
+  A.format = saved ? saved->format : 0;
+  A.gamma = gamma;
+  A.beta = beta;
+  A.mean = const_cast<float*>(mean);
+  A.rstd = const_cast<float*>(rstd);
+  A.dgamma = dgamma;
+  A.dbeta = dbeta;
+  A.part = static_cast<float*>(workspace);
+  A.coef = reinterpret_cast<float*>(static_cast<char*>(workspace) + P.coef_at);
+  A.act = act;
+  if ((st = check_stream(stream)) != ACP_OK) return st;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = hipSuccess;
+  if (elements(dyd) == 0) {  // no samples: the gradients of the parameters are zero
+    A.col_rows = 0;
+    if (!dgamma && !dbeta) return launched_nothing();
+    return launched(acp::norm_columns_launch(A, s), "group norm backward of no samples");
+  }
+  if (P.per_row) {
+    e = acp::norm_dx_launch(P.dt, true, saved != nullptr, A, s);
+    if (e == hipSuccess) e = acp::norm_columns_launch(A, s);
+  } else {
+    e = acp::norm_sums_launch(P.dt, saved != nullptr, A, s);
+    if (e == hipSuccess) e = acp::norm_coef_launch(A, s);
+    if (e == hipSuccess) e = acp::norm_dx_launch(P.dt, false, saved != nullptr, A, s);
+  }
+  return launched(e, norm_text(saved ? "group norm backward from 8 bits" : "group norm backward", P));
+}
+
+// Nothing throws across the ABI.
+template <class F>
+acp_status guarded(F&& f) {
+  try {
+    return f();
+  } catch (...) {
+    return ACP_ERR_INVALID;
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+acp_status acp_pack8(const acp_packed8* out, const acp_tile_desc* x, void* hip_stream) {
+  return guarded([&] { return pack8(out, x, hip_stream); });
+}
+
+acp_status acp_unpack8(const acp_tile_desc* out, const acp_packed8* in, void* hip_stream) {
+  return guarded([&] { return unpack8(out, in, hip_stream); });
+}
+
+acp_status acp_act_forward(acp_activation act, const acp_tile_desc* out, const acp_tile_desc* x,
+                           const acp_tile_desc* z, const acp_packed8* save_x, const acp_packed8* save_z,
+                           void* hip_stream) {
+  return guarded([&] { return act_forward(act, out, x, z, save_x, save_z, hip_stream); });
+}
+
+acp_status acp_act_backward(acp_activation act, const acp_tile_desc* dx, const acp_tile_desc* dz,
+                            const acp_tile_desc* dy, const acp_packed8* x, const acp_packed8* z, void* hip_stream) {
+  return guarded([&] { return act_backward(act, dx, dz, dy, x, z, hip_stream); });
+}
+
+acp_status acp_group_norm_workspace(const acp_tile_desc* x, int groups, int64_t* bytes) {
+  return guarded([&] { return group_norm_workspace(x, groups, bytes); });
+}
+
+acp_status acp_group_norm(const acp_tile_desc* y, const acp_tile_desc* x, const float* gamma, const float* beta,
+                          int groups, float eps, acp_activation act, float* mean, float* rstd,
+                          const acp_packed8* save, void* workspace, int64_t workspace_bytes, void* hip_stream) {
+  return guarded([&] {
+    return group_norm(y, x, gamma, beta, groups, eps, act, mean, rstd, save, workspace, workspace_bytes, hip_stream);
+  });
+}
+
+acp_status acp_group_norm_backward(const acp_tile_desc* dx, float* dgamma, float* dbeta, const acp_tile_desc* dy,
+                                   const acp_tile_desc* x, const acp_packed8* saved, const float* mean,
+                                   const float* rstd, const float* gamma, const float* beta, int groups,
+                                   acp_activation act, void* workspace, int64_t workspace_bytes, void* hip_stream) {
+  return guarded([&] {
+    return group_norm_backward(dx, dgamma, dbeta, dy, x, saved, mean, rstd, gamma, beta, groups, act, workspace,
+                               workspace_bytes, hip_stream);
+  });
+}
+
+}  // extern "C"

@@ -10,6 +10,12 @@
  *   acp_stream_binary       two tensors streamed through one ring (add, mul)
  *   acp_stream_reduce_rows  row sums of ring-staged tiles
  *
+ * and over the rows of a tensor:
+ *
+ *   acp_pack8, acp_unpack8                    8-bit checkpoints of a tensor
+ *   acp_act_forward, acp_act_backward         (gated) activations that keep their operands in 8 bits
+ *   acp_group_norm, acp_group_norm_backward   group norm with an activation, channels last
+ *
  * plus the host-side descriptor encoder / planner they share.  The method
  * follows four pages:
  *   [tma]    "copy_async -> tma"            (TVM TIRx docs)
@@ -78,7 +84,17 @@ typedef enum {
   ACP_ERR_HIP = 5
 } acp_status;
 
-typedef enum { ACP_U8 = 0, ACP_U16 = 1, ACP_U32 = 2, ACP_U64 = 3, ACP_F16 = 4, ACP_F32 = 5 } acp_dtype;
+/* ACP_BF16 tensors are copied (acp_tile_copy) and taken by the row
+ * operators; the tile and stream operators do not compute with them. */
+typedef enum {
+  ACP_U8 = 0,
+  ACP_U16 = 1,
+  ACP_U32 = 2,
+  ACP_U64 = 3,
+  ACP_F16 = 4,
+  ACP_F32 = 5,
+  ACP_BF16 = 6
+} acp_dtype;
 
 /* LDS layout of a staged tile.  ACP_SWIZZLE_128B carries the mode number of
  * [tma]'s worked example (3): 16-byte chunk index XOR (128-byte row index
@@ -308,6 +324,108 @@ typedef enum { ACP_STAGE_RING = 0, ACP_STAGE_SET = 1 } acp_staging;
 acp_status acp_stream_binary(acp_op op, const acp_tile_desc* out, const acp_tile_desc* x, const acp_tile_desc* z,
                              const int32_t* stage_box, int stages, int threads, int workgroups,
                              acp_staging z_staging, void* hip_stream);
+
+/* ------------------------------------------------------------------------
+ * Row operators.  Their tensors are descriptors like every other: base,
+ * dtype (f16, bf16 or f32; every float tensor of a call the same one),
+ * shape and strides.  They choose their own split of the work: the box and
+ * the swizzle of a descriptor are not used, and a base needs only its
+ * element's alignment.  The innermost dim is the row; the outer dims have to
+ * join into at most three (group norm: the dims between the first and the
+ * last into at most two), else ACP_ERR_UNSUPPORTED.  Sums and statistics are
+ * held in float32 and added in a fixed order: the same call gives the same
+ * bits.  A written tensor must not overlap itself or share memory with
+ * another operand (ACP_ERR_INVALID); memory between the rows of an output is
+ * left as it was.  Zero elements are a call that does nothing.  A call
+ * enqueues one to three kernels and, like the others, allocates nothing and
+ * can be captured into a HIP graph; all its memory is of the current device,
+ * which is the stream's. */
+
+/* A tensor in 8 bits: one code a value, and one float32 scale for every
+ * `block` neighbouring values of a row (the last block of a row may be
+ * short).  A value is its code times its block's scale.
+ *   ACP_PACK_I8    code round(x / scale), ties to even, in -127..127;
+ *                  scale = max(fl(amax / 127), 2^-126), amax the block's
+ *                  largest |x| (at most the largest float32 whose 127-fold
+ *                  is finite).  Off by at most scale / 2
+ *   ACP_PACK_E4M3  code x / scale rounded to the OCP E4M3 format (4 exponent
+ *                  and 3 mantissa bits, largest value 448), ties to even;
+ *                  scale the smallest power of two >= 2^-126 with
+ *                  amax <= 448 * scale.  Off by at most 2^-4 of |x|, or
+ *                  2^-10 of the scale where that is more.  What would round
+ *                  past the largest value of x's own type takes the value
+ *                  below instead (61440 for f16, 1.875 * 2^127 else)
+ * A block that holds a NaN or an infinity has a NaN scale: all of it unpacks
+ * to NaN, and its codes are unspecified. */
+typedef enum { ACP_PACK_I8 = 0, ACP_PACK_E4M3 = 1 } acp_pack_format;
+
+typedef struct {
+  const acp_tile_desc* codes; /* ACP_U8, the tensor's shape, strides of its own */
+  float* scales;              /* device, packed row-major [shape[:-1], ceil(shape[-1] / block)] */
+  int32_t format;             /* acp_pack_format */
+  int32_t block;              /* 32, 64, 128 or 256 */
+} acp_packed8;
+
+/* out = x in 8 bits (codes and scales are written). */
+acp_status acp_pack8(const acp_packed8* out, const acp_tile_desc* x, void* hip_stream);
+
+/* out = the values that `in` stands for: code * scale in float32, rounded to
+ * the output's type. */
+acp_status acp_unpack8(const acp_tile_desc* out, const acp_packed8* in, void* hip_stream);
+
+/* Activations: SILU u / (1 + e^-u), GELU u (1 + erf(u / sqrt 2)) / 2. */
+typedef enum { ACP_ACT_NONE = 0, ACP_ACT_SILU = 1, ACP_ACT_GELU = 2 } acp_activation;
+
+/* out = act(x), or act(x) * z where z is not NULL, computed in float32 and
+ * rounded once.  save_x, and with z save_z, keep the operands in 8 bits for
+ * the backward pass (both or neither; one format and block), from the same
+ * read of them.  NULL: not kept. */
+acp_status acp_act_forward(acp_activation act, const acp_tile_desc* out, const acp_tile_desc* x,
+                           const acp_tile_desc* z, const acp_packed8* save_x, const acp_packed8* save_z,
+                           void* hip_stream);
+
+/* dx = dy * act'(x) [* z] and dz = dy * act(x), with x and z the values of
+ * their 8-bit forms.  z and dz NULL: no gate. */
+acp_status acp_act_backward(acp_activation act, const acp_tile_desc* dx, const acp_tile_desc* dz,
+                            const acp_tile_desc* dy, const acp_packed8* x, const acp_packed8* z, void* hip_stream);
+
+/* Bytes of workspace that acp_group_norm and acp_group_norm_backward need at
+ * most for tensors of x's shape and dtype, saved in 8 bits or not (may be 0).
+ * The caller owns the workspace (device memory, 16-byte aligned, any
+ * contents); it holds nothing between calls, and calls that may run at the
+ * same time (other streams, graphs replayed together) need one each. */
+acp_status acp_group_norm_workspace(const acp_tile_desc* x, int groups, int64_t* bytes);
+
+/* Group norm with an activation, channels last: x [samples, ..., channels],
+ * rank >= 2; the dims between are a sample's rows (none: one row).  Each
+ * sample's channels form `groups` runs of channels / groups neighbours, each
+ * normalised over its channels and all the sample's rows:
+ *   y = act((x - mean) * rstd * gamma + beta),  rstd = 1 / sqrt(var + eps)
+ * with the biased variance.
+ *   gamma, beta  device float32 [channels]; NULL: 1 and 0
+ *   eps          finite, >= 0
+ *   mean, rstd   device float32 [samples, groups], written; NULL: not wanted.
+ *                The backward pass takes both
+ *   save         x in 8 bits, written in the pass that normalises; NULL: not
+ *                kept
+ * A group with a NaN or an infinity, or whose squared deviations overflow
+ * float32, gives NaN throughout. */
+acp_status acp_group_norm(const acp_tile_desc* y, const acp_tile_desc* x, const float* gamma, const float* beta,
+                          int groups, float eps, acp_activation act, float* mean, float* rstd,
+                          const acp_packed8* save, void* workspace, int64_t workspace_bytes, void* hip_stream);
+
+/* Its backward pass, from x or (x NULL) from `saved`, its 8-bit form, with
+ * the mean and rstd of the forward pass:
+ *   z = (x - mean) * rstd,  a = dy * act'(z * gamma + beta)
+ *   dbeta = sum a,  dgamma = sum a * z  over samples and rows
+ *   dx = rstd * (gamma a - M(gamma a) - z M(gamma a z)),  M the mean over a
+ *        sample's group
+ * dgamma and dbeta (device float32 [channels]) are written, not added to;
+ * NULL: not wanted. */
+acp_status acp_group_norm_backward(const acp_tile_desc* dx, float* dgamma, float* dbeta, const acp_tile_desc* dy,
+                                   const acp_tile_desc* x, const acp_packed8* saved, const float* mean,
+                                   const float* rstd, const float* gamma, const float* beta, int groups,
+                                   acp_activation act, void* workspace, int64_t workspace_bytes, void* hip_stream);
 
 /* Test export: the raw LDS bytes of tile `tile_index` of `src` after its
  * direct-to-LDS load, written to `out_bytes` (device, tile_bytes long). */

@@ -24,6 +24,8 @@ Modules
 ``ring``      the circular-buffer event schedule with per-wait counters.
 ``reference`` the plain definitions every result must equal (copy,
               elementwise, streamed fma, store with reduce-add, row sums).
+``rows``      the row operators in binary64: 8-bit checkpoints, activations,
+              group norm with an activation and its backward pass.
 
 Only ``tests/``, ``__graft_entry__.smoke()`` and the ``cpu_baseline`` leg of
 ``bench.py`` may import this package.  It shares no code with the HIP path
