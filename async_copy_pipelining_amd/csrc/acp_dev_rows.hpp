@@ -29,6 +29,49 @@ __device__ __forceinline__ uint32_t divide(uint32_t n, const Div& d) {
 __device__ __forceinline__ float as_float(uint32_t u) { return __builtin_bit_cast(float, u); }
 __device__ __forceinline__ uint32_t as_bits(float f) { return __builtin_bit_cast(uint32_t, f); }
 
+// ---------------------------------------------------------------- across lanes
+
+// f(v, w) with w from the other half of each 2^(STEP + 1) neighbouring lanes,
+// where the lanes of a half hold one value already (steps are taken in
+// order).  Within a row of 16 lanes these are DPP moves of the vector ALU
+// (neighbour, pair, mirrored 8, mirrored 16), past it the row swaps; none
+// waits for LDS as a general permute does.
+template <int STEP, class F>
+__device__ __forceinline__ int lane_step(int v, F f) {
+  if constexpr (STEP == 0) return f(v, __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true));
+  if constexpr (STEP == 1) return f(v, __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true));
+  if constexpr (STEP == 2) return f(v, __builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true));
+  if constexpr (STEP == 3) return f(v, __builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, true));
+  if constexpr (STEP == 4) {
+    const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return f(static_cast<int>(p[0]), static_cast<int>(p[1]));
+  }
+  if constexpr (STEP == 5) {
+    const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return f(static_cast<int>(p[0]), static_cast<int>(p[1]));
+  }
+  return v;
+}
+
+// f over the 2^n lanes that share a value to be made, n uniform; the lanes
+// are aligned to 2^n and all of them get the result.
+template <class F>
+__device__ __forceinline__ int over_lanes(int v, int n, F f) {
+  if (n > 0) v = lane_step<0>(v, f);
+  if (n > 1) v = lane_step<1>(v, f);
+  if (n > 2) v = lane_step<2>(v, f);
+  if (n > 3) v = lane_step<3>(v, f);
+  if (n > 4) v = lane_step<4>(v, f);
+  if (n > 5) v = lane_step<5>(v, f);
+  return v;
+}
+
+__device__ __forceinline__ float sum_lanes(float v, int n) {
+  return as_float(static_cast<uint32_t>(over_lanes(static_cast<int>(as_bits(v)), n, [](int a, int b) {
+    return static_cast<int>(as_bits(as_float(static_cast<uint32_t>(a)) + as_float(static_cast<uint32_t>(b))));
+  })));
+}
+
 // ---------------------------------------------------------------- 16-byte chunks
 
 template <class T>
@@ -85,11 +128,16 @@ __device__ __forceinline__ rw4 narrow(const float (&f)[4], const float*) {
 }
 
 // `n` channels at p (all of a chunk, or fewer at a row's end; none for n <= 0);
-// channels past n read as zero.
-template <class T>
+// channels past n read as zero.  KEEP: another kernel reads them again soon
+// (the cached policy; else non-temporal).  Without TAIL n is all or none.
+template <class T, bool KEEP = false, bool TAIL = true>
 __device__ __forceinline__ rw4 load_chunk(const char* p, int n) {
   constexpr int V = kChunk<T>;
-  if (n >= V) return __builtin_nontemporal_load(reinterpret_cast<const rw4_any*>(p));
+  if (TAIL ? n >= V : n > 0) {
+    if constexpr (KEEP) return *reinterpret_cast<const rw4_any*>(p);
+    return __builtin_nontemporal_load(reinterpret_cast<const rw4_any*>(p));
+  }
+  if constexpr (!TAIL) return rw4{0u, 0u, 0u, 0u};
   uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int k = 0; k < V - 1; ++k)
@@ -102,11 +150,11 @@ __device__ __forceinline__ rw4 load_chunk(const char* p, int n) {
   return rw4{w[0], w[1], w[2], w[3]};
 }
 
-template <class T>
-__device__ __forceinline__ void store_chunk_n(char* p, int n, const rw4& r) {
+template <class T, bool TAIL = true>
+__device__ __forceinline__ void store_chunk(char* p, int n, const rw4& r) {
   constexpr int V = kChunk<T>;
-  if (n >= V) {
-    __builtin_nontemporal_store(r, reinterpret_cast<rw4_any*>(p));
+  if (!TAIL || n >= V) {
+    if (n > 0) __builtin_nontemporal_store(r, reinterpret_cast<rw4_any*>(p));
     return;
   }
 #pragma unroll
@@ -125,30 +173,34 @@ struct Codes {
   uint32_t w[V / 4];
 };
 
-template <int V>
+template <int V, bool KEEP = false, bool TAIL = true>
 __device__ __forceinline__ Codes<V> load_codes(const char* p, int n) {
   Codes<V> c;
-  if (n >= V) {
+  if (TAIL ? n >= V : n > 0) {
     if constexpr (V == 8) {
-      const rw2 r = __builtin_nontemporal_load(reinterpret_cast<const rw2_any*>(p));
+      const rw2_any* q = reinterpret_cast<const rw2_any*>(p);
+      const rw2 r = KEEP ? *q : __builtin_nontemporal_load(q);
       c.w[0] = r[0];
       c.w[1] = r[1];
     } else {
-      c.w[0] = __builtin_nontemporal_load(reinterpret_cast<const rw1_any*>(p));
+      const rw1_any* q = reinterpret_cast<const rw1_any*>(p);
+      c.w[0] = KEEP ? *q : __builtin_nontemporal_load(q);
     }
     return c;
   }
 #pragma unroll
   for (int k = 0; k < V / 4; ++k) c.w[k] = 0u;
+  if constexpr (!TAIL) return c;
 #pragma unroll
   for (int k = 0; k < V - 1; ++k)
     if (k < n) c.w[k / 4] |= static_cast<uint32_t>(reinterpret_cast<const uint8_t*>(p)[k]) << (8 * (k & 3));
   return c;
 }
 
-template <int V>
+template <int V, bool TAIL = true>
 __device__ __forceinline__ void store_codes(char* p, int n, const Codes<V>& c) {
-  if (n >= V) {
+  if (!TAIL && n == 0) return;
+  if (!TAIL || n >= V) {
     if constexpr (V == 8) {
       __builtin_nontemporal_store(rw2{c.w[0], c.w[1]}, reinterpret_cast<rw2_any*>(p));
     } else {
@@ -270,11 +322,7 @@ __device__ __forceinline__ uint32_t block_amax(const float (&x)[V], int lb) {
     const uint32_t b = as_bits(x[k]) & 0x7FFFFFFFu;
     m = b > m ? b : m;
   }
-  for (int k = 0; k < lb; ++k) {
-    const uint32_t o = static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 1 << k));
-    m = o > m ? o : m;
-  }
-  return m;
+  return static_cast<uint32_t>(over_lanes(static_cast<int>(m), lb, [](int a, int b) { return a > b ? a : b; }));
 }
 
 // ---------------------------------------------------------------- activations
@@ -288,13 +336,31 @@ __device__ __forceinline__ float sigmoid(float u) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u * -1.44269504088896341f));
 }
 
-__device__ __forceinline__ float normal_cdf(float u) { return 0.5f + 0.5f * erff(u * 0.70710678118654752f); }
+// e^(-u^2 / 2), and the normal distribution function from it:
+// 1 - Phi(|u|) = e^(-u^2 / 2) (a1 t + ... + a5 t^5) / 2 with
+// t = 1 / (1 + p |u| / sqrt 2), formula 7.1.26 of Abramowitz and Stegun's
+// Handbook of Mathematical Functions, whose erf is off by at most 1.5e-7.
+// One exponential and one reciprocal; it keeps its digits for large negative
+// u, where 1 + erf loses them.
+__device__ __forceinline__ float normal_bell(float u) {
+  return __builtin_amdgcn_exp2f(u * u * -0.721347520444481704f);
+}
+
+__device__ __forceinline__ float normal_cdf(float u, float bell) {
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(__builtin_fabsf(u), 0.3275911f * 0.707106781186547524f, 1.0f));
+  float q = __builtin_fmaf(t, 1.061405429f * 0.5f, -1.453152027f * 0.5f);
+  q = __builtin_fmaf(t, q, 1.421413741f * 0.5f);
+  q = __builtin_fmaf(t, q, -0.284496736f * 0.5f);
+  q = __builtin_fmaf(t, q, 0.254829592f * 0.5f);
+  q *= t * bell;
+  return u < 0.0f ? q : 1.0f - q;
+}
 
 // act(u)
 template <int ACT>
 __device__ __forceinline__ float act_value(float u) {
   if constexpr (ACT == kActSilu) return u * sigmoid(u);
-  if constexpr (ACT == kActGelu) return u * normal_cdf(u);
+  if constexpr (ACT == kActGelu) return u * normal_cdf(u, normal_bell(u));
   return u;
 }
 
@@ -306,9 +372,9 @@ __device__ __forceinline__ void act_both(float u, float* value, float* slope) {
     *value = u * s;
     *slope = s * (1.0f + u * (1.0f - s));
   } else if constexpr (ACT == kActGelu) {
-    const float p = normal_cdf(u);
+    const float bell = normal_bell(u), p = normal_cdf(u, bell);
     *value = u * p;
-    *slope = p + u * (0.398942280401432678f * __builtin_amdgcn_exp2f(u * u * -0.721347520444481704f));
+    *slope = __builtin_fmaf(u * 0.398942280401432678f, bell, p);
   } else {
     *value = u;
     *slope = 1.0f;

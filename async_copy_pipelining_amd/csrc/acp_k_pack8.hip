@@ -47,19 +47,19 @@ __device__ __forceinline__ void saved_chunk(const RowsArgs& A, const Codes<V>& c
   decode(A.format, c, s, x);
 }
 
-template <class T>
+template <class T, int U>
 __global__ __launch_bounds__(kRowThreads) void pack8_kernel(const RowsArgs A) {
-  constexpr int V = kChunk<T>, U = kRowUnroll;
-  const uint32_t i0 = blockIdx.x * (kRowThreads * U) + threadIdx.x;
+  constexpr int V = kChunk<T>;
+  const uint32_t i0 = blockIdx.x * (blockDim.x * U) + threadIdx.x;
   rw4 r[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const Chunk k(A, i0 + u * kRowThreads, V);
+    const Chunk k(A, i0 + u * blockDim.x, V);
     r[u] = load_chunk<T>(k.at(A.x, sizeof(T)), k.n);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const uint32_t i = i0 + u * kRowThreads;
+    const uint32_t i = i0 + u * blockDim.x;
     const Chunk k(A, i, V);
     float x[V];
     widen(r[u], x, static_cast<const T*>(nullptr));
@@ -67,43 +67,43 @@ __global__ __launch_bounds__(kRowThreads) void pack8_kernel(const RowsArgs A) {
   }
 }
 
-template <class T>
+template <class T, int U>
 __global__ __launch_bounds__(kRowThreads) void unpack8_kernel(const RowsArgs A) {
-  constexpr int V = kChunk<T>, U = kRowUnroll;
-  const uint32_t i0 = blockIdx.x * (kRowThreads * U) + threadIdx.x;
+  constexpr int V = kChunk<T>;
+  const uint32_t i0 = blockIdx.x * (blockDim.x * U) + threadIdx.x;
   Codes<V> c[U];
   float s[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const uint32_t i = i0 + u * kRowThreads;
+    const uint32_t i = i0 + u * blockDim.x;
     const Chunk k(A, i, V);
     c[u] = load_codes<V>(k.at(A.px.codes, 1), k.n);
     s[u] = k.n > 0 ? A.px.scales[i >> A.lb_log2] : 0.0f;
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const Chunk k(A, i0 + u * kRowThreads, V);
+    const Chunk k(A, i0 + u * blockDim.x, V);
     float x[V];
     saved_chunk<V>(A, c[u], s[u], x);
-    if (k.n > 0) store_chunk_n<T>(k.at(A.y, sizeof(T)), k.n, narrow(x, static_cast<const T*>(nullptr)));
+    if (k.n > 0) store_chunk<T>(k.at(A.y, sizeof(T)), k.n, narrow(x, static_cast<const T*>(nullptr)));
   }
 }
 
 // y = act(x) [* z], and x [and z] kept in 8 bits.
-template <class T, bool GATED, bool SAVE>
+template <class T, bool GATED, bool SAVE, int U>
 __global__ __launch_bounds__(kRowThreads) void act_forward_kernel(const RowsArgs A) {
-  constexpr int V = kChunk<T>, U = GATED ? kRowUnroll / 2 : kRowUnroll;
-  const uint32_t i0 = blockIdx.x * (kRowThreads * U) + threadIdx.x;
+  constexpr int V = kChunk<T>;
+  const uint32_t i0 = blockIdx.x * (blockDim.x * U) + threadIdx.x;
   rw4 rx[U], rz[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const Chunk k(A, i0 + u * kRowThreads, V);
+    const Chunk k(A, i0 + u * blockDim.x, V);
     rx[u] = load_chunk<T>(k.at(A.x, sizeof(T)), k.n);
     if constexpr (GATED) rz[u] = load_chunk<T>(k.at(A.z, sizeof(T)), k.n);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const uint32_t i = i0 + u * kRowThreads;
+    const uint32_t i = i0 + u * blockDim.x;
     const Chunk k(A, i, V);
     float x[V], z[V];
     widen(rx[u], x, static_cast<const T*>(nullptr));
@@ -115,21 +115,21 @@ __global__ __launch_bounds__(kRowThreads) void act_forward_kernel(const RowsArgs
 #pragma unroll
       for (int e = 0; e < V; ++e) x[e] *= z[e];
     }
-    if (k.n > 0) store_chunk_n<T>(k.at(A.y, sizeof(T)), k.n, narrow(x, static_cast<const T*>(nullptr)));
+    if (k.n > 0) store_chunk<T>(k.at(A.y, sizeof(T)), k.n, narrow(x, static_cast<const T*>(nullptr)));
   }
 }
 
 // dx = dy act'(x) [* z], dz = dy act(x), with x and z from their 8-bit forms.
-template <class T, bool GATED>
+template <class T, bool GATED, int U>
 __global__ __launch_bounds__(kRowThreads) void act_backward_kernel(const RowsArgs A) {
-  constexpr int V = kChunk<T>, U = GATED ? kRowUnroll / 2 : kRowUnroll;
-  const uint32_t i0 = blockIdx.x * (kRowThreads * U) + threadIdx.x;
+  constexpr int V = kChunk<T>;
+  const uint32_t i0 = blockIdx.x * (blockDim.x * U) + threadIdx.x;
   rw4 rd[U];
   Codes<V> cx[U], cz[U];
   float sx[U], sz[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const uint32_t i = i0 + u * kRowThreads;
+    const uint32_t i = i0 + u * blockDim.x;
     const Chunk k(A, i, V);
     rd[u] = load_chunk<T>(k.at(A.dy, sizeof(T)), k.n);
     cx[u] = load_codes<V>(k.at(A.px.codes, 1), k.n);
@@ -141,7 +141,7 @@ __global__ __launch_bounds__(kRowThreads) void act_backward_kernel(const RowsArg
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const Chunk k(A, i0 + u * kRowThreads, V);
+    const Chunk k(A, i0 + u * blockDim.x, V);
     float d[V], x[V], value[V], slope[V];
     widen(rd[u], d, static_cast<const T*>(nullptr));
     saved_chunk<V>(A, cx[u], sx[u], x);
@@ -156,9 +156,9 @@ __global__ __launch_bounds__(kRowThreads) void act_backward_kernel(const RowsArg
         slope[e] *= z[e];
         value[e] *= d[e];
       }
-      if (k.n > 0) store_chunk_n<T>(k.at(A.dz, sizeof(T)), k.n, narrow(value, static_cast<const T*>(nullptr)));
+      if (k.n > 0) store_chunk<T>(k.at(A.dz, sizeof(T)), k.n, narrow(value, static_cast<const T*>(nullptr)));
     }
-    if (k.n > 0) store_chunk_n<T>(k.at(A.dx, sizeof(T)), k.n, narrow(slope, static_cast<const T*>(nullptr)));
+    if (k.n > 0) store_chunk<T>(k.at(A.dx, sizeof(T)), k.n, narrow(slope, static_cast<const T*>(nullptr)));
   }
 }
 
@@ -166,53 +166,73 @@ __global__ __launch_bounds__(kRowThreads) void act_backward_kernel(const RowsArg
 
 namespace {
 
+// Up to this many chunks (one a lane, eight waves a CU) a call is bound by
+// latency: lanes take one chunk each and workgroups one wave, so that the
+// chunks spread over the CUs and a wave's code is short enough to come in
+// quickly.  Past it, workgroups of four waves with U chunks in flight a lane.
+constexpr uint32_t kSmallChunks = 256u * 64u * 8u;
+
 template <class K>
-hipError_t launch_rows(K kernel, const RowsArgs& a, int unroll, hipStream_t s) {
-  const uint32_t per = kRowThreads * static_cast<uint32_t>(unroll);
+hipError_t launch_rows(K kernel, const RowsArgs& a, uint32_t threads, uint32_t unroll, hipStream_t s) {
+  const uint32_t per = threads * unroll;
   const uint32_t grid = a.total / per + (a.total % per ? 1u : 0u);
   void* args[] = {const_cast<RowsArgs*>(&a)};
-  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(grid), dim3(kRowThreads), args, 0, s);
+  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(grid), dim3(threads), args, 0, s);
+}
+
+template <class K>
+hipError_t launch_rows(K one, K many, uint32_t unroll, const RowsArgs& a, hipStream_t s) {
+  return a.total <= kSmallChunks ? launch_rows(one, a, 64, 1, s) : launch_rows(many, a, kRowThreads, unroll, s);
+}
+
+template <class T>
+hipError_t pack8_t(const RowsArgs& a, hipStream_t s) {
+  return launch_rows(dev::pack8_kernel<T, 1>, dev::pack8_kernel<T, 4>, 4, a, s);
+}
+
+template <class T>
+hipError_t unpack8_t(const RowsArgs& a, hipStream_t s) {
+  return launch_rows(dev::unpack8_kernel<T, 1>, dev::unpack8_kernel<T, 4>, 4, a, s);
+}
+
+template <class T, bool GATED>
+hipError_t act_forward_t(bool save, const RowsArgs& a, hipStream_t s) {
+  constexpr int U = GATED ? 2 : 4;
+  return save ? launch_rows(dev::act_forward_kernel<T, GATED, true, 1>, dev::act_forward_kernel<T, GATED, true, U>, U, a, s)
+              : launch_rows(dev::act_forward_kernel<T, GATED, false, 1>, dev::act_forward_kernel<T, GATED, false, U>, U, a, s);
+}
+
+template <class T, bool GATED>
+hipError_t act_backward_t(const RowsArgs& a, hipStream_t s) {
+  constexpr int U = GATED ? 2 : 4;
+  return launch_rows(dev::act_backward_kernel<T, GATED, 1>, dev::act_backward_kernel<T, GATED, U>, U, a, s);
 }
 
 }  // namespace
 
 hipError_t pack8_launch(int dt, const RowsArgs& a, hipStream_t s) {
-  if (dt == kRowF16) return launch_rows(dev::pack8_kernel<_Float16>, a, kRowUnroll, s);
-  if (dt == kRowBF16) return launch_rows(dev::pack8_kernel<dev::bf16_t>, a, kRowUnroll, s);
-  return launch_rows(dev::pack8_kernel<float>, a, kRowUnroll, s);
+  if (dt == kRowF16) return pack8_t<_Float16>(a, s);
+  if (dt == kRowBF16) return pack8_t<dev::bf16_t>(a, s);
+  return pack8_t<float>(a, s);
 }
 
 hipError_t unpack8_launch(int dt, const RowsArgs& a, hipStream_t s) {
-  if (dt == kRowF16) return launch_rows(dev::unpack8_kernel<_Float16>, a, kRowUnroll, s);
-  if (dt == kRowBF16) return launch_rows(dev::unpack8_kernel<dev::bf16_t>, a, kRowUnroll, s);
-  return launch_rows(dev::unpack8_kernel<float>, a, kRowUnroll, s);
-}
-
-template <class T>
-static hipError_t act_forward_t(bool gated, bool save, const RowsArgs& a, hipStream_t s) {
-  if (gated)
-    return save ? launch_rows(dev::act_forward_kernel<T, true, true>, a, kRowUnroll / 2, s)
-                : launch_rows(dev::act_forward_kernel<T, true, false>, a, kRowUnroll / 2, s);
-  return save ? launch_rows(dev::act_forward_kernel<T, false, true>, a, kRowUnroll, s)
-              : launch_rows(dev::act_forward_kernel<T, false, false>, a, kRowUnroll, s);
+  if (dt == kRowF16) return unpack8_t<_Float16>(a, s);
+  if (dt == kRowBF16) return unpack8_t<dev::bf16_t>(a, s);
+  return unpack8_t<float>(a, s);
 }
 
 hipError_t act_forward_launch(int dt, bool gated, bool save, const RowsArgs& a, hipStream_t s) {
-  if (dt == kRowF16) return act_forward_t<_Float16>(gated, save, a, s);
-  if (dt == kRowBF16) return act_forward_t<dev::bf16_t>(gated, save, a, s);
-  return act_forward_t<float>(gated, save, a, s);
-}
-
-template <class T>
-static hipError_t act_backward_t(bool gated, const RowsArgs& a, hipStream_t s) {
-  return gated ? launch_rows(dev::act_backward_kernel<T, true>, a, kRowUnroll / 2, s)
-               : launch_rows(dev::act_backward_kernel<T, false>, a, kRowUnroll, s);
+  if (dt == kRowF16) return gated ? act_forward_t<_Float16, true>(save, a, s) : act_forward_t<_Float16, false>(save, a, s);
+  if (dt == kRowBF16)
+    return gated ? act_forward_t<dev::bf16_t, true>(save, a, s) : act_forward_t<dev::bf16_t, false>(save, a, s);
+  return gated ? act_forward_t<float, true>(save, a, s) : act_forward_t<float, false>(save, a, s);
 }
 
 hipError_t act_backward_launch(int dt, bool gated, const RowsArgs& a, hipStream_t s) {
-  if (dt == kRowF16) return act_backward_t<_Float16>(gated, a, s);
-  if (dt == kRowBF16) return act_backward_t<dev::bf16_t>(gated, a, s);
-  return act_backward_t<float>(gated, a, s);
+  if (dt == kRowF16) return gated ? act_backward_t<_Float16, true>(a, s) : act_backward_t<_Float16, false>(a, s);
+  if (dt == kRowBF16) return gated ? act_backward_t<dev::bf16_t, true>(a, s) : act_backward_t<dev::bf16_t, false>(a, s);
+  return gated ? act_backward_t<float, true>(a, s) : act_backward_t<float, false>(a, s);
 }
 
 }  // namespace acp

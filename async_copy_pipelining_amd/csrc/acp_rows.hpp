@@ -46,28 +46,39 @@ struct RowsArgs {
 };
 
 // Group norm.  A workgroup covers `lanes` chunks of a row (channel block
-// blk) and `row_lanes` rows at a time.  Sample n's rows are split into
-// `chunks` runs of `rpc` rows; row r of a sample is (r / row2.d, r % row2.d).
+// blk) and `row_lanes` rows at a time, over one of the runs of `run_rows`
+// rows that a sample's rows are split into.
 struct NormArgs {
-  RowTensor x, y, dy, dx;   // s[0] per sample, s[1] and s[2] per row index
-  Packed px;                // the saved form of x, written (forward) or read (backward)
+  RowTensor x, y, dy, dx;   // s[0] per sample; row r of a sample at r / row2.d * s[1] + r % row2.d * s[2]
+  RowTensor codes, scales;  // the saved form of x, written (forward) or read (backward)
   const float* gamma;       // nullptr: 1
   const float* beta;        // nullptr: 0
   float* mean;              // [samples, groups]
   float* rstd;
   float* dgamma;            // [c]
   float* dbeta;
-  float* part;              // workspace: partial statistics or partial sums
+  float* part;              // workspace: partial statistics or partial sums of the parts
   float* coef;              // workspace: two coefficients for each sample and group
   uint32_t samples, rows, c, groups, per_group;
-  Div row2, lanes;
-  uint32_t row_lanes, blocks;  // channel blocks of a row
-  uint32_t chunks, rpc;
+  Div row2, lanes, blocks;  // blocks: channel blocks of a row
+  uint32_t row_lanes;
+  Div runs;                 // runs of this pass
+  uint32_t run_rows;
+  uint32_t parts, part_rows;  // runs of the pass that left the parts, and their rows
   uint32_t pieces;          // channel blocks that one group may reach into
   uint32_t main_grid;       // workgroups before those that sum columns
   uint32_t col_rows;        // rows of partial column sums
   int lb_log2, group_lanes_log2, format, act;
   float eps;
+};
+
+// How a pass runs, beside its type.
+struct NormShape {
+  int dt;
+  bool linear;   // rows one stride apart, a run's bytes within 31 bits
+  bool whole;    // a chunk's channels are of one group
+  bool packed;   // forward: saves x in 8 bits; backward: x is its 8-bit form
+  uint32_t threads;
 };
 
 enum { kRowF16 = 0, kRowBF16 = 1, kRowF32 = 2 };
@@ -78,14 +89,24 @@ hipError_t unpack8_launch(int dt, const RowsArgs& a, hipStream_t s);
 hipError_t act_forward_launch(int dt, bool gated, bool save, const RowsArgs& a, hipStream_t s);
 hipError_t act_backward_launch(int dt, bool gated, const RowsArgs& a, hipStream_t s);
 
-hipError_t norm_stats_launch(int dt, const NormArgs& a, hipStream_t s);
-hipError_t norm_apply_launch(int dt, bool per_row, bool save, const NormArgs& a, hipStream_t s);
-hipError_t norm_sums_launch(int dt, bool packed, const NormArgs& a, hipStream_t s);
+// forward: one row a sample; a sample's slab on chip; by parts (two passes)
+hipError_t norm_row_launch(const NormShape& k, const NormArgs& a, hipStream_t s);
+hipError_t norm_slab_launch(const NormShape& k, const NormArgs& a, hipStream_t s);
+hipError_t norm_stats_launch(const NormShape& k, const NormArgs& a, hipStream_t s);
+hipError_t norm_apply_launch(const NormShape& k, const NormArgs& a, hipStream_t s);
+// backward, and the sums of columns that follow
+hipError_t norm_row_backward_launch(const NormShape& k, const NormArgs& a, hipStream_t s);
+hipError_t norm_slab_backward_launch(const NormShape& k, const NormArgs& a, hipStream_t s);
+hipError_t norm_sums_launch(const NormShape& k, const NormArgs& a, hipStream_t s);
 hipError_t norm_coef_launch(const NormArgs& a, hipStream_t s);
-hipError_t norm_dx_launch(int dt, bool per_row, bool packed, const NormArgs& a, hipStream_t s);
+hipError_t norm_dx_launch(const NormShape& k, const NormArgs& a, hipStream_t s);
 hipError_t norm_columns_launch(const NormArgs& a, hipStream_t s);
 
-constexpr int kRowThreads = 256;   // workgroup size of every row kernel
-constexpr int kRowUnroll = 4;      // chunks a lane has in flight
+constexpr int kRowThreads = 256;      // workgroup size, but for small calls and slabs
+constexpr int kRowUnroll = 4;         // chunks a lane has in flight
+constexpr int kSlabRows = 8;          // chunks that a lane of a forward slab holds
+constexpr int kSlabRowsBackward = 4;  // ... of a backward slab
+constexpr int kSlabThreads = 1024;    // largest workgroup of a forward slab
+constexpr int kSlabThreadsBackward = 512;
 
 }  // namespace acp

@@ -341,99 +341,245 @@ acp_status act_backward(acp_activation act, const acp_tile_desc* dx, const acp_t
 
 // ---------------------------------------------------------------- group norm
 
-// Workgroups that a pass over the data is split into.  By parts: enough to
-// fill 256 CUs several times over; each joins its sample's parts first, so no
-// more than 512 runs a sample.  Per row with sums of columns to leave behind:
-// two a CU, since each leaves 8 bytes for every channel.
-constexpr int64_t kNormGroups = 2048;
-constexpr int64_t kNormGroupsColumns = 512;
-constexpr int64_t kNormRuns = 512;
+// The form that a norm takes (acp_dev_norm.hpp).
+enum NormForm { kNormRow, kNormSlab, kNormParts };
 
-// Sizes, split and workspace of a group norm of `t`; tensors and pointers
-// are filled in by the caller.
+// Workgroups that the passes over the data aim at, on 256 CUs: the passes
+// that write the result several a CU; those that leave parts fewer, since the
+// next pass reads all parts of a sample (at most kNormMaxRuns of them); the
+// per-row and slab backward passes two and four a CU, since each leaves 8
+// bytes for every channel.
+constexpr int64_t kNormApply = 2048, kNormPartial = 1024, kNormRowBackward = 512, kNormSlabBackward = 1024;
+constexpr int64_t kNormMaxRuns = 256;
+
 struct NormPlan {
+  NormForm form = kNormParts;
   acp::NormArgs A{};
-  int dt = 0, v = 0;
-  bool per_row = false;
-  int64_t forward_bytes = 0, backward_bytes = 0;  // workspace
-  int64_t coef_at = 0;                            // of the backward pass
+  acp::NormShape K{};
+  acp::Div runs1{}, runs2{};  // by parts: runs of the two passes, and their rows
+  uint32_t rows1 = 0, rows2 = 0;
+  int64_t workspace = 0, coef_at = 0;
 };
 
-acp_status norm_plan(const acp::DescData& t, int groups, int block, bool backward, NormPlan* P) {
+// ACP_NORM_FORM=slab|parts (measurement aid): slab: not per row; parts: by
+// parts whatever fits.
+int norm_form_env() {
+  static const int v = [] {
+    const char* e = std::getenv("ACP_NORM_FORM");
+    return !e ? 0 : std::strcmp(e, "slab") == 0 ? 1 : std::strcmp(e, "parts") == 0 ? 2 : 0;
+  }();
+  return v;
+}
+
+int64_t gcd64(int64_t a, int64_t b) { return b ? gcd64(b, a % b) : a; }
+int64_t lcm64(int64_t a, int64_t b) { return a / gcd64(a, b) * b; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The sizes of one norm.
+struct NormDims {
+  int64_t samples, rows, c, groups, per, v, block;  // block: 0 without an 8-bit form
+  bool backward;
+};
+
+// Splits `rows` into runs of whole steps of row_lanes rows, about `target` of
+// them and at least `least` steps each.
+void split_rows(int64_t rows, int64_t row_lanes, int64_t target, int64_t least, int64_t* runs, int64_t* run_rows) {
+  target = std::max<int64_t>(1, target);
+  int64_t steps = std::max(ceil_div(ceil_div(rows, target), row_lanes), least);
+  steps = std::min(steps, std::max<int64_t>(1, ceil_div(rows, row_lanes)));
+  *run_rows = steps * row_lanes;
+  *runs = std::max<int64_t>(1, ceil_div(rows, *run_rows));
+}
+
+// A row's chunks in equal channel blocks of at most 256 lanes, each a whole
+// number of `unit` lanes.
+void split_lanes(int64_t cpr, int64_t unit, int64_t* lanes, int64_t* blocks) {
+  *blocks = ceil_div(cpr, acp::kRowThreads);
+  *lanes = ceil_div(ceil_div(cpr, *blocks), unit) * unit;
+  *blocks = ceil_div(cpr, *lanes);
+}
+
+void set_block(acp::NormArgs* A, int64_t lanes, int64_t blocks, int64_t threads) {
+  A->lanes = div_by(static_cast<uint64_t>(lanes));
+  A->blocks = div_by(static_cast<uint64_t>(blocks));
+  A->row_lanes = static_cast<uint32_t>(threads / lanes);
+}
+
+void set_runs(acp::NormArgs* A, int64_t runs, int64_t run_rows) {
+  A->runs = div_by(static_cast<uint64_t>(runs));
+  A->run_rows = static_cast<uint32_t>(run_rows);
+}
+
+// One row a sample, a group in a power of two of a wave's lanes: rows are
+// samples.
+bool plan_row(const NormDims& d, NormPlan* P) {
+  const int64_t gl = d.per / d.v;
+  if (d.rows != 1 || d.per % d.v || gl > 64 || (gl & (gl - 1))) return false;
+  P->form = kNormRow;
+  acp::NormArgs& A = P->A;
+  int64_t lanes, blocks, runs, run_rows;
+  // backward keeps no scale block together: it reads single codes
+  split_lanes(d.c / d.v, std::max(gl, d.block && !d.backward ? d.block / d.v : 1), &lanes, &blocks);
+  set_block(&A, lanes, blocks, acp::kRowThreads);
+  const int64_t target = (d.backward ? kNormRowBackward : kNormApply) / blocks;
+  split_rows(d.samples, A.row_lanes, target, 1, &runs, &run_rows);
+  set_runs(&A, runs, run_rows);
+  A.samples = 1;
+  A.rows = static_cast<uint32_t>(d.samples);
+  A.group_lanes_log2 = log2_of(gl);
+  A.main_grid = static_cast<uint32_t>(blocks * runs);
+  A.col_rows = static_cast<uint32_t>(runs);
+  P->K.threads = acp::kRowThreads;
+  P->workspace = d.backward ? runs * 2 * d.c * 4 : 0;
+  return true;
+}
+
+// All rows of a sample, for a block of whole groups (and whole scale blocks
+// where it saves), in a workgroup's registers.  Blocks are as narrow as leaves
+// 128 bytes of a row and a chunk for each of 256 lanes, so that small tensors
+// spread over many CUs.
+bool plan_slab(const NormDims& d, NormPlan* P) {
+  const int64_t U = d.backward ? acp::kSlabRowsBackward : acp::kSlabRows;
+  // a lane's statistics are one pair, or (groups that end inside a chunk) one
+  // for each channel of its chunk: those keep to 32 KiB of LDS
+  const bool whole = d.per % d.v == 0;
+  const int64_t most = d.backward ? acp::kSlabThreadsBackward : (whole || d.v == 4 ? acp::kSlabThreads : acp::kSlabThreads / 2);
+  const bool saves = d.block && !d.backward;
+  const int64_t cpr = ceil_div(d.c, d.v), align = saves ? d.block / d.v : 1;
+  const int64_t unit_c = saves ? lcm64(lcm64(d.per, d.v), d.block) : lcm64(d.per, d.v);
+  const int64_t unit = std::min(unit_c / d.v, ceil_div(cpr, align) * align);
+  auto fits = [&](int64_t lanes, int64_t threads) { return lanes <= threads && U * (threads / lanes) >= d.rows; };
+  if (!fits(unit, most)) return false;
+  int64_t lanes = unit;
+  while (lanes < cpr && (lanes < 8 || d.rows * lanes < 256) && fits(lanes + unit, most)) lanes += unit;
+  int64_t blocks = ceil_div(cpr, lanes);
+  if (blocks == 1) lanes = ceil_div(cpr, align) * align;
+  if (!fits(lanes, most)) return false;
+  int64_t threads = 64;
+  while (!fits(lanes, threads)) threads *= 2;
+  // few workgroups: more lanes with fewer chunks each
+  while (threads < most && d.samples * blocks * threads <= 256 * 512 && 2 * (threads / lanes) < d.rows) threads *= 2;
+  P->form = kNormSlab;
+  acp::NormArgs& A = P->A;
+  set_block(&A, lanes, blocks, threads);
+  const int64_t runs =
+      d.backward ? std::max<int64_t>(1, std::min(d.samples, kNormSlabBackward / blocks)) : 1;
+  set_runs(&A, runs, d.rows);
+  A.samples = static_cast<uint32_t>(d.samples);
+  A.rows = static_cast<uint32_t>(d.rows);
+  A.main_grid = static_cast<uint32_t>(d.backward ? blocks * runs : d.samples * blocks);
+  A.col_rows = static_cast<uint32_t>(runs);
+  P->K.threads = static_cast<uint32_t>(threads);
+  P->workspace = d.backward && runs > 1 ? runs * 2 * d.c * 4 : 0;
+  return true;
+}
+
+void plan_parts(const NormDims& d, NormPlan* P) {
+  P->form = kNormParts;
+  acp::NormArgs& A = P->A;
+  int64_t lanes, blocks, runs, run_rows;
+  const int64_t cpr = ceil_div(d.c, d.v);
+  split_lanes(cpr, d.block && !d.backward ? d.block / d.v : 1, &lanes, &blocks);
+  set_block(&A, lanes, blocks, acp::kRowThreads);
+  const int64_t each = std::max<int64_t>(1, d.samples * blocks);
+  split_rows(d.rows, A.row_lanes, std::min(kNormMaxRuns, kNormPartial / each), 2, &runs, &run_rows);
+  P->runs1 = div_by(static_cast<uint64_t>(runs));
+  P->rows1 = static_cast<uint32_t>(run_rows);
+  A.parts = static_cast<uint32_t>(runs);
+  A.part_rows = static_cast<uint32_t>(run_rows);
+  int64_t runs2;
+  split_rows(d.rows, A.row_lanes, kNormApply / each, 2, &runs2, &run_rows);
+  P->runs2 = div_by(static_cast<uint64_t>(runs2));
+  P->rows2 = static_cast<uint32_t>(run_rows);
+  A.samples = static_cast<uint32_t>(d.samples);
+  A.rows = static_cast<uint32_t>(d.rows);
+  const int64_t width = lanes * d.v;
+  A.pieces = static_cast<uint32_t>(std::min(blocks, (d.per + width - 2) / width + 1));
+  A.col_rows = static_cast<uint32_t>(d.samples);
+  P->K.threads = acp::kRowThreads;
+  P->coef_at = align_up(d.samples * runs * 2 * d.c * 4, 16);
+  P->workspace = d.backward ? P->coef_at + d.samples * d.groups * 8 : d.samples * d.groups * runs * A.pieces * 8;
+}
+
+acp_status norm_dims(const acp::DescData& t, int groups, int block, bool backward, NormDims* d) {
   const int r = t.rank;
   if (r < 2) return ret(ACP_ERR_INVALID, "group norm needs a sample dim and a channel dim");
-  const int64_t samples = t.shape[0], c = t.shape[r - 1];
-  int64_t rows = 1;
-  for (int d = 1; d + 1 < r; ++d) rows *= t.shape[d];
-  if (c < 1 || rows < 1) return ret(ACP_ERR_INVALID, "group norm needs at least one row and one channel");
-  if (groups < 1 || c % groups) return ret(ACP_ERR_INVALID, "the groups must divide the channels");
-  if (samples >= kRowLimit || rows >= kRowLimit || c >= kRowLimit / 2)
+  d->samples = t.shape[0];
+  d->c = t.shape[r - 1];
+  d->rows = 1;
+  for (int k = 1; k + 1 < r; ++k) d->rows *= t.shape[k];
+  if (d->c < 1 || d->rows < 1) return ret(ACP_ERR_INVALID, "group norm needs at least one row and one channel");
+  if (groups < 1 || d->c % groups) return ret(ACP_ERR_INVALID, "the groups must divide the channels");
+  if (d->samples >= kRowLimit || d->rows >= kRowLimit || d->c >= kRowLimit / 2 ||
+      d->samples * ceil_div(d->c, 64) >= kRowLimit)
     return ret(ACP_ERR_UNSUPPORTED, "group norm extents go up to 2^31");
-  acp::NormArgs& A = P->A;
-  P->dt = row_dtype(t.dtype);
-  P->v = 16 / t.esize;
-  const int64_t v = P->v, per = c / groups;
-  const int64_t gl = per / v;  // lanes of a group
-  P->per_row = rows == 1 && per % v == 0 && gl <= 64 && (gl & (gl - 1)) == 0;
-  // lanes: the row's chunks in equal channel blocks, in whole scale blocks
-  // and (per row) whole groups
-  const int64_t unit = std::max<int64_t>(block ? block / v : 1, P->per_row ? gl : 1);
-  const int64_t cpr = (c + v - 1) / v;
-  int64_t blocks = (cpr + acp::kRowThreads - 1) / acp::kRowThreads;
-  int64_t lanes = ((cpr + blocks - 1) / blocks + unit - 1) / unit * unit;
-  blocks = (cpr + lanes - 1) / lanes;
-  const int64_t row_lanes = acp::kRowThreads / lanes;
-  const int64_t n = P->per_row ? 1 : samples;
-  if (P->per_row) rows = samples;
-  const int64_t target = P->per_row && backward ? kNormGroupsColumns : kNormGroups;
-  const int64_t want = std::min(P->per_row ? target : kNormRuns, std::max<int64_t>(1, target / std::max<int64_t>(1, n * blocks)));
-  int64_t rpc = std::max<int64_t>((rows + want - 1) / want, row_lanes * (P->per_row ? 1 : acp::kRowUnroll));
-  rpc = (rpc + row_lanes - 1) / row_lanes * row_lanes;
-  const int64_t chunks = rows ? (rows + rpc - 1) / rpc : 1;
-  if (n * blocks * chunks + 2 * c / 32 + 1 >= kRowLimit || n * groups >= kRowLimit * 128)
-    return ret(ACP_ERR_UNSUPPORTED, "more than 2^31 workgroups");
-  A.samples = static_cast<uint32_t>(n);
-  A.rows = static_cast<uint32_t>(rows);
-  A.c = static_cast<uint32_t>(c);
-  A.groups = static_cast<uint32_t>(groups);
-  A.per_group = static_cast<uint32_t>(per);
-  A.lanes = div_by(static_cast<uint64_t>(lanes));
-  A.row_lanes = static_cast<uint32_t>(row_lanes);
-  A.blocks = static_cast<uint32_t>(blocks);
-  A.chunks = static_cast<uint32_t>(chunks);
-  A.rpc = static_cast<uint32_t>(rpc);
-  const int64_t width = lanes * v;
-  A.pieces = static_cast<uint32_t>(std::min(blocks, (per + width - 2) / width + 1));
-  A.lb_log2 = block ? log2_of(block / v) : 0;
-  A.group_lanes_log2 = P->per_row ? log2_of(gl) : 0;
-  A.col_rows = static_cast<uint32_t>(P->per_row ? (rows ? chunks : 0) : n);
-  P->forward_bytes = P->per_row ? 0 : n * groups * chunks * A.pieces * 8;
-  P->coef_at = align_up(n * chunks * 2 * c * 4, 16);
-  P->backward_bytes = P->coef_at + (P->per_row ? 0 : n * groups * 8);
+  d->groups = groups;
+  d->per = d->c / groups;
+  d->v = 16 / t.esize;
+  d->block = block;
+  d->backward = backward;
   return ACP_OK;
 }
 
-// Rows of the tensors: s[0] per sample, (s[1], s[2]) per row of a sample.
-acp_status norm_rows(const acp::DescData* const* t, acp::RowTensor* const* rt, int nt, NormPlan* P) {
-  Collapsed o;
-  if (P->per_row) {
-    P->A.row2 = div_by(1);
-    for (int k = 0; k < nt; ++k) {
-      rt[k]->p = reinterpret_cast<char*>(t[k]->gbase);
-      rt[k]->s[0] = rt[k]->s[2] = 0;
-      rt[k]->s[1] = t[k]->strides[0] * t[k]->esize;
-    }
-    return ACP_OK;
+// Whether the rows of a run of every tensor lie one stride apart, within the
+// 31 bits that the kernels' lane offsets take.
+bool norm_linear(const Collapsed& o, int nt, const NormDims& d, const NormPlan& P, int64_t run_rows, bool by_sample,
+                 const acp::DescData* const* t) {
+  const int64_t reach = run_rows + 3 * int64_t(2) * acp::kRowUnroll * P.A.row_lanes;
+  auto in = [&](int64_t stride) { return reach * stride + 16 * P.A.lanes.d < (int64_t(1) << 31); };
+  if (!by_sample && o.n > 1) return false;
+  for (int k = 0; k < nt; ++k) {
+    const int64_t stride = by_sample ? t[k]->strides[0] * t[k]->esize : (o.n ? o.stride[k][0] : 0);
+    if (!in(stride)) return false;
   }
+  return !d.block || in(ceil_div(d.c, d.block) * 4);
+}
+
+// The form, split and tensors of a norm over `t` (of one shape).  `scales`:
+// of the 8-bit form, or nullptr.
+acp_status norm_plan(const acp::DescData* const* t, acp::RowTensor* const* rt, int nt, const NormDims& d,
+                     float* scales, NormPlan* out) {
+  Collapsed o;
   if (!collapse(t, nt, 1, 2, &o))
     return ret(ACP_ERR_UNSUPPORTED, "the inner row dims of these strides do not join into two");
-  P->A.row2 = div_by(static_cast<uint64_t>(o.n >= 1 ? o.ext[o.n - 1] : 1));
-  for (int k = 0; k < nt; ++k) {
-    rt[k]->p = reinterpret_cast<char*>(t[k]->gbase);
-    rt[k]->s[0] = t[k]->strides[0] * t[k]->esize;
-    rt[k]->s[1] = o.n >= 2 ? o.stride[k][0] : 0;
-    rt[k]->s[2] = o.n >= 1 ? o.stride[k][o.n - 1] : 0;
+  // the tensors' pointers are members of *out: the plan is made beside them
+  NormPlan P;
+  const int env = norm_form_env();
+  bool done = env < 1 && plan_row(d, &P) && norm_linear(o, nt, d, P, P.A.run_rows, true, t);
+  if (!done) P = NormPlan();
+  if (!done && env < 2) done = plan_slab(d, &P) && norm_linear(o, nt, d, P, P.A.run_rows, false, t);
+  if (!done) {
+    P = NormPlan();
+    plan_parts(d, &P);
   }
+  const bool row = P.form == kNormRow;
+  acp::NormArgs& A = P.A;
+  P.K.linear = P.form != kNormParts || norm_linear(o, nt, d, P, std::max(P.rows1, P.rows2), false, t);
+  P.K.whole = d.per % d.v == 0;
+  P.K.packed = d.block != 0;
+  P.K.dt = row_dtype(t[0]->dtype);
+  A.c = static_cast<uint32_t>(d.c);
+  A.groups = static_cast<uint32_t>(d.groups);
+  A.per_group = static_cast<uint32_t>(d.per);
+  A.lb_log2 = d.block ? log2_of(d.block / d.v) : 0;
+  A.row2 = div_by(static_cast<uint64_t>(row ? std::max<int64_t>(1, d.samples) : (o.n >= 1 ? o.ext[o.n - 1] : 1)));
+  const int64_t scale_row = d.block ? ceil_div(d.c, d.block) * 4 : 0;
+  A.scales.p = reinterpret_cast<char*>(scales);
+  A.scales.s[0] = row ? 0 : scale_row * d.rows;
+  A.scales.s[1] = row ? 0 : scale_row * A.row2.d;
+  A.scales.s[2] = scale_row;
+  acp::RowTensor v[4];
+  for (int k = 0; k < nt; ++k) {
+    v[k].p = reinterpret_cast<char*>(t[k]->gbase);
+    const int64_t sample = t[k]->strides[0] * t[k]->esize;
+    v[k].s[0] = row ? 0 : sample;
+    v[k].s[1] = !row && o.n >= 2 ? o.stride[k][0] : 0;
+    v[k].s[2] = row ? sample : (o.n >= 1 ? o.stride[k][o.n - 1] : 0);
+  }
+  if (static_cast<int64_t>(A.samples) * A.blocks.d * std::max({A.runs.d, P.runs1.d, P.runs2.d}) + d.c / 16 + 1 >= kRowLimit)
+    return ret(ACP_ERR_UNSUPPORTED, "more than 2^31 workgroups");
+  *out = P;
+  for (int k = 0; k < nt; ++k) *rt[k] = v[k];
   return ACP_OK;
 }
 
@@ -448,9 +594,12 @@ acp_status check_workspace(const void* workspace, int64_t bytes, int64_t need) {
 }
 
 std::string norm_text(const char* what, const NormPlan& P) {
-  return std::string(what) + (P.per_row ? " per row" : " by parts") + " lanes " + std::to_string(P.A.lanes.d) + "x" +
-         std::to_string(P.A.row_lanes) + " blocks " + std::to_string(P.A.blocks) + " runs " +
-         std::to_string(P.A.chunks);
+  static const char* const forms[] = {" per row", " slab", " by parts"};
+  return std::string(what) + forms[P.form] + (P.K.whole ? " whole" : " split") + (P.K.linear ? "" : " strided") +
+         " threads " + std::to_string(P.K.threads) + " lanes " + std::to_string(P.A.lanes.d) + "x" +
+         std::to_string(P.A.row_lanes) + " blocks " + std::to_string(P.A.blocks.d) + " runs " +
+         std::to_string(P.form == kNormParts ? P.runs1.d : P.A.runs.d) +
+         (P.form == kNormParts ? "+" + std::to_string(P.runs2.d) : std::string());
 }
 
 acp_status group_norm_workspace(const acp_tile_desc* x, int groups, int64_t* bytes) {
@@ -458,13 +607,18 @@ acp_status group_norm_workspace(const acp_tile_desc* x, int groups, int64_t* byt
   if (!bytes) return ret(ACP_ERR_INVALID, "null argument");
   const acp_status st = load_float(x, "x", &xd);
   if (st != ACP_OK) return st;
+  // the strides of the other tensors decide about the form: the most of all
   int64_t need = 0;
   for (int block : {0, 32, 64, 128, 256})
     for (int backward = 0; backward < 2; ++backward) {
-      NormPlan P;
-      const acp_status sp = norm_plan(xd, groups, block, backward != 0, &P);
-      if (sp != ACP_OK) return sp;
-      need = std::max(need, backward ? P.backward_bytes : P.forward_bytes);
+      NormDims d;
+      const acp_status sd = norm_dims(xd, groups, block, backward != 0, &d);
+      if (sd != ACP_OK) return sd;
+      NormPlan row, slab, parts;
+      if (plan_row(d, &row)) need = std::max(need, row.workspace);
+      if (plan_slab(d, &slab)) need = std::max(need, slab.workspace);
+      plan_parts(d, &parts);
+      need = std::max(need, parts.workspace);
     }
   *bytes = need;
   return ret(ACP_OK);
@@ -483,27 +637,27 @@ acp_status group_norm(const acp_tile_desc* y, const acp_tile_desc* x, const floa
   if (save && (st = load_packed(save, xd, "the saved x", &cd)) != ACP_OK) return st;
   if (misaligned4(gamma) || misaligned4(beta) || misaligned4(mean) || misaligned4(rstd))
     return ret(ACP_ERR_INVALID, "a float32 array is not 4-byte aligned");
+  NormDims d;
+  if ((st = norm_dims(xd, groups, save ? save->block : 0, false, &d)) != ACP_OK) return st;
   NormPlan P;
-  if ((st = norm_plan(xd, groups, save ? save->block : 0, false, &P)) != ACP_OK) return st;
-  if ((st = check_workspace(workspace, workspace_bytes, P.forward_bytes)) != ACP_OK) return st;
+  acp::NormArgs& A = P.A;
+  const acp::DescData* t[] = {&xd, &yd, &cd};
+  acp::RowTensor* rt[] = {&A.x, &A.y, &A.codes};
+  if ((st = norm_plan(t, rt, save ? 3 : 2, d, save ? save->scales : nullptr, &P)) != ACP_OK) return st;
+  if ((st = check_workspace(workspace, workspace_bytes, P.workspace)) != ACP_OK) return st;
   if (self_overlap(yd) || (save && self_overlap(cd))) return ret(ACP_ERR_INVALID, "an output overlaps itself");
-  const int64_t c = xd.shape[xd.rank - 1], stat = xd.shape[0] * groups * 4;
+  const int64_t stat = d.samples * groups * 4;
   Range w[6] = {range_of(yd, "y"), range_of(mean, stat, "mean"), range_of(rstd, stat, "rstd"),
-                range_of(workspace, P.forward_bytes, "the workspace")};
+                range_of(workspace, P.workspace, "the workspace")};
   int nw = 4;
   if (save) {
     w[nw++] = range_of(cd, "the codes");
     w[nw++] = range_of(save->scales, scale_bytes(cd, save->block), "the scales");
   }
-  const Range r[] = {range_of(xd, "x"), range_of(gamma, c * 4, "gamma"), range_of(beta, c * 4, "beta")};
+  const Range r[] = {range_of(xd, "x"), range_of(gamma, d.c * 4, "gamma"), range_of(beta, d.c * 4, "beta")};
   if ((st = check_ranges(w, nw, r, 3)) != ACP_OK) return st;
   if (elements(xd) == 0) return launched_nothing();
   if ((st = check_stream(stream)) != ACP_OK) return st;
-  acp::NormArgs& A = P.A;
-  const acp::DescData* t[] = {&xd, &yd, &cd};
-  acp::RowTensor* rt[] = {&A.x, &A.y, &A.px.codes};
-  if ((st = norm_rows(t, rt, save ? 3 : 2, &P)) != ACP_OK) return st;
-  A.px.scales = save ? save->scales : nullptr;
   A.format = save ? save->format : 0;
   A.gamma = gamma;
   A.beta = beta;
@@ -514,8 +668,18 @@ acp_status group_norm(const acp_tile_desc* y, const acp_tile_desc* x, const floa
   A.eps = eps;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = hipSuccess;
-  if (!P.per_row) e = acp::norm_stats_launch(P.dt, A, s);
-  if (e == hipSuccess) e = acp::norm_apply_launch(P.dt, P.per_row, save != nullptr, A, s);
+  if (P.form == kNormRow) e = acp::norm_row_launch(P.K, A, s);
+  if (P.form == kNormSlab) e = acp::norm_slab_launch(P.K, A, s);
+  if (P.form == kNormParts) {
+    A.runs = P.runs1;
+    A.run_rows = P.rows1;
+    A.main_grid = A.samples * A.blocks.d * A.runs.d;
+    e = acp::norm_stats_launch(P.K, A, s);
+    A.runs = P.runs2;
+    A.run_rows = P.rows2;
+    A.main_grid = A.samples * A.blocks.d * A.runs.d;
+    if (e == hipSuccess) e = acp::norm_apply_launch(P.K, A, s);
+  }
   return launched(e, norm_text(save ? "group norm saved" : "group norm", P));
 }
 
@@ -537,15 +701,20 @@ acp_status group_norm_backward(const acp_tile_desc* dx, float* dgamma, float* db
   if (misaligned4(gamma) || misaligned4(beta) || misaligned4(mean) || misaligned4(rstd) || misaligned4(dgamma) ||
       misaligned4(dbeta))
     return ret(ACP_ERR_INVALID, "a float32 array is not 4-byte aligned");
+  NormDims d;
+  if ((st = norm_dims(dyd, groups, saved ? saved->block : 0, true, &d)) != ACP_OK) return st;
   NormPlan P;
-  if ((st = norm_plan(dyd, groups, saved ? saved->block : 0, true, &P)) != ACP_OK) return st;
-  if ((st = check_workspace(workspace, workspace_bytes, P.backward_bytes)) != ACP_OK) return st;
+  acp::NormArgs& A = P.A;
+  const acp::DescData* t[] = {&dyd, &dxd, x ? &xd : &cd};
+  acp::RowTensor* rt[] = {&A.dy, &A.dx, x ? &A.x : &A.codes};
+  if ((st = norm_plan(t, rt, 3, d, saved ? saved->scales : nullptr, &P)) != ACP_OK) return st;
+  if ((st = check_workspace(workspace, workspace_bytes, P.workspace)) != ACP_OK) return st;
   if (self_overlap(dxd)) return ret(ACP_ERR_INVALID, "an output overlaps itself");
-  const int64_t c = dyd.shape[dyd.rank - 1], stat = dyd.shape[0] * groups * 4;
-  const Range w[] = {range_of(dxd, "dx"), range_of(dgamma, c * 4, "dgamma"), range_of(dbeta, c * 4, "dbeta"),
-                     range_of(workspace, P.backward_bytes, "the workspace")};
+  const int64_t stat = d.samples * groups * 4;
+  const Range w[] = {range_of(dxd, "dx"), range_of(dgamma, d.c * 4, "dgamma"), range_of(dbeta, d.c * 4, "dbeta"),
+                     range_of(workspace, P.workspace, "the workspace")};
   Range r[7] = {range_of(dyd, "dy"), range_of(mean, stat, "mean"), range_of(rstd, stat, "rstd"),
-                range_of(gamma, c * 4, "gamma"), range_of(beta, c * 4, "beta")};
+                range_of(gamma, d.c * 4, "gamma"), range_of(beta, d.c * 4, "beta")};
   int nr = 5;
   if (x) r[nr++] = range_of(xd, "x");
   if (saved) {
@@ -553,11 +722,6 @@ acp_status group_norm_backward(const acp_tile_desc* dx, float* dgamma, float* db
     r[nr++] = range_of(saved->scales, scale_bytes(cd, saved->block), "the scales");
   }
   if ((st = check_ranges(w, 4, r, nr)) != ACP_OK) return st;
-  acp::NormArgs& A = P.A;
-  const acp::DescData* t[] = {&dyd, &dxd, x ? &xd : &cd};
-  acp::RowTensor* rt[] = {&A.dy, &A.dx, x ? &A.x : &A.px.codes};
-  if ((st = norm_rows(t, rt, 3, &P)) != ACP_OK) return st;
-  A.px.scales = saved ? saved->scales : nullptr;
   A.format = saved ? saved->format : 0;
   A.gamma = gamma;
   A.beta = beta;
@@ -576,13 +740,20 @@ acp_status group_norm_backward(const acp_tile_desc* dx, float* dgamma, float* db
     if (!dgamma && !dbeta) return launched_nothing();
     return launched(acp::norm_columns_launch(A, s), "group norm backward of no samples");
   }
-  if (P.per_row) {
-    e = acp::norm_dx_launch(P.dt, true, saved != nullptr, A, s);
-    if (e == hipSuccess) e = acp::norm_columns_launch(A, s);
-  } else {
-    e = acp::norm_sums_launch(P.dt, saved != nullptr, A, s);
+  if (P.form == kNormRow) e = acp::norm_row_backward_launch(P.K, A, s);
+  if (P.form == kNormSlab) e = acp::norm_slab_backward_launch(P.K, A, s);
+  if (P.form == kNormParts) {
+    A.runs = P.runs1;
+    A.run_rows = P.rows1;
+    A.main_grid = A.samples * A.blocks.d * A.runs.d;
+    e = acp::norm_sums_launch(P.K, A, s);
     if (e == hipSuccess) e = acp::norm_coef_launch(A, s);
-    if (e == hipSuccess) e = acp::norm_dx_launch(P.dt, false, saved != nullptr, A, s);
+    A.runs = P.runs2;
+    A.run_rows = P.rows2;
+    A.main_grid = A.samples * A.blocks.d * A.runs.d;
+    if (e == hipSuccess) e = acp::norm_dx_launch(P.K, A, s);
+  } else if (P.workspace > 0 && e == hipSuccess) {
+    e = acp::norm_columns_launch(A, s);
   }
   return launched(e, norm_text(saved ? "group norm backward from 8 bits" : "group norm backward", P));
 }

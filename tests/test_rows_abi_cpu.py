@@ -89,6 +89,18 @@ def norm(**kw):
     acp.acp_group_norm(**a)
 
 
+# rows that no workgroup holds: these take the workspace
+BIG = (4, 20000, 64)
+
+
+def norm_big(**kw):
+    norm(x=desc(1, BIG), y=desc(2, BIG), **kw)
+
+
+def grad_big(**kw):
+    grad(dx=desc(5, BIG), dy=desc(4, BIG), x=desc(1, BIG), **kw)
+
+
 def grad(**kw):
     a = dict(dx=DX, dgamma=BASE * 24, dbeta=BASE * 25, dy=DY, x=X, mean=BASE * 22, rstd=BASE * 23, gamma=BASE * 20,
              beta=BASE * 21, groups=8, act="silu", **WS)
@@ -114,10 +126,10 @@ def grad(**kw):
     (lambda: norm(gamma=BASE * 20 + 2), INVALID, "aligned"),
     (lambda: norm(mean=BASE * 20), INVALID, "share memory"),
     (lambda: norm(rstd=BASE * 22), INVALID, "share memory"),
-    (lambda: norm(workspace=None), INVALID, "workspace"),
-    (lambda: norm(workspace_bytes=8), INVALID, "workspace"),
-    (lambda: norm(workspace=BASE * 30 + 8), INVALID, "16-byte"),
-    (lambda: norm(workspace=BASE * 1), INVALID, "share memory"),
+    (lambda: norm_big(workspace=None), INVALID, "workspace"),
+    (lambda: norm_big(workspace_bytes=8), INVALID, "workspace"),
+    (lambda: norm_big(workspace=BASE * 30 + 8), INVALID, "16-byte"),
+    (lambda: norm_big(workspace=BASE * 1), INVALID, "share memory"),
     (lambda: norm(save=packed(8, shape=(4, 6, 32))), INVALID, "shape"),
     (lambda: norm(save=packed(2)), INVALID, "share memory"),
     (lambda: norm(x=desc(1, dtype="u16"), y=desc(2, dtype="u16")), UNSUPPORTED, "f16, bf16 or f32"),
@@ -134,7 +146,7 @@ def grad(**kw):
     (lambda: grad(x=packed(5)), INVALID, "share memory"),
     (lambda: grad(x=packed(8, block=16)), INVALID, "block"),
     (lambda: grad(dy=desc(4, dtype="f32")), INVALID, "differ"),
-    (lambda: grad(workspace_bytes=64), INVALID, "workspace"),
+    (lambda: grad_big(workspace_bytes=64), INVALID, "workspace"),
     (lambda: grad(groups=9), INVALID, "divide"),
 ])
 def test_refusals_of_group_norm(call, status, why):
