@@ -233,53 +233,50 @@ def acp_stream_binary(op, out: acp_tile_desc, x: acp_tile_desc, z: acp_tile_desc
                                   int(threads), int(workgroups), stg, _stream(stream)))
 
 
-def _ref(x):
-    return None if x is None else ctypes.byref(x)
-
-
+# The row operators take descriptors and packed forms as they are: ctypes
+# passes a structure by reference where a pointer is declared.
 def _act(act) -> int:
     return ACTIVATIONS[act] if isinstance(act, str) else int(act)
 
 
 def acp_pack8(out: acp_packed8, x: acp_tile_desc, stream=None) -> None:
-    _check(_lib.acp_pack8(_ref(out), _ref(x), _stream(stream)))
+    _check(_lib.acp_pack8(out, x, _stream(stream)))
 
 
 def acp_unpack8(out: acp_tile_desc, src: acp_packed8, stream=None) -> None:
-    _check(_lib.acp_unpack8(_ref(out), _ref(src), _stream(stream)))
+    _check(_lib.acp_unpack8(out, src, _stream(stream)))
 
 
 def acp_act_forward(act, out: acp_tile_desc, x: acp_tile_desc, z: acp_tile_desc | None = None,
                     save_x: acp_packed8 | None = None, save_z: acp_packed8 | None = None, stream=None) -> None:
-    _check(_lib.acp_act_forward(_act(act), _ref(out), _ref(x), _ref(z), _ref(save_x), _ref(save_z), _stream(stream)))
+    _check(_lib.acp_act_forward(_act(act), out, x, z, save_x, save_z, _stream(stream)))
 
 
 def acp_act_backward(act, dx: acp_tile_desc, dz: acp_tile_desc | None, dy: acp_tile_desc, x: acp_packed8,
                      z: acp_packed8 | None = None, stream=None) -> None:
-    _check(_lib.acp_act_backward(_act(act), _ref(dx), _ref(dz), _ref(dy), _ref(x), _ref(z), _stream(stream)))
+    _check(_lib.acp_act_backward(_act(act), dx, dz, dy, x, z, _stream(stream)))
 
 
 def acp_group_norm_workspace(x: acp_tile_desc, groups: int) -> int:
     n = ctypes.c_int64()
-    _check(_lib.acp_group_norm_workspace(_ref(x), int(groups), ctypes.byref(n)))
+    _check(_lib.acp_group_norm_workspace(x, int(groups), ctypes.byref(n)))
     return n.value
 
 
 def acp_group_norm(y: acp_tile_desc, x: acp_tile_desc, gamma, beta, groups: int, eps: float, act="none", mean=None,
                    rstd=None, save: acp_packed8 | None = None, workspace=None, workspace_bytes: int = 0,
                    stream=None) -> None:
-    _check(_lib.acp_group_norm(_ref(y), _ref(x), _ptr(gamma), _ptr(beta), int(groups), float(eps), _act(act),
-                               _ptr(mean), _ptr(rstd), _ref(save), _ptr(workspace), int(workspace_bytes),
-                               _stream(stream)))
+    _check(_lib.acp_group_norm(y, x, _ptr(gamma), _ptr(beta), groups, eps, _act(act), _ptr(mean), _ptr(rstd), save,
+                               _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 def acp_group_norm_backward(dx: acp_tile_desc, dgamma, dbeta, dy: acp_tile_desc, x: acp_tile_desc | acp_packed8,
                             mean, rstd, gamma, beta, groups: int, act="none", workspace=None,
                             workspace_bytes: int = 0, stream=None) -> None:
     plain, saved = (None, x) if isinstance(x, acp_packed8) else (x, None)
-    _check(_lib.acp_group_norm_backward(_ref(dx), _ptr(dgamma), _ptr(dbeta), _ref(dy), _ref(plain), _ref(saved),
-                                        _ptr(mean), _ptr(rstd), _ptr(gamma), _ptr(beta), int(groups), _act(act),
-                                        _ptr(workspace), int(workspace_bytes), _stream(stream)))
+    _check(_lib.acp_group_norm_backward(dx, _ptr(dgamma), _ptr(dbeta), dy, plain, saved, _ptr(mean), _ptr(rstd),
+                                        _ptr(gamma), _ptr(beta), groups, _act(act), _ptr(workspace), workspace_bytes,
+                                        _stream(stream)))
 
 
 def acp_debug_lds_image(src: acp_tile_desc, tile_index: int, threads: int, out_bytes, stream=None) -> None:

@@ -37,8 +37,10 @@ SOURCES = [
     ("acp_k_stream_f16.hip", True),
     ("acp_k_ref.hip", True),
     ("acp_k_pack8.hip", True),
-    ("acp_k_norm_fwd.hip", True),
-    ("acp_k_norm_bwd.hip", True),
+    ("acp_k_norm.hip", True),
+    ("acp_k_norm_f16.hip", True),
+    ("acp_k_norm_bf16.hip", True),
+    ("acp_k_norm_f32.hip", True),
 ]
 
 

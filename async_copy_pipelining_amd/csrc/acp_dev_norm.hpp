@@ -29,10 +29,16 @@
 // (mean, sum of squared deviations) about the first one's mean.
 #pragma once
 
+#include <type_traits>
+
 #include "acp_dev_rows.hpp"
 
 namespace acp {
 namespace dev {
+
+// Kernels are built for one activation and one 8-bit form each: a wave's code
+// has to come into the instruction cache, and for small tensors that is most
+// of its time.
 
 // Where a lane of a workgroup works.
 struct Spot {
@@ -40,7 +46,10 @@ struct Spot {
   uint32_t cl, rl;   // chunk lane and row lane
   uint32_t c;        // first channel
   int valid;         // channels of the chunk; 0 for a lane without one
-  uint32_t r0, rows; // first row and rows of the run
+  // Steps of row_lanes rows are dealt out to the runs in turn, so that all
+  // workgroups together read consecutive rows: row lane rl of the run has the
+  // rows r0 + rl + k step, those below r0 + rows.
+  uint32_t r0, rows, step;
 
   __device__ __forceinline__ Spot(const NormArgs& A, uint32_t wg, int v) {
     const uint32_t q = divide(wg, A.runs);
@@ -52,34 +61,36 @@ struct Spot {
     c = (blk * A.lanes.d + cl) * v;
     valid = 0;
     if (rl < A.row_lanes && c < A.c) valid = A.c - c < static_cast<uint32_t>(v) ? static_cast<int>(A.c - c) : v;
-    r0 = run * A.run_rows;
-    rows = A.rows - r0 < A.run_rows ? A.rows - r0 : A.run_rows;
+    r0 = run * A.row_lanes;
+    step = A.runs.d * A.row_lanes;
+    rows = A.rows > r0 ? A.rows - r0 : 0u;
   }
-  // channels of row step k (row r0 + rl + k * row_lanes): none past the run
+  // channels of row step k: none past the tensor's rows
   __device__ __forceinline__ int channels(const NormArgs& A, uint32_t k) const {
-    return rl + k * A.row_lanes < rows ? valid : 0;
+    return rl + k * step < rows ? valid : 0;
   }
 };
 
 // The lane's chunk of one tensor, row step by row step.  LINEAR: a uniform
-// base and a 32-bit lane offset, one addition a step.
+// address that moves by a uniform step, and a 32-bit lane offset.
 template <bool LINEAR>
 struct Walk {
   const RowTensor* t;
   char* base;
-  uint32_t off, step;  // LINEAR
+  uint32_t off;        // LINEAR
+  int64_t step;
   uint32_t n, row;     // else: sample and the lane's first row
   uint32_t col;        // ... and bytes into the row
 
-  // bytes of a chunk of this tensor, or of its column at hand
   __device__ __forceinline__ Walk(const NormArgs& A, const RowTensor& rt, const Spot& w, uint32_t block_bytes,
                                   uint32_t lane_bytes)
       : t(&rt) {
     if constexpr (LINEAR) {
       base = rt.p + w.n * rt.s[0] + w.r0 * rt.s[2] + block_bytes;
       off = w.rl * static_cast<uint32_t>(rt.s[2]) + lane_bytes;
-      step = A.row_lanes * static_cast<uint32_t>(rt.s[2]);
+      step = w.step * rt.s[2];
     } else {
+      step = w.step;
       n = w.n;
       row = w.r0 + w.rl;
       col = block_bytes + lane_bytes;
@@ -87,9 +98,9 @@ struct Walk {
   }
   __device__ __forceinline__ char* at(const NormArgs& A, uint32_t k) const {
     if constexpr (LINEAR) {
-      return base + (off + k * step);
+      return base + k * step + off;
     } else {
-      const uint32_t r = row + k * A.row_lanes, a = divide(r, A.row2);
+      const uint32_t r = row + k * static_cast<uint32_t>(step), a = divide(r, A.row2);
       return t->p + n * t->s[0] + a * t->s[1] + (r - a * A.row2.d) * t->s[2] + col;
     }
   }
@@ -133,8 +144,8 @@ struct BlockGroups {
   __device__ __forceinline__ BlockGroups(const NormArgs& A, uint32_t blk, uint32_t width) {
     lo = blk * width;
     hi = lo + width < A.c ? lo + width : A.c;
-    g0 = lo / A.per_group;
-    g1 = (hi - 1) / A.per_group;
+    g0 = divide(lo, A.per);
+    g1 = divide(hi - 1, A.per);
   }
 };
 
@@ -199,16 +210,24 @@ struct LaneStats {
   }
 };
 
-// Rows that row lane `rl` has among `rows`.
-__device__ __forceinline__ uint32_t lane_rows(const NormArgs& A, uint32_t rows, uint32_t rl) {
-  return rows > rl ? (rows - rl - 1) / A.row_lanes + 1 : 0u;
-}
+// Rows that each row lane of a run has: `all`, and one more below `more`.
+struct RunRows {
+  uint32_t all, more;
+  __device__ __forceinline__ RunRows(const NormArgs& A, uint32_t rows, uint32_t step) {
+    all = rows / step;
+    more = rows - all * step;
+    more = more < A.row_lanes ? more : A.row_lanes;
+  }
+  __device__ __forceinline__ uint32_t of(uint32_t rl) const { return all + (rl < more ? 1u : 0u); }
+  __device__ __forceinline__ uint32_t total(const NormArgs& A) const { return all * A.row_lanes + more; }
+  __device__ __forceinline__ uint32_t lanes(const NormArgs& A) const { return all ? A.row_lanes : more; }
+};
 
 // Joins the lanes' statistics of group g's piece in this channel block: its
 // mean and squared deviations, in all 2^lg lanes that share the group.
 template <int V, bool WHOLE>
 __device__ __forceinline__ float2 join_lanes(const NormArgs& A, const float2* sh, const BlockGroups& b, uint32_t blk,
-                                             uint32_t g, uint32_t rows, int lg) {
+                                             uint32_t g, const RunRows& rr, int lg) {
   const uint32_t lane = threadIdx.x & ((1u << lg) - 1u);
   const uint32_t width = A.lanes.d * V;
   const uint32_t p0 = g * A.per_group > b.lo ? g * A.per_group : b.lo;
@@ -216,14 +235,14 @@ __device__ __forceinline__ float2 join_lanes(const NormArgs& A, const float2* sh
   const uint32_t cols = WHOLE ? ch / V : ch;               // entries of a row lane
   const uint32_t first = WHOLE ? (p0 - b.lo) / V : p0 - b.lo;
   const uint32_t stride = WHOLE ? A.lanes.d : width;
-  const uint32_t used = rows < A.row_lanes ? rows : A.row_lanes;
+  const uint32_t used = rr.lanes(A);
   const float m0 = sh[first].x;
   float a1 = 0.0f, a2 = 0.0f;
   uint32_t row = lane / cols, col = lane - row * cols;
   const uint32_t drow = (1u << lg) / cols, dcol = (1u << lg) - drow * cols;
   while (row < used) {
     const float2 v = sh[row * stride + first + col];
-    const float n = static_cast<float>(lane_rows(A, rows, row) * (WHOLE ? V : 1));
+    const float n = static_cast<float>(rr.of(row) * (WHOLE ? V : 1));
     const float d = v.x - m0;
     a1 = __builtin_fmaf(n, d, a1);
     a2 += __builtin_fmaf(n * d, d, v.y);
@@ -236,7 +255,7 @@ __device__ __forceinline__ float2 join_lanes(const NormArgs& A, const float2* sh
   }
   a1 = sum_lanes(a1, lg);
   a2 = sum_lanes(a2, lg);
-  const float m = a1 / (static_cast<float>(rows) * static_cast<float>(ch));
+  const float m = a1 / (static_cast<float>(rr.total(A)) * static_cast<float>(ch));
   const float q = __builtin_fmaxf(0.0f, __builtin_fmaf(-a1, m, a2));
   // the maximum drops a NaN: a piece with a NaN or an infinity, or whose
   // squared deviations overflow, keeps a NaN

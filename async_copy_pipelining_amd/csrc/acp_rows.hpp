@@ -46,8 +46,8 @@ struct RowsArgs {
 };
 
 // Group norm.  A workgroup covers `lanes` chunks of a row (channel block
-// blk) and `row_lanes` rows at a time, over one of the runs of `run_rows`
-// rows that a sample's rows are split into.
+// blk) and `row_lanes` rows at a time; such steps are dealt out to the runs
+// that a sample's rows are split into.
 struct NormArgs {
   RowTensor x, y, dy, dx;   // s[0] per sample; row r of a sample at r / row2.d * s[1] + r % row2.d * s[2]
   RowTensor codes, scales;  // the saved form of x, written (forward) or read (backward)
@@ -58,26 +58,34 @@ struct NormArgs {
   float* dgamma;            // [c]
   float* dbeta;
   float* part;              // workspace: partial statistics or partial sums of the parts
-  float* coef;              // workspace: two coefficients for each sample and group
+  float* coef;              // workspace: partial sums of the groups' two coefficients
   uint32_t samples, rows, c, groups, per_group;
   Div row2, lanes, blocks;  // blocks: channel blocks of a row
+  Div per;                  // per_group
   uint32_t row_lanes;
   Div runs;                 // runs of this pass
-  uint32_t run_rows;
-  uint32_t parts, part_rows;  // runs of the pass that left the parts, and their rows
+  uint32_t parts;           // runs of the pass that left the parts
   uint32_t pieces;          // channel blocks that one group may reach into
-  uint32_t main_grid;       // workgroups before those that sum columns
+  uint32_t main_grid;       // workgroups beside those that sum columns
   uint32_t col_rows;        // rows of partial column sums
-  int lb_log2, group_lanes_log2, format, act;
+  int lb_log2, group_lanes_log2;
   float eps;
 };
 
-// How a pass runs, beside its type.
+// What a chunk may hold and how its row is found: channels of one group; whole
+// chunks that groups may divide; anything (rows that end inside a chunk, rows
+// more than one stride apart, or so far that a step passes 31 bits).
+enum NormKind { kNormWhole = 0, kNormSplit = 1, kNormAny = 2 };
+
+enum NormOp { kNormOpRow, kNormOpSlab, kNormOpStats, kNormOpApply,                     // forward
+              kNormOpRowBackward, kNormOpSlabBackward, kNormOpSums, kNormOpDx };       // backward
+
+// The kernel of a pass.
 struct NormShape {
   int dt;
-  bool linear;   // rows one stride apart, a run's bytes within 31 bits
-  bool whole;    // a chunk's channels are of one group
-  bool packed;   // forward: saves x in 8 bits; backward: x is its 8-bit form
+  NormKind kind;
+  int packed;    // 0 none, 1 i8, 2 e4m3: the form of x that is written (forward) or read (backward)
+  int act;
   uint32_t threads;
 };
 
@@ -89,18 +97,15 @@ hipError_t unpack8_launch(int dt, const RowsArgs& a, hipStream_t s);
 hipError_t act_forward_launch(int dt, bool gated, bool save, const RowsArgs& a, hipStream_t s);
 hipError_t act_backward_launch(int dt, bool gated, const RowsArgs& a, hipStream_t s);
 
-// forward: one row a sample; a sample's slab on chip; by parts (two passes)
-hipError_t norm_row_launch(const NormShape& k, const NormArgs& a, hipStream_t s);
-hipError_t norm_slab_launch(const NormShape& k, const NormArgs& a, hipStream_t s);
-hipError_t norm_stats_launch(const NormShape& k, const NormArgs& a, hipStream_t s);
-hipError_t norm_apply_launch(const NormShape& k, const NormArgs& a, hipStream_t s);
-// backward, and the sums of columns that follow
-hipError_t norm_row_backward_launch(const NormShape& k, const NormArgs& a, hipStream_t s);
-hipError_t norm_slab_backward_launch(const NormShape& k, const NormArgs& a, hipStream_t s);
-hipError_t norm_sums_launch(const NormShape& k, const NormArgs& a, hipStream_t s);
-hipError_t norm_coef_launch(const NormArgs& a, hipStream_t s);
-hipError_t norm_dx_launch(const NormShape& k, const NormArgs& a, hipStream_t s);
+// One pass of a group norm: forward, one row a sample; a sample's slab on
+// chip; by parts, the statistics and then the result.  Backward likewise; by
+// parts the sums, and then dx with the sums of columns.
+hipError_t norm_launch(NormOp op, const NormShape& k, const NormArgs& a, hipStream_t s);
+hipError_t norm_launch_f16(NormOp op, const NormShape& k, const NormArgs& a, hipStream_t s);
+hipError_t norm_launch_bf16(NormOp op, const NormShape& k, const NormArgs& a, hipStream_t s);
+hipError_t norm_launch_f32(NormOp op, const NormShape& k, const NormArgs& a, hipStream_t s);
 hipError_t norm_columns_launch(const NormArgs& a, hipStream_t s);
+uint32_t norm_column_grid(const NormArgs& a);  // workgroups that sum columns: 0 if nothing wants them
 
 constexpr int kRowThreads = 256;      // workgroup size, but for small calls and slabs
 constexpr int kRowUnroll = 4;         // chunks a lane has in flight
@@ -108,5 +113,6 @@ constexpr int kSlabRows = 8;          // chunks that a lane of a forward slab ho
 constexpr int kSlabRowsBackward = 4;  // ... of a backward slab
 constexpr int kSlabThreads = 1024;    // largest workgroup of a forward slab
 constexpr int kSlabThreadsBackward = 512;
+constexpr int kRowThreadsBackward = 512;
 
 }  // namespace acp

@@ -342,23 +342,41 @@ acp_status act_backward(acp_activation act, const acp_tile_desc* dx, const acp_t
 // ---------------------------------------------------------------- group norm
 
 // The form that a norm takes (acp_dev_norm.hpp).
-enum NormForm { kNormRow, kNormSlab, kNormParts };
+enum NormForm { kFormRow, kFormSlab, kFormParts };
 
-// Workgroups that the passes over the data aim at, on 256 CUs: the passes
-// that write the result several a CU; those that leave parts fewer, since the
-// next pass reads all parts of a sample (at most kNormMaxRuns of them); the
-// per-row and slab backward passes two and four a CU, since each leaves 8
-// bytes for every channel.
-constexpr int64_t kNormApply = 2048, kNormPartial = 1024, kNormRowBackward = 512, kNormSlabBackward = 1024;
-constexpr int64_t kNormMaxRuns = 256;
+// Workgroups that the passes over the data aim at, on 256 CUs, measured on
+// [128, 500, 1024] float16 (by parts, a training step's three passes together),
+// [16384, 4096] and [8192, 4096] bfloat16 (per row):
+// * by parts, the pass that leaves parts: four a CU (176 us; 181 with two, 182
+//   with eight, whose parts the next pass has to read), at most 256 a sample;
+//   the pass that writes the result: sixteen a CU (176 us; 180 with four);
+// * by parts, tensors that the eight L2s hold together: the same split for
+//   both passes, so that a workgroup of the second finds its data in the L2
+//   that the first brought it to ([4, 64, 64, 320] bfloat16 14.7 us with 512
+//   workgroups in both; 16.3 with 512 and 1024, 21.5 with 1024 and 2048).
+//   Few bytes take few workgroups, and so few parts ([3, 37, 41, 352] float32
+//   backward 17.3 us with 256, 18.1 with 512);
+// * per row: four a CU, forward (50 us; 52 with two, 61 with sixteen); backward
+//   one of 512 lanes a CU (43 us; 45 with two, 50 with one of 256), since each
+//   leaves 8 bytes for every channel;
+// * slab, backward: a workgroup walks samples, since it leaves as much.
+constexpr int64_t kNormPartial = 1024, kNormApply = 4096, kNormMaxRuns = 256;
+constexpr int64_t kNormCached = 512, kNormCachedFew = 256;
+constexpr int64_t kNormCachedBytes = 24 << 20, kNormFewBytes = 8 << 20;
+constexpr int64_t kNormRow = 1024, kNormRowBackward = 256;
+constexpr int64_t kNormSlabBackward = 1024;
+// Lanes of a slab's channel block: 128 bytes of a row, a cache line
+// ([128, 500, 1024] float16 66 us; 79 with 64 bytes, 71 with 256).
+constexpr int64_t kSlabLanes = 8;
 
 struct NormPlan {
-  NormForm form = kNormParts;
+  NormForm form = kFormParts;
   acp::NormArgs A{};
   acp::NormShape K{};
-  acp::Div runs1{}, runs2{};  // by parts: runs of the two passes, and their rows
-  uint32_t rows1 = 0, rows2 = 0;
+  acp::Div runs1{}, runs2{};  // by parts: runs of the two passes
   int64_t workspace = 0, coef_at = 0;
+  int64_t strides[4][3] = {};  // of the tensors, as RowTensor has them
+  std::string text;            // acp_last_kernel's
 };
 
 // ACP_NORM_FORM=slab|parts (measurement aid): slab: not per row; parts: by
@@ -381,14 +399,11 @@ struct NormDims {
   bool backward;
 };
 
-// Splits `rows` into runs of whole steps of row_lanes rows, about `target` of
-// them and at least `least` steps each.
-void split_rows(int64_t rows, int64_t row_lanes, int64_t target, int64_t least, int64_t* runs, int64_t* run_rows) {
-  target = std::max<int64_t>(1, target);
-  int64_t steps = std::max(ceil_div(ceil_div(rows, target), row_lanes), least);
-  steps = std::min(steps, std::max<int64_t>(1, ceil_div(rows, row_lanes)));
-  *run_rows = steps * row_lanes;
-  *runs = std::max<int64_t>(1, ceil_div(rows, *run_rows));
+// About `target` runs for the steps of row_lanes rows that `rows` make, at
+// least `least` steps each.
+int64_t split_rows(int64_t rows, int64_t row_lanes, int64_t target, int64_t least) {
+  const int64_t steps = std::max<int64_t>(1, ceil_div(rows, row_lanes));
+  return std::max<int64_t>(1, std::min(target, steps / least));
 }
 
 // A row's chunks in equal channel blocks of at most 256 lanes, each a whole
@@ -405,31 +420,28 @@ void set_block(acp::NormArgs* A, int64_t lanes, int64_t blocks, int64_t threads)
   A->row_lanes = static_cast<uint32_t>(threads / lanes);
 }
 
-void set_runs(acp::NormArgs* A, int64_t runs, int64_t run_rows) {
-  A->runs = div_by(static_cast<uint64_t>(runs));
-  A->run_rows = static_cast<uint32_t>(run_rows);
-}
 
 // One row a sample, a group in a power of two of a wave's lanes: rows are
 // samples.
 bool plan_row(const NormDims& d, NormPlan* P) {
   const int64_t gl = d.per / d.v;
   if (d.rows != 1 || d.per % d.v || gl > 64 || (gl & (gl - 1))) return false;
-  P->form = kNormRow;
+  P->form = kFormRow;
   acp::NormArgs& A = P->A;
-  int64_t lanes, blocks, runs, run_rows;
+  int64_t lanes, blocks;
   // backward keeps no scale block together: it reads single codes
   split_lanes(d.c / d.v, std::max(gl, d.block && !d.backward ? d.block / d.v : 1), &lanes, &blocks);
-  set_block(&A, lanes, blocks, acp::kRowThreads);
-  const int64_t target = (d.backward ? kNormRowBackward : kNormApply) / blocks;
-  split_rows(d.samples, A.row_lanes, target, 1, &runs, &run_rows);
-  set_runs(&A, runs, run_rows);
+  const int64_t threads = d.backward ? acp::kRowThreadsBackward : acp::kRowThreads;
+  set_block(&A, lanes, blocks, threads);
+  const int64_t target = (d.backward ? kNormRowBackward : kNormRow) / blocks;
+  const int64_t runs = split_rows(d.samples, A.row_lanes, target, 1);
+  A.runs = div_by(static_cast<uint64_t>(runs));
   A.samples = 1;
   A.rows = static_cast<uint32_t>(d.samples);
   A.group_lanes_log2 = log2_of(gl);
   A.main_grid = static_cast<uint32_t>(blocks * runs);
   A.col_rows = static_cast<uint32_t>(runs);
-  P->K.threads = acp::kRowThreads;
+  P->K.threads = static_cast<uint32_t>(threads);
   P->workspace = d.backward ? runs * 2 * d.c * 4 : 0;
   return true;
 }
@@ -451,7 +463,7 @@ bool plan_slab(const NormDims& d, NormPlan* P) {
   auto fits = [&](int64_t lanes, int64_t threads) { return lanes <= threads && U * (threads / lanes) >= d.rows; };
   if (!fits(unit, most)) return false;
   int64_t lanes = unit;
-  while (lanes < cpr && (lanes < 8 || d.rows * lanes < 256) && fits(lanes + unit, most)) lanes += unit;
+  while (lanes < cpr && (lanes < kSlabLanes || d.rows * lanes < 256) && fits(lanes + unit, most)) lanes += unit;
   int64_t blocks = ceil_div(cpr, lanes);
   if (blocks == 1) lanes = ceil_div(cpr, align) * align;
   if (!fits(lanes, most)) return false;
@@ -459,12 +471,15 @@ bool plan_slab(const NormDims& d, NormPlan* P) {
   while (!fits(lanes, threads)) threads *= 2;
   // few workgroups: more lanes with fewer chunks each
   while (threads < most && d.samples * blocks * threads <= 256 * 512 && 2 * (threads / lanes) < d.rows) threads *= 2;
-  P->form = kNormSlab;
+  // backward, a lane's values fill so many registers that a CU holds one
+  // workgroup: past one a CU the two passes by parts are faster
+  if (d.backward && d.samples * blocks * threads > 256 * 512) return false;
+  P->form = kFormSlab;
   acp::NormArgs& A = P->A;
   set_block(&A, lanes, blocks, threads);
   const int64_t runs =
       d.backward ? std::max<int64_t>(1, std::min(d.samples, kNormSlabBackward / blocks)) : 1;
-  set_runs(&A, runs, d.rows);
+  A.runs = div_by(static_cast<uint64_t>(runs));
   A.samples = static_cast<uint32_t>(d.samples);
   A.rows = static_cast<uint32_t>(d.rows);
   A.main_grid = static_cast<uint32_t>(d.backward ? blocks * runs : d.samples * blocks);
@@ -475,30 +490,30 @@ bool plan_slab(const NormDims& d, NormPlan* P) {
 }
 
 void plan_parts(const NormDims& d, NormPlan* P) {
-  P->form = kNormParts;
+  P->form = kFormParts;
   acp::NormArgs& A = P->A;
-  int64_t lanes, blocks, runs, run_rows;
+  int64_t lanes, blocks;
   const int64_t cpr = ceil_div(d.c, d.v);
   split_lanes(cpr, d.block && !d.backward ? d.block / d.v : 1, &lanes, &blocks);
   set_block(&A, lanes, blocks, acp::kRowThreads);
   const int64_t each = std::max<int64_t>(1, d.samples * blocks);
-  split_rows(d.rows, A.row_lanes, std::min(kNormMaxRuns, kNormPartial / each), 2, &runs, &run_rows);
+  const int64_t bytes = d.samples * d.rows * d.c * (16 / d.v);
+  const bool cached = bytes <= kNormCachedBytes;
+  const int64_t both = bytes <= kNormFewBytes ? kNormCachedFew : kNormCached;
+  const int64_t first = cached ? both : kNormPartial, second = cached ? both : kNormApply;
+  const int64_t runs = split_rows(d.rows, A.row_lanes, std::min(kNormMaxRuns, first / each), 2);
   P->runs1 = div_by(static_cast<uint64_t>(runs));
-  P->rows1 = static_cast<uint32_t>(run_rows);
+  P->runs2 = div_by(static_cast<uint64_t>(split_rows(d.rows, A.row_lanes, second / each, 2)));
   A.parts = static_cast<uint32_t>(runs);
-  A.part_rows = static_cast<uint32_t>(run_rows);
-  int64_t runs2;
-  split_rows(d.rows, A.row_lanes, kNormApply / each, 2, &runs2, &run_rows);
-  P->runs2 = div_by(static_cast<uint64_t>(runs2));
-  P->rows2 = static_cast<uint32_t>(run_rows);
   A.samples = static_cast<uint32_t>(d.samples);
   A.rows = static_cast<uint32_t>(d.rows);
   const int64_t width = lanes * d.v;
   A.pieces = static_cast<uint32_t>(std::min(blocks, (d.per + width - 2) / width + 1));
-  A.col_rows = static_cast<uint32_t>(d.samples);
+  A.col_rows = static_cast<uint32_t>(d.samples * runs);
   P->K.threads = acp::kRowThreads;
+  const int64_t group_parts = d.samples * d.groups * runs * A.pieces * 8;
   P->coef_at = align_up(d.samples * runs * 2 * d.c * 4, 16);
-  P->workspace = d.backward ? P->coef_at + d.samples * d.groups * 8 : d.samples * d.groups * runs * A.pieces * 8;
+  P->workspace = d.backward ? P->coef_at + group_parts : group_parts;
 }
 
 acp_status norm_dims(const acp::DescData& t, int groups, int block, bool backward, NormDims* d) {
@@ -521,66 +536,114 @@ acp_status norm_dims(const acp::DescData& t, int groups, int block, bool backwar
   return ACP_OK;
 }
 
-// Whether the rows of a run of every tensor lie one stride apart, within the
-// 31 bits that the kernels' lane offsets take.
-bool norm_linear(const Collapsed& o, int nt, const NormDims& d, const NormPlan& P, int64_t run_rows, bool by_sample,
+// Whether the rows of every tensor lie one stride apart, with the lanes of a
+// step within the 31 bits of an offset.
+bool norm_linear(const Collapsed& o, int nt, const NormDims& d, const NormPlan& P, bool by_sample,
                  const acp::DescData* const* t) {
-  const int64_t reach = run_rows + 3 * int64_t(2) * acp::kRowUnroll * P.A.row_lanes;
-  auto in = [&](int64_t stride) { return reach * stride + 16 * P.A.lanes.d < (int64_t(1) << 31); };
+  auto in = [&](int64_t stride) { return P.A.row_lanes * stride + 16 * P.A.lanes.d < (int64_t(1) << 31); };
   if (!by_sample && o.n > 1) return false;
-  for (int k = 0; k < nt; ++k) {
-    const int64_t stride = by_sample ? t[k]->strides[0] * t[k]->esize : (o.n ? o.stride[k][0] : 0);
-    if (!in(stride)) return false;
-  }
+  for (int k = 0; k < nt; ++k)
+    if (!in(by_sample ? t[k]->strides[0] * t[k]->esize : (o.n ? o.stride[k][0] : 0))) return false;
   return !d.block || in(ceil_div(d.c, d.block) * 4);
 }
 
-// The form, split and tensors of a norm over `t` (of one shape).  `scales`:
-// of the 8-bit form, or nullptr.
-acp_status norm_plan(const acp::DescData* const* t, acp::RowTensor* const* rt, int nt, const NormDims& d,
-                     float* scales, NormPlan* out) {
+// Rows of a descriptor: what a plan depends on, without its address.
+struct NormKey {
+  int64_t v[16 + 4 * (2 * acp::kMaxInputRank)];
+  int n = 0;
+  void add(int64_t x) { v[n++] = x; }
+  bool operator==(const NormKey& o) const { return n == o.n && std::memcmp(v, o.v, sizeof(int64_t) * n) == 0; }
+};
+
+std::string norm_text(const NormDims& d, const NormPlan& P) {
+  static const char* const forms[] = {" per row", " slab", " by parts"};
+  static const char* const kinds[] = {" whole", " split", " any"};
+  return std::string(d.backward ? "group norm backward" : "group norm") +
+         (d.block ? (d.backward ? " from 8 bits" : " saved") : "") + forms[P.form] + kinds[P.K.kind] + " threads " +
+         std::to_string(P.K.threads) + " lanes " + std::to_string(P.A.lanes.d) + "x" + std::to_string(P.A.row_lanes) +
+         " blocks " + std::to_string(P.A.blocks.d) + " runs " +
+         std::to_string(P.form == kFormParts ? P.runs1.d : P.A.runs.d) +
+         (P.form == kFormParts ? "+" + std::to_string(P.runs2.d) : std::string());
+}
+
+// The form, split and strides of a norm over `t` (of one shape).
+acp_status norm_geometry(const acp::DescData* const* t, int nt, const NormDims& d, NormPlan* out) {
   Collapsed o;
   if (!collapse(t, nt, 1, 2, &o))
     return ret(ACP_ERR_UNSUPPORTED, "the inner row dims of these strides do not join into two");
-  // the tensors' pointers are members of *out: the plan is made beside them
   NormPlan P;
   const int env = norm_form_env();
-  bool done = env < 1 && plan_row(d, &P) && norm_linear(o, nt, d, P, P.A.run_rows, true, t);
+  bool done = env < 1 && plan_row(d, &P) && norm_linear(o, nt, d, P, true, t);
   if (!done) P = NormPlan();
-  if (!done && env < 2) done = plan_slab(d, &P) && norm_linear(o, nt, d, P, P.A.run_rows, false, t);
+  if (!done && env < 2) done = plan_slab(d, &P) && norm_linear(o, nt, d, P, false, t);
   if (!done) {
     P = NormPlan();
     plan_parts(d, &P);
   }
-  const bool row = P.form == kNormRow;
+  const bool row = P.form == kFormRow;
   acp::NormArgs& A = P.A;
-  P.K.linear = P.form != kNormParts || norm_linear(o, nt, d, P, std::max(P.rows1, P.rows2), false, t);
-  P.K.whole = d.per % d.v == 0;
-  P.K.packed = d.block != 0;
+  const bool linear = P.form != kFormParts || norm_linear(o, nt, d, P, false, t);
+  P.K.kind = !linear || d.c % d.v ? acp::kNormAny : d.per % d.v ? acp::kNormSplit : acp::kNormWhole;
   P.K.dt = row_dtype(t[0]->dtype);
   A.c = static_cast<uint32_t>(d.c);
   A.groups = static_cast<uint32_t>(d.groups);
   A.per_group = static_cast<uint32_t>(d.per);
+  A.per = div_by(static_cast<uint64_t>(d.per));
   A.lb_log2 = d.block ? log2_of(d.block / d.v) : 0;
   A.row2 = div_by(static_cast<uint64_t>(row ? std::max<int64_t>(1, d.samples) : (o.n >= 1 ? o.ext[o.n - 1] : 1)));
   const int64_t scale_row = d.block ? ceil_div(d.c, d.block) * 4 : 0;
-  A.scales.p = reinterpret_cast<char*>(scales);
   A.scales.s[0] = row ? 0 : scale_row * d.rows;
   A.scales.s[1] = row ? 0 : scale_row * A.row2.d;
   A.scales.s[2] = scale_row;
-  acp::RowTensor v[4];
   for (int k = 0; k < nt; ++k) {
-    v[k].p = reinterpret_cast<char*>(t[k]->gbase);
     const int64_t sample = t[k]->strides[0] * t[k]->esize;
-    v[k].s[0] = row ? 0 : sample;
-    v[k].s[1] = !row && o.n >= 2 ? o.stride[k][0] : 0;
-    v[k].s[2] = row ? sample : (o.n >= 1 ? o.stride[k][o.n - 1] : 0);
+    P.strides[k][0] = row ? 0 : sample;
+    P.strides[k][1] = !row && o.n >= 2 ? o.stride[k][0] : 0;
+    P.strides[k][2] = row ? sample : (o.n >= 1 ? o.stride[k][o.n - 1] : 0);
   }
   if (static_cast<int64_t>(A.samples) * A.blocks.d * std::max({A.runs.d, P.runs1.d, P.runs2.d}) + d.c / 16 + 1 >= kRowLimit)
     return ret(ACP_ERR_UNSUPPORTED, "more than 2^31 workgroups");
+  P.text = norm_text(d, P);
   *out = P;
-  for (int k = 0; k < nt; ++k) *rt[k] = v[k];
   return ACP_OK;
+}
+
+// The plan of a norm over `t`, with the tensors' addresses in their places.
+// Each thread keeps the plans of its last few geometries (shapes, strides and
+// types; no addresses): planning costs as much as a launch.
+acp_status norm_plan(const acp::DescData* const* t, int nt, const NormDims& d, NormPlan* out) {
+  NormKey key;
+  for (int64_t x : {int64_t(t[0]->dtype), int64_t(t[0]->rank), d.groups, d.block, int64_t(d.backward), int64_t(nt)})
+    key.add(x);
+  for (int k = 0; k < t[0]->rank; ++k) key.add(t[0]->shape[k]);
+  for (int k = 0; k < nt; ++k) {
+    key.add(t[k]->esize);
+    for (int e = 0; e < t[k]->rank; ++e) key.add(t[k]->strides[e]);
+  }
+  struct Entry {
+    NormKey key;
+    NormPlan plan;
+  };
+  constexpr int kEntries = 16;
+  thread_local Entry entries[kEntries];
+  thread_local int next = 0;
+  for (const Entry& e : entries)
+    if (e.key == key) {
+      *out = e.plan;
+      return ACP_OK;
+    }
+  const acp_status st = norm_geometry(t, nt, d, out);
+  if (st != ACP_OK) return st;
+  Entry& e = entries[next];
+  next = (next + 1) % kEntries;
+  e.key = key;
+  e.plan = *out;
+  return ACP_OK;
+}
+
+void set_tensor(const NormPlan& P, int k, const acp::DescData& d, acp::RowTensor* t) {
+  t->p = reinterpret_cast<char*>(d.gbase);
+  for (int e = 0; e < 3; ++e) t->s[e] = P.strides[k][e];
 }
 
 bool misaligned4(const void* p) { return reinterpret_cast<uint64_t>(p) % 4 != 0; }
@@ -591,15 +654,6 @@ acp_status check_workspace(const void* workspace, int64_t bytes, int64_t need) {
     return ret(ACP_ERR_INVALID, "the workspace is smaller than acp_group_norm_workspace says");
   if (reinterpret_cast<uint64_t>(workspace) % 16) return ret(ACP_ERR_INVALID, "the workspace is not 16-byte aligned");
   return ACP_OK;
-}
-
-std::string norm_text(const char* what, const NormPlan& P) {
-  static const char* const forms[] = {" per row", " slab", " by parts"};
-  return std::string(what) + forms[P.form] + (P.K.whole ? " whole" : " split") + (P.K.linear ? "" : " strided") +
-         " threads " + std::to_string(P.K.threads) + " lanes " + std::to_string(P.A.lanes.d) + "x" +
-         std::to_string(P.A.row_lanes) + " blocks " + std::to_string(P.A.blocks.d) + " runs " +
-         std::to_string(P.form == kNormParts ? P.runs1.d : P.A.runs.d) +
-         (P.form == kNormParts ? "+" + std::to_string(P.runs2.d) : std::string());
 }
 
 acp_status group_norm_workspace(const acp_tile_desc* x, int groups, int64_t* bytes) {
@@ -642,8 +696,13 @@ acp_status group_norm(const acp_tile_desc* y, const acp_tile_desc* x, const floa
   NormPlan P;
   acp::NormArgs& A = P.A;
   const acp::DescData* t[] = {&xd, &yd, &cd};
-  acp::RowTensor* rt[] = {&A.x, &A.y, &A.codes};
-  if ((st = norm_plan(t, rt, save ? 3 : 2, d, save ? save->scales : nullptr, &P)) != ACP_OK) return st;
+  if ((st = norm_plan(t, save ? 3 : 2, d, &P)) != ACP_OK) return st;
+  set_tensor(P, 0, xd, &A.x);
+  set_tensor(P, 1, yd, &A.y);
+  if (save) {
+    set_tensor(P, 2, cd, &A.codes);
+    A.scales.p = reinterpret_cast<char*>(save->scales);
+  }
   if ((st = check_workspace(workspace, workspace_bytes, P.workspace)) != ACP_OK) return st;
   if (self_overlap(yd) || (save && self_overlap(cd))) return ret(ACP_ERR_INVALID, "an output overlaps itself");
   const int64_t stat = d.samples * groups * 4;
@@ -658,29 +717,27 @@ acp_status group_norm(const acp_tile_desc* y, const acp_tile_desc* x, const floa
   if ((st = check_ranges(w, nw, r, 3)) != ACP_OK) return st;
   if (elements(xd) == 0) return launched_nothing();
   if ((st = check_stream(stream)) != ACP_OK) return st;
-  A.format = save ? save->format : 0;
+  P.K.packed = save ? 1 + save->format : 0;
+  P.K.act = act;
   A.gamma = gamma;
   A.beta = beta;
   A.mean = mean;
   A.rstd = rstd;
   A.part = static_cast<float*>(workspace);
-  A.act = act;
   A.eps = eps;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = hipSuccess;
-  if (P.form == kNormRow) e = acp::norm_row_launch(P.K, A, s);
-  if (P.form == kNormSlab) e = acp::norm_slab_launch(P.K, A, s);
-  if (P.form == kNormParts) {
+  if (P.form == kFormRow) e = acp::norm_launch(acp::kNormOpRow, P.K, A, s);
+  if (P.form == kFormSlab) e = acp::norm_launch(acp::kNormOpSlab, P.K, A, s);
+  if (P.form == kFormParts) {
     A.runs = P.runs1;
-    A.run_rows = P.rows1;
     A.main_grid = A.samples * A.blocks.d * A.runs.d;
-    e = acp::norm_stats_launch(P.K, A, s);
+    e = acp::norm_launch(acp::kNormOpStats, P.K, A, s);
     A.runs = P.runs2;
-    A.run_rows = P.rows2;
     A.main_grid = A.samples * A.blocks.d * A.runs.d;
-    if (e == hipSuccess) e = acp::norm_apply_launch(P.K, A, s);
+    if (e == hipSuccess) e = acp::norm_launch(acp::kNormOpApply, P.K, A, s);
   }
-  return launched(e, norm_text(save ? "group norm saved" : "group norm", P));
+  return launched(e, P.text);
 }
 
 acp_status group_norm_backward(const acp_tile_desc* dx, float* dgamma, float* dbeta, const acp_tile_desc* dy,
@@ -706,8 +763,11 @@ acp_status group_norm_backward(const acp_tile_desc* dx, float* dgamma, float* db
   NormPlan P;
   acp::NormArgs& A = P.A;
   const acp::DescData* t[] = {&dyd, &dxd, x ? &xd : &cd};
-  acp::RowTensor* rt[] = {&A.dy, &A.dx, x ? &A.x : &A.codes};
-  if ((st = norm_plan(t, rt, 3, d, saved ? saved->scales : nullptr, &P)) != ACP_OK) return st;
+  if ((st = norm_plan(t, 3, d, &P)) != ACP_OK) return st;
+  set_tensor(P, 0, dyd, &A.dy);
+  set_tensor(P, 1, dxd, &A.dx);
+  set_tensor(P, 2, *t[2], x ? &A.x : &A.codes);
+  if (saved) A.scales.p = reinterpret_cast<char*>(saved->scales);
   if ((st = check_workspace(workspace, workspace_bytes, P.workspace)) != ACP_OK) return st;
   if (self_overlap(dxd)) return ret(ACP_ERR_INVALID, "an output overlaps itself");
   const int64_t stat = d.samples * groups * 4;
@@ -722,7 +782,8 @@ acp_status group_norm_backward(const acp_tile_desc* dx, float* dgamma, float* db
     r[nr++] = range_of(saved->scales, scale_bytes(cd, saved->block), "the scales");
   }
   if ((st = check_ranges(w, 4, r, nr)) != ACP_OK) return st;
-  A.format = saved ? saved->format : 0;
+  P.K.packed = saved ? 1 + saved->format : 0;
+  P.K.act = act;
   A.gamma = gamma;
   A.beta = beta;
   A.mean = const_cast<float*>(mean);
@@ -731,7 +792,6 @@ acp_status group_norm_backward(const acp_tile_desc* dx, float* dgamma, float* db
   A.dbeta = dbeta;
   A.part = static_cast<float*>(workspace);
   A.coef = reinterpret_cast<float*>(static_cast<char*>(workspace) + P.coef_at);
-  A.act = act;
   if ((st = check_stream(stream)) != ACP_OK) return st;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = hipSuccess;
@@ -740,22 +800,19 @@ acp_status group_norm_backward(const acp_tile_desc* dx, float* dgamma, float* db
     if (!dgamma && !dbeta) return launched_nothing();
     return launched(acp::norm_columns_launch(A, s), "group norm backward of no samples");
   }
-  if (P.form == kNormRow) e = acp::norm_row_backward_launch(P.K, A, s);
-  if (P.form == kNormSlab) e = acp::norm_slab_backward_launch(P.K, A, s);
-  if (P.form == kNormParts) {
+  if (P.form == kFormRow) e = acp::norm_launch(acp::kNormOpRowBackward, P.K, A, s);
+  if (P.form == kFormSlab) e = acp::norm_launch(acp::kNormOpSlabBackward, P.K, A, s);
+  if (P.form == kFormParts) {
     A.runs = P.runs1;
-    A.run_rows = P.rows1;
     A.main_grid = A.samples * A.blocks.d * A.runs.d;
-    e = acp::norm_sums_launch(P.K, A, s);
-    if (e == hipSuccess) e = acp::norm_coef_launch(A, s);
+    e = acp::norm_launch(acp::kNormOpSums, P.K, A, s);
     A.runs = P.runs2;
-    A.run_rows = P.rows2;
     A.main_grid = A.samples * A.blocks.d * A.runs.d;
-    if (e == hipSuccess) e = acp::norm_dx_launch(P.K, A, s);
+    if (e == hipSuccess) e = acp::norm_launch(acp::kNormOpDx, P.K, A, s);
   } else if (P.workspace > 0 && e == hipSuccess) {
     e = acp::norm_columns_launch(A, s);
   }
-  return launched(e, norm_text(saved ? "group norm backward from 8 bits" : "group norm backward", P));
+  return launched(e, P.text);
 }
 
 // Nothing throws across the ABI.
