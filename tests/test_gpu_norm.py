@@ -151,8 +151,19 @@ ROW_SHAPES = [
 ]
 
 
+# more rows than a workgroup holds: whole, split and cut chunks, groups that
+# reach over several channel blocks, and more samples than slabs are taken for
+PART_SHAPES = [
+    ((1, 9000, 16), 1), ((2, 5000, 40), 4), ((1, 3000, 33), 3), ((3, 1300, 264), 3), ((2, 600, 4100), 2),
+    ((1, 700, 4096), 1), ((700, 33, 64), 8), ((1, 40, 50, 5, 24), 3),
+]
+# one row a sample, groups that no power of two of lanes holds, and the
+# widest slabs
+WIDE_SHAPES = [((2, 2, 4096), 1), ((3, 1, 2040), 1), ((2, 3, 1536), 1), ((5, 1, 3000), 3), ((2, 2048), 2048)]
+
+
 @pytest.mark.parametrize("dtype", list(DTYPES))
-@pytest.mark.parametrize("shape, groups", SHAPES + ROW_SHAPES)
+@pytest.mark.parametrize("shape, groups", SHAPES + ROW_SHAPES + PART_SHAPES + WIDE_SHAPES)
 def test_forward_and_backward(shape, groups, dtype):
     name = ("none", "silu", "gelu")[(len(shape) + groups + shape[0]) % 3]
     Case(shape, groups, dtype, name, seed=groups).run()
@@ -165,6 +176,29 @@ def test_saved_in_8_bits(dtype, fmt, block):
                                          ((5, 64), 8), ((33, 512), 8), ((3, 4096), 64), ((4, 8192), 8),
                                          ((2, 4104), 9), ((1, 6, 4100), 2), ((2, 40, 320), 32)]):
         Case(shape, groups, dtype, ("silu", "gelu", "none")[k % 3], seed=k, fmt=fmt, block=block).run()
+
+
+def test_saved_by_parts():
+    for k, (shape, groups) in enumerate(PART_SHAPES):
+        fmt, block = ("i8", "e4m3")[k % 2], (32, 64, 128, 256)[k % 4]
+        f, _ = Case(shape, groups, ("f16", "bf16", "f32")[k % 3], ("silu", "gelu")[k % 2], seed=k, fmt=fmt,
+                    block=block).run()
+        assert "by parts" in f or shape[0] > 100
+
+
+def test_forms_and_kinds_are_the_ones_meant():
+    """Which form a norm takes is said by acp_last_kernel."""
+    for shape, groups, dtype, fwd, bwd in (
+            ((64, 1024), 16, "f16", "per row whole", "per row whole"),
+            ((3, 100, 64), 8, "f16", "slab whole", "slab whole"),
+            ((3, 100, 40), 4, "bf16", "slab split", "slab split"),
+            ((2, 20, 33), 3, "f32", "slab any", "slab any"),
+            ((1, 9000, 16), 1, "f16", "by parts whole", "by parts whole"),
+            ((2, 5000, 40), 4, "f16", "by parts split", "by parts split"),
+            ((1, 3000, 33), 3, "f16", "by parts any", "by parts any"),
+            ((700, 33, 64), 8, "f16", "slab whole", "by parts whole")):
+        f, b = Case(shape, groups, dtype, "silu").run()
+        assert fwd in f and bwd in b, (f, b)
 
 
 @pytest.mark.parametrize("name", ["none", "silu", "gelu"])
@@ -181,7 +215,15 @@ def test_rows_of_a_cropped_map():
     whole = torch.randn(2, 9, 11, 16, device=DEV).to(torch.bfloat16)
     view = whole[:, 2:8, 3:10, :]
     c.x.t, c.x.desc = view, acp.acp_encode_tiled("bf16", view, view.shape, view.stride(), (1,) * 4)
-    c.run("cropped")
+    f, b = c.run("cropped")
+    assert "by parts any" in f and "by parts any" in b
+    # the same for a gradient that is a window, with the saved form of x
+    c = Case((3, 40, 9, 64), 4, "f16", "gelu", fmt="i8")
+    wide = torch.randn(3, 42, 12, 64, device=DEV).to(torch.float16)
+    view = wide[:, 1:41, 2:11, :]
+    c.dy.t, c.dy.desc = view, acp.acp_encode_tiled("f16", view, view.shape, view.stride(), (1,) * 4)
+    f, b = c.run("cropped dy")
+    assert "slab" in f and "by parts any" in b
 
 
 def test_without_parameters_or_statistics():
