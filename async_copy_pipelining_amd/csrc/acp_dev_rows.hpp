@@ -336,7 +336,7 @@ __device__ __forceinline__ float sigmoid(float u) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u * -1.44269504088896341f));
 }
 
-// e^(-u^2 / 2), and the normal distribution function from it:
+// e^(-u^2 / 2), and the normal distribution's tail from it:
 // 1 - Phi(|u|) = e^(-u^2 / 2) (a1 t + ... + a5 t^5) / 2 with
 // t = 1 / (1 + p |u| / sqrt 2), formula 7.1.26 of Abramowitz and Stegun's
 // Handbook of Mathematical Functions, whose erf is off by at most 1.5e-7.
@@ -346,21 +346,26 @@ __device__ __forceinline__ float normal_bell(float u) {
   return __builtin_amdgcn_exp2f(u * u * -0.721347520444481704f);
 }
 
-__device__ __forceinline__ float normal_cdf(float u, float bell) {
+// 1 - Phi(|u|)
+__device__ __forceinline__ float normal_tail(float u, float bell) {
   const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(__builtin_fabsf(u), 0.3275911f * 0.707106781186547524f, 1.0f));
   float q = __builtin_fmaf(t, 1.061405429f * 0.5f, -1.453152027f * 0.5f);
   q = __builtin_fmaf(t, q, 1.421413741f * 0.5f);
   q = __builtin_fmaf(t, q, -0.284496736f * 0.5f);
   q = __builtin_fmaf(t, q, 0.254829592f * 0.5f);
-  q *= t * bell;
-  return u < 0.0f ? q : 1.0f - q;
+  return q * (t * bell);
+}
+
+// u Phi(u) = max(u, 0) - |u| (1 - Phi(|u|))
+__device__ __forceinline__ float gelu(float u, float tail) {
+  return __builtin_fmaf(-__builtin_fabsf(u), tail, __builtin_fmaxf(u, 0.0f));
 }
 
 // act(u)
 template <int ACT>
 __device__ __forceinline__ float act_value(float u) {
   if constexpr (ACT == kActSilu) return u * sigmoid(u);
-  if constexpr (ACT == kActGelu) return u * normal_cdf(u, normal_bell(u));
+  if constexpr (ACT == kActGelu) return gelu(u, normal_tail(u, normal_bell(u)));
   return u;
 }
 
@@ -372,9 +377,9 @@ __device__ __forceinline__ void act_both(float u, float* value, float* slope) {
     *value = u * s;
     *slope = s * (1.0f + u * (1.0f - s));
   } else if constexpr (ACT == kActGelu) {
-    const float bell = normal_bell(u), p = normal_cdf(u, bell);
-    *value = u * p;
-    *slope = __builtin_fmaf(u * 0.398942280401432678f, bell, p);
+    const float bell = normal_bell(u), tail = normal_tail(u, bell);
+    *value = gelu(u, tail);
+    *slope = __builtin_fmaf(u * 0.398942280401432678f, bell, u < 0.0f ? tail : 1.0f - tail);
   } else {
     *value = u;
     *slope = 1.0f;
