@@ -233,28 +233,52 @@ def acp_stream_binary(op, out: acp_tile_desc, x: acp_tile_desc, z: acp_tile_desc
                                   int(threads), int(workgroups), stg, _stream(stream)))
 
 
-# The row operators take descriptors and packed forms as they are: ctypes
-# passes a structure by reference where a pointer is declared.
+# The row operators' smallest calls last as long as their marshalling, so it is
+# kept short: ctypes passes a structure by reference where a pointer is
+# declared, addresses and streams are asked for directly, and a status is
+# looked at only when it is not ACP_OK.
+def _addr(x) -> int | None:
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        return x if x is None else int(x)
+
+
+def _handle(s) -> int | None:
+    try:
+        return s.cuda_stream
+    except AttributeError:
+        return s if s is None else int(s)
+
+
 def _act(act) -> int:
     return ACTIVATIONS[act] if isinstance(act, str) else int(act)
 
 
 def acp_pack8(out: acp_packed8, x: acp_tile_desc, stream=None) -> None:
-    _check(_lib.acp_pack8(out, x, _stream(stream)))
+    st = _lib.acp_pack8(out, x, _handle(stream))
+    if st:
+        _check(st)
 
 
 def acp_unpack8(out: acp_tile_desc, src: acp_packed8, stream=None) -> None:
-    _check(_lib.acp_unpack8(out, src, _stream(stream)))
+    st = _lib.acp_unpack8(out, src, _handle(stream))
+    if st:
+        _check(st)
 
 
 def acp_act_forward(act, out: acp_tile_desc, x: acp_tile_desc, z: acp_tile_desc | None = None,
                     save_x: acp_packed8 | None = None, save_z: acp_packed8 | None = None, stream=None) -> None:
-    _check(_lib.acp_act_forward(_act(act), out, x, z, save_x, save_z, _stream(stream)))
+    st = _lib.acp_act_forward(_act(act), out, x, z, save_x, save_z, _handle(stream))
+    if st:
+        _check(st)
 
 
 def acp_act_backward(act, dx: acp_tile_desc, dz: acp_tile_desc | None, dy: acp_tile_desc, x: acp_packed8,
                      z: acp_packed8 | None = None, stream=None) -> None:
-    _check(_lib.acp_act_backward(_act(act), dx, dz, dy, x, z, _stream(stream)))
+    st = _lib.acp_act_backward(_act(act), dx, dz, dy, x, z, _handle(stream))
+    if st:
+        _check(st)
 
 
 def acp_group_norm_workspace(x: acp_tile_desc, groups: int) -> int:
@@ -266,17 +290,21 @@ def acp_group_norm_workspace(x: acp_tile_desc, groups: int) -> int:
 def acp_group_norm(y: acp_tile_desc, x: acp_tile_desc, gamma, beta, groups: int, eps: float, act="none", mean=None,
                    rstd=None, save: acp_packed8 | None = None, workspace=None, workspace_bytes: int = 0,
                    stream=None) -> None:
-    _check(_lib.acp_group_norm(y, x, _ptr(gamma), _ptr(beta), groups, eps, _act(act), _ptr(mean), _ptr(rstd), save,
-                               _ptr(workspace), workspace_bytes, _stream(stream)))
+    st = _lib.acp_group_norm(y, x, _addr(gamma), _addr(beta), groups, eps, _act(act), _addr(mean), _addr(rstd), save,
+                             _addr(workspace), workspace_bytes, _handle(stream))
+    if st:
+        _check(st)
 
 
 def acp_group_norm_backward(dx: acp_tile_desc, dgamma, dbeta, dy: acp_tile_desc, x: acp_tile_desc | acp_packed8,
                             mean, rstd, gamma, beta, groups: int, act="none", workspace=None,
                             workspace_bytes: int = 0, stream=None) -> None:
     plain, saved = (None, x) if isinstance(x, acp_packed8) else (x, None)
-    _check(_lib.acp_group_norm_backward(dx, _ptr(dgamma), _ptr(dbeta), dy, plain, saved, _ptr(mean), _ptr(rstd),
-                                        _ptr(gamma), _ptr(beta), groups, _act(act), _ptr(workspace), workspace_bytes,
-                                        _stream(stream)))
+    st = _lib.acp_group_norm_backward(dx, _addr(dgamma), _addr(dbeta), dy, plain, saved, _addr(mean), _addr(rstd),
+                                      _addr(gamma), _addr(beta), groups, _act(act), _addr(workspace),
+                                      workspace_bytes, _handle(stream))
+    if st:
+        _check(st)
 
 
 def acp_debug_lds_image(src: acp_tile_desc, tile_index: int, threads: int, out_bytes, stream=None) -> None:

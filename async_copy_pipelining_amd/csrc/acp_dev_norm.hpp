@@ -51,7 +51,7 @@ struct Spot {
   // rows r0 + rl + k step, those below r0 + rows.
   uint32_t r0, rows, step;
 
-  __device__ __forceinline__ Spot(const NormArgs& A, uint32_t wg, int v) {
+  __device__ __forceinline__ Spot(const NormCore& A, uint32_t wg, int v) {
     const uint32_t q = divide(wg, A.runs);
     run = wg - q * A.runs.d;
     n = divide(q, A.blocks);
@@ -66,7 +66,7 @@ struct Spot {
     rows = A.rows > r0 ? A.rows - r0 : 0u;
   }
   // channels of row step k: none past the tensor's rows
-  __device__ __forceinline__ int channels(const NormArgs& A, uint32_t k) const {
+  __device__ __forceinline__ int channels(const NormCore& A, uint32_t k) const {
     return rl + k * step < rows ? valid : 0;
   }
 };
@@ -82,7 +82,7 @@ struct Walk {
   uint32_t n, row;     // else: sample and the lane's first row
   uint32_t col;        // ... and bytes into the row
 
-  __device__ __forceinline__ Walk(const NormArgs& A, const RowTensor& rt, const Spot& w, uint32_t block_bytes,
+  __device__ __forceinline__ Walk(const NormCore& A, const RowTensor& rt, const Spot& w, uint32_t block_bytes,
                                   uint32_t lane_bytes)
       : t(&rt) {
     if constexpr (LINEAR) {
@@ -96,7 +96,7 @@ struct Walk {
       col = block_bytes + lane_bytes;
     }
   }
-  __device__ __forceinline__ char* at(const NormArgs& A, uint32_t k) const {
+  __device__ __forceinline__ char* at(const NormCore& A, uint32_t k) const {
     if constexpr (LINEAR) {
       return base + k * step + off;
     } else {
@@ -107,19 +107,19 @@ struct Walk {
 };
 
 template <class T, bool LINEAR>
-__device__ __forceinline__ Walk<LINEAR> walk(const NormArgs& A, const RowTensor& t, const Spot& w) {
+__device__ __forceinline__ Walk<LINEAR> walk(const NormCore& A, const RowTensor& t, const Spot& w) {
   return Walk<LINEAR>(A, t, w, w.blk * A.lanes.d * 16u, w.cl * 16u);
 }
 // the saved form's codes (V bytes a chunk) and scales (one for 2^lb_log2 chunks)
 template <int V, bool LINEAR>
-__device__ __forceinline__ Walk<LINEAR> walk_codes(const NormArgs& A, const Spot& w) {
-  return Walk<LINEAR>(A, A.codes, w, w.blk * A.lanes.d * V, w.cl * V);
+__device__ __forceinline__ Walk<LINEAR> walk_codes(const NormCore& A, const RowTensor& t, const Spot& w) {
+  return Walk<LINEAR>(A, t, w, w.blk * A.lanes.d * V, w.cl * V);
 }
 template <bool LINEAR>
-__device__ __forceinline__ Walk<LINEAR> walk_scales(const NormArgs& A, const Spot& w) {
+__device__ __forceinline__ Walk<LINEAR> walk_scales(const NormCore& A, const RowTensor& t, const Spot& w) {
   // a channel block that starts inside a scale block: both terms are of the whole row
   const uint32_t first = w.blk * A.lanes.d;
-  return Walk<LINEAR>(A, A.scales, w, (first >> A.lb_log2) * 4u,
+  return Walk<LINEAR>(A, t, w, (first >> A.lb_log2) * 4u,
                       (((first + w.cl) >> A.lb_log2) - (first >> A.lb_log2)) * 4u);
 }
 
@@ -141,7 +141,7 @@ __device__ __forceinline__ int join_log2(uint32_t groups, uint32_t threads) {
 // The groups that a channel block touches.
 struct BlockGroups {
   uint32_t lo, hi, g0, g1;  // channels [lo, hi), groups g0..g1
-  __device__ __forceinline__ BlockGroups(const NormArgs& A, uint32_t blk, uint32_t width) {
+  __device__ __forceinline__ BlockGroups(const NormCore& A, uint32_t blk, uint32_t width) {
     lo = blk * width;
     hi = lo + width < A.c ? lo + width : A.c;
     g0 = divide(lo, A.per);
@@ -150,7 +150,7 @@ struct BlockGroups {
 };
 
 // Channels of group g that lie in channel block blk.
-__device__ __forceinline__ uint32_t piece_channels(const NormArgs& A, uint32_t g, uint32_t blk, uint32_t width) {
+__device__ __forceinline__ uint32_t piece_channels(const NormCore& A, uint32_t g, uint32_t blk, uint32_t width) {
   const uint32_t lo = g * A.per_group > blk * width ? g * A.per_group : blk * width;
   uint32_t hi = (g + 1) * A.per_group < (blk + 1) * width ? (g + 1) * A.per_group : (blk + 1) * width;
   hi = hi < A.c ? hi : A.c;
@@ -213,20 +213,20 @@ struct LaneStats {
 // Rows that each row lane of a run has: `all`, and one more below `more`.
 struct RunRows {
   uint32_t all, more;
-  __device__ __forceinline__ RunRows(const NormArgs& A, uint32_t rows, uint32_t step) {
+  __device__ __forceinline__ RunRows(const NormCore& A, uint32_t rows, uint32_t step) {
     all = rows / step;
     more = rows - all * step;
     more = more < A.row_lanes ? more : A.row_lanes;
   }
   __device__ __forceinline__ uint32_t of(uint32_t rl) const { return all + (rl < more ? 1u : 0u); }
-  __device__ __forceinline__ uint32_t total(const NormArgs& A) const { return all * A.row_lanes + more; }
-  __device__ __forceinline__ uint32_t lanes(const NormArgs& A) const { return all ? A.row_lanes : more; }
+  __device__ __forceinline__ uint32_t total(const NormCore& A) const { return all * A.row_lanes + more; }
+  __device__ __forceinline__ uint32_t lanes(const NormCore& A) const { return all ? A.row_lanes : more; }
 };
 
 // Joins the lanes' statistics of group g's piece in this channel block: its
 // mean and squared deviations, in all 2^lg lanes that share the group.
 template <int V, bool WHOLE>
-__device__ __forceinline__ float2 join_lanes(const NormArgs& A, const float2* sh, const BlockGroups& b, uint32_t blk,
+__device__ __forceinline__ float2 join_lanes(const NormCore& A, const float2* sh, const BlockGroups& b, uint32_t blk,
                                              uint32_t g, const RunRows& rr, int lg) {
   const uint32_t lane = threadIdx.x & ((1u << lg) - 1u);
   const uint32_t width = A.lanes.d * V;
@@ -267,7 +267,7 @@ template <int V>
 struct Params {
   float gamma[V], beta[V];
 
-  __device__ __forceinline__ Params(const NormArgs& A, uint32_t c, int valid) {
+  __device__ __forceinline__ Params(const NormCore& A, uint32_t c, int valid) {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       gamma[e] = 1.0f;

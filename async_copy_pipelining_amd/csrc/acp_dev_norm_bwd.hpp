@@ -11,39 +11,55 @@ namespace dev {
 template <class T, int KIND, int PK>
 struct Source {
   static constexpr int V = kChunk<T>;
-  static constexpr bool PACKED = PK != 0, TAIL = KIND == kNormAny, LINEAR = !TAIL;
+  static constexpr bool TAIL = KIND == kNormAny, LINEAR = !TAIL;
   struct Raw {
-    rw4 raw;
     Codes<V> codes;
     float s;
   };
-  Walk<LINEAR> x, scales;
+  Walk<LINEAR> codes, scales;
 
-  __device__ __forceinline__ Source(const NormArgs& A, const Spot& w)
-      : x(PACKED ? walk_codes<V, LINEAR>(A, w) : walk<T, LINEAR>(A, A.x, w)), scales(walk_scales<LINEAR>(A, w)) {}
+  __device__ __forceinline__ Source(const NormBackwardSaved& A, const Spot& w)
+      : codes(walk_codes<V, LINEAR>(A, A.codes, w)), scales(walk_scales<LINEAR>(A, A.scales, w)) {}
   template <bool KEEP>
-  __device__ __forceinline__ void load(const NormArgs& A, uint32_t k, int n, Raw* r) const {
-    if constexpr (PACKED) {
-      r->codes = load_codes<V, KEEP, TAIL>(x.at(A, k), n);
-      r->s = n > 0 ? *reinterpret_cast<const float*>(scales.at(A, k)) : 0.0f;
-    } else {
-      r->raw = load_chunk<T, KEEP, TAIL>(x.at(A, k), n);
-    }
+  __device__ __forceinline__ void load(const NormCore& A, uint32_t k, int n, Raw* r) const {
+    r->codes = load_codes<V, KEEP, TAIL>(codes.at(A, k), n);
+    r->s = n > 0 ? *reinterpret_cast<const float*>(scales.at(A, k)) : 0.0f;
   }
-  // z = x rstd - mu rstd, one fma from a value or from a code (whose scale
-  // joins rstd).  The rounding of mu rstd moves z by half an ulp of it, as the
-  // rounding of mu to float32 has done already.
+  // z = x rstd - mu rstd, one fma from a code, whose scale joins rstd.  The
+  // rounding of mu rstd moves z by half an ulp of it, as the rounding of mu to
+  // float32 has done already.
   template <class P>
   __device__ static __forceinline__ void z(const Raw& r, const P& st, float (&v)[V]) {
-    if constexpr (PACKED) decode(PK - 1, r.codes, 1.0f, v);
-    else widen(r.raw, v, static_cast<const T*>(nullptr));
+    decode(PK - 1, r.codes, 1.0f, v);
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float k = PACKED ? st.second(e) * r.s : st.second(e);
-      v[e] = __builtin_fmaf(v[e], k, st.first(e));
-    }
+    for (int e = 0; e < V; ++e) v[e] = __builtin_fmaf(v[e], st.second(e) * r.s, st.first(e));
   }
 };
+
+template <class T, int KIND>
+struct Source<T, KIND, 0> {
+  static constexpr int V = kChunk<T>;
+  static constexpr bool TAIL = KIND == kNormAny, LINEAR = !TAIL;
+  struct Raw {
+    rw4 raw;
+  };
+  Walk<LINEAR> x;
+
+  __device__ __forceinline__ Source(const NormBackward& A, const Spot& w) : x(walk<T, LINEAR>(A, A.x, w)) {}
+  template <bool KEEP>
+  __device__ __forceinline__ void load(const NormCore& A, uint32_t k, int n, Raw* r) const {
+    r->raw = load_chunk<T, KEEP, TAIL>(x.at(A, k), n);
+  }
+  template <class P>
+  __device__ static __forceinline__ void z(const Raw& r, const P& st, float (&v)[V]) {
+    widen(r.raw, v, static_cast<const T*>(nullptr));
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = __builtin_fmaf(v[e], st.second(e), st.first(e));
+  }
+};
+
+template <int PK>
+using BackwardArgs = std::conditional_t<PK != 0, NormBackwardSaved, NormBackward>;
 
 // Two values of each of a lane's channels: (-mean rstd, rstd), or those of
 // dx: (-rstd c1, -rstd c2) with c1 and c2 the group's two means.  WHOLE (the channels are of one group): one pair for all of them.
@@ -56,7 +72,7 @@ struct Pairs {
   __device__ __forceinline__ float second(int e) const { return q[WHOLE ? 0 : e]; }
   // at(group) gives a pair
   template <class F>
-  __device__ __forceinline__ void load(const NormArgs& A, uint32_t c, int valid, F at) {
+  __device__ __forceinline__ void load(const NormCore& A, uint32_t c, int valid, F at) {
 #pragma unroll
     for (int e = 0; e < K; ++e) {
       const float2 v = e < valid ? at(divide(c + e, A.per)) : make_float2(0.0f, 0.0f);
@@ -64,7 +80,7 @@ struct Pairs {
       q[e] = v.y;
     }
   }
-  __device__ __forceinline__ void load_stats(const NormArgs& A, uint32_t n, uint32_t c, int valid) {
+  __device__ __forceinline__ void load_stats(const NormCore& A, uint32_t n, uint32_t c, int valid) {
     const uint64_t row = static_cast<uint64_t>(n) * A.groups;
     load(A, c, valid, [&](uint32_t g) {
       const float r = A.rstd[row + g];
@@ -122,7 +138,7 @@ __device__ __forceinline__ void times_slope_scaled(const Params<V>& p, const flo
 // that every thread has a share: it sums every P-th row lane of a channel,
 // then the P parts are added.  sh holds blockDim.x * (V + 1) pairs.
 template <int V>
-__device__ __forceinline__ void channel_sums(const NormArgs& A, float2* sh, float2* chan, const float (&sa)[V],
+__device__ __forceinline__ void channel_sums(const NormCore& A, float2* sh, float2* chan, const float (&sa)[V],
                                              const float (&sz)[V]) {
   const uint32_t width = A.lanes.d * V, threads = blockDim.x;
   float2* parts = sh + threads * V;
@@ -175,7 +191,7 @@ __device__ __forceinline__ float2 weigh(const float2* chan, const float* gl, uin
 }
 
 // Writes a channel block's sums: a[c], and z[c] a row of the tensor further.
-__device__ __forceinline__ void write_channels(const NormArgs& A, const Spot& w, uint32_t width, float* out,
+__device__ __forceinline__ void write_channels(const NormCore& A, const Spot& w, uint32_t width, float* out,
                                                const float2* chan) {
   for (uint32_t ch = threadIdx.x; ch < width; ch += blockDim.x) {
     const uint32_t c = w.blk * width + ch;
@@ -191,7 +207,7 @@ __device__ __forceinline__ void write_channels(const NormArgs& A, const Spot& w,
 // that few rounds of loads follow one another.
 constexpr uint32_t kColumns = 16;
 
-__device__ __forceinline__ void sum_columns(const NormArgs& A, uint32_t wg, uint64_t step) {
+__device__ __forceinline__ void sum_columns(const NormCore& A, uint32_t wg, uint64_t step) {
   constexpr uint32_t S = kRowThreads / kColumns;
   __shared__ float sh[kRowThreads];
   const uint32_t col = wg * kColumns + threadIdx.x % kColumns, sub = threadIdx.x / kColumns;
@@ -219,7 +235,7 @@ __device__ __forceinline__ void sum_columns(const NormArgs& A, uint32_t wg, uint
 // One row a sample.  The group sums are taken here; the per-channel sums of
 // this workgroup's rows go to part[run][2][c].
 template <class T, int PK, int ACT>
-__global__ __launch_bounds__(kRowThreadsBackward) void norm_row_backward_kernel(const NormArgs A) {
+__global__ __launch_bounds__(kRowThreadsBackward) void norm_row_backward_kernel(const BackwardArgs<PK> A) {
   constexpr int V = kChunk<T>, U = kRowUnroll;
   extern __shared__ float2 lds[];
   const Spot w(A, blockIdx.x, V);
@@ -287,7 +303,7 @@ __global__ __launch_bounds__(kRowThreadsBackward) void norm_row_backward_kernel(
 // samples run, run + runs, ... and leaves its per-channel sums in
 // part[run][2][c].
 template <class T, int KIND, int PK, int ACT>
-__global__ __launch_bounds__(kSlabThreadsBackward) void norm_slab_backward_kernel(const NormArgs A) {
+__global__ __launch_bounds__(kSlabThreadsBackward) void norm_slab_backward_kernel(const BackwardArgs<PK> A) {
   constexpr bool WHOLE = KIND == kNormWhole, TAIL = KIND == kNormAny, LINEAR = !TAIL;
   constexpr int V = kChunk<T>, U = kSlabRowsBackward;
   extern __shared__ float2 lds[];
@@ -391,7 +407,7 @@ __global__ __launch_bounds__(kSlabThreadsBackward) void norm_slab_backward_kerne
 // the caches for the second pass; each chunk's place takes the one U steps on
 // as soon as it is used.
 template <class T, int KIND, int PK, int ACT>
-__global__ __launch_bounds__(kRowThreads) void norm_sums_kernel(const NormArgs A) {
+__global__ __launch_bounds__(kRowThreads) void norm_sums_kernel(const BackwardArgs<PK> A) {
   constexpr bool WHOLE = KIND == kNormWhole, TAIL = KIND == kNormAny, LINEAR = !TAIL;
   constexpr int V = kChunk<T>, U = kRowUnroll;
   extern __shared__ float2 lds[];
@@ -454,7 +470,7 @@ __global__ __launch_bounds__(kRowThreads) void norm_sums_kernel(const NormArgs A
 
 // (-rstd c1, -rstd c2) of group g of sample n from its parts, in all of the
 // 2^lg lanes that share the group.
-__device__ __forceinline__ float2 join_sums(const NormArgs& A, uint32_t n, uint32_t g, uint32_t width, int lg) {
+__device__ __forceinline__ float2 join_sums(const NormCore& A, uint32_t n, uint32_t g, uint32_t width, int lg) {
   const uint32_t lane = threadIdx.x & ((1u << lg) - 1u);
   const uint64_t at = static_cast<uint64_t>(n) * A.groups + g;
   const float2* part = reinterpret_cast<const float2*>(A.coef) + at * A.parts * A.pieces;
@@ -488,7 +504,7 @@ __device__ __forceinline__ float2 join_sums(const NormArgs& A, uint32_t n, uint3
 // dx.  The first workgroups add up dgamma and dbeta.  The first chunks are on
 // their way while the parts are joined.
 template <class T, int KIND, int PK, int ACT>
-__global__ __launch_bounds__(kRowThreads) void norm_dx_kernel(const NormArgs A) {
+__global__ __launch_bounds__(kRowThreads) void norm_dx_kernel(const BackwardArgs<PK> A) {
   constexpr bool WHOLE = KIND == kNormWhole, TAIL = KIND == kNormAny, LINEAR = !TAIL;
   constexpr int V = kChunk<T>, U = kRowUnroll;
   extern __shared__ float2 coef[];

@@ -13,10 +13,10 @@ struct Saver {
   static constexpr bool LINEAR = KIND != kNormAny;
   Walk<LINEAR> codes, scales;
 
-  __device__ __forceinline__ Saver(const NormArgs& A, const Spot& w)
-      : codes(walk_codes<V, LINEAR>(A, w)), scales(walk_scales<LINEAR>(A, w)) {}
+  __device__ __forceinline__ Saver(const NormForwardSaved& A, const Spot& w)
+      : codes(walk_codes<V, LINEAR>(A, A.codes, w)), scales(walk_scales<LINEAR>(A, A.scales, w)) {}
   // all lanes of a scale block come here together; n: channels to write
-  __device__ __forceinline__ void save(const NormArgs& A, const Spot& w, uint32_t k, int n, const float (&x)[V]) const {
+  __device__ __forceinline__ void save(const NormCore& A, const Spot& w, uint32_t k, int n, const float (&x)[V]) const {
     const float s = block_scale(PK - 1, block_amax(x, A.lb_log2));
     float v[V];
 #pragma unroll
@@ -29,12 +29,20 @@ struct Saver {
   }
 };
 
+template <class T, int KIND>
+struct Saver<T, KIND, 0> {
+  __device__ __forceinline__ Saver(const NormForward&, const Spot&) {}
+};
+
+template <int PK>
+using ForwardArgs = std::conditional_t<PK != 0, NormForwardSaved, NormForward>;
+
 // ---------------------------------------------------------------- per row
 
 // One row a sample: rows are samples, and a group lies in 2^group_lanes_log2
 // lanes of a wave.
 template <class T, int PK, int ACT>
-__global__ __launch_bounds__(kRowThreads) void norm_row_kernel(const NormArgs A) {
+__global__ __launch_bounds__(kRowThreads) void norm_row_kernel(const ForwardArgs<PK> A) {
   constexpr int V = kChunk<T>, U = kRowUnroll;
   const Spot w(A, blockIdx.x, V);
   const Walk<true> px = walk<T, true>(A, A.x, w), py = walk<T, true>(A, A.y, w);
@@ -85,7 +93,7 @@ __global__ __launch_bounds__(kRowThreads) void norm_row_kernel(const NormArgs A)
 // All rows of a sample for a block of whole groups: a lane holds up to
 // kSlabRows chunks, so x is read once.
 template <class T, int KIND, int PK, int ACT>
-__global__ __launch_bounds__(kSlabThreads) void norm_slab_kernel(const NormArgs A) {
+__global__ __launch_bounds__(kSlabThreads) void norm_slab_kernel(const ForwardArgs<PK> A) {
   constexpr bool WHOLE = KIND == kNormWhole, TAIL = KIND == kNormAny, LINEAR = !TAIL;
   constexpr int V = kChunk<T>, U = kSlabRows;
   extern __shared__ float2 sh[];
@@ -160,7 +168,7 @@ __global__ __launch_bounds__(kSlabThreads) void norm_slab_kernel(const NormArgs 
 // group's piece in this channel block, into part[n][g][run][piece].  The
 // loads keep the data in the caches for the second pass.
 template <class T, int KIND>
-__global__ __launch_bounds__(kRowThreads) void norm_stats_kernel(const NormArgs A) {
+__global__ __launch_bounds__(kRowThreads) void norm_stats_kernel(const NormStats A) {
   constexpr bool WHOLE = KIND == kNormWhole, TAIL = KIND == kNormAny, LINEAR = !TAIL;
   constexpr int V = kChunk<T>, U = 2 * kRowUnroll;
   __shared__ float2 sh[kRowThreads * (WHOLE ? 1 : V)];
@@ -197,7 +205,7 @@ __global__ __launch_bounds__(kRowThreads) void norm_stats_kernel(const NormArgs 
 
 // mean and rstd of group g of sample n from its parts, in all of the 2^lg
 // lanes that share the group.
-__device__ __forceinline__ float2 join_parts(const NormArgs& A, uint32_t n, uint32_t g, uint32_t width, int lg) {
+__device__ __forceinline__ float2 join_parts(const NormCore& A, uint32_t n, uint32_t g, uint32_t width, int lg) {
   const uint32_t lane = threadIdx.x & ((1u << lg) - 1u);
   const float2* part = reinterpret_cast<const float2*>(A.part) +
                        (static_cast<uint64_t>(n) * A.groups + g) * A.parts * A.pieces;
@@ -250,7 +258,7 @@ __device__ __forceinline__ float2 join_parts(const NormArgs& A, uint32_t n, uint
 // y, and where asked mean, rstd and the 8-bit form of x.  The first chunks
 // are on their way while the parts are joined.
 template <class T, int KIND, int PK, int ACT>
-__global__ __launch_bounds__(kRowThreads) void norm_apply_kernel(const NormArgs A) {
+__global__ __launch_bounds__(kRowThreads) void norm_apply_kernel(const ForwardArgs<PK> A) {
   constexpr bool WHOLE = KIND == kNormWhole, TAIL = KIND == kNormAny, LINEAR = !TAIL;
   constexpr int V = kChunk<T>, U = kRowUnroll;
   extern __shared__ float2 sh[];

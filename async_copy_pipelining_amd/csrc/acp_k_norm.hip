@@ -5,27 +5,20 @@
 namespace acp {
 namespace dev {
 
-__global__ __launch_bounds__(kRowThreads) void norm_columns_kernel(const NormArgs A) {
+__global__ __launch_bounds__(kRowThreads) void norm_columns_kernel(const NormCore A) {
   sum_columns(A, blockIdx.x, 2u * static_cast<uint64_t>(A.c));
 }
 
 }  // namespace dev
 
-namespace {
-
-template <class K>
-hipError_t launch(K kernel, const NormArgs& a, uint32_t grid, uint32_t threads, hipStream_t s) {
-  void* args[] = {const_cast<NormArgs*>(&a)};
-  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(grid), dim3(threads), args, 0, s);
-}
-
-}  // namespace
-
 uint32_t norm_column_grid(const NormArgs& a) { return a.dgamma || a.dbeta ? (2u * a.c + dev::kColumns - 1u) / dev::kColumns : 0u; }
 
 hipError_t norm_columns_launch(const NormArgs& a, hipStream_t s) {
   const uint32_t grid = norm_column_grid(a);
-  return grid ? launch(dev::norm_columns_kernel, a, grid, kRowThreads, s) : hipSuccess;
+  if (grid == 0) return hipSuccess;
+  NormCore core = a;
+  void* args[] = {&core};
+  return hipLaunchKernel(reinterpret_cast<const void*>(dev::norm_columns_kernel), dim3(grid), dim3(kRowThreads), args, 0, s);
 }
 
 hipError_t norm_launch(NormOp op, const NormShape& k, const NormArgs& a, hipStream_t s) {

@@ -13,7 +13,7 @@ struct Chunk {
   int64_t c;  // first channel
   int n;      // channels; none past the row's or the launch's end
 
-  __device__ __forceinline__ Chunk(const RowsArgs& A, uint32_t i, int v) {
+  __device__ __forceinline__ Chunk(const RowsCore& A, uint32_t i, int v) {
     const uint32_t row = divide(i, A.cpr);
     c = static_cast<int64_t>(i - row * A.cpr.d) * v;
     const uint32_t q = divide(row, A.n2);
@@ -29,7 +29,7 @@ struct Chunk {
 };
 
 template <class T, int V>
-__device__ __forceinline__ void save_chunk(const RowsArgs& A, const Packed& p, const Chunk& k, uint32_t i,
+__device__ __forceinline__ void save_chunk(const RowsCore& A, const Packed& p, const Chunk& k, uint32_t i,
                                            const float (&v)[V]) {
   float x[V];
 #pragma unroll
@@ -43,19 +43,19 @@ __device__ __forceinline__ void save_chunk(const RowsArgs& A, const Packed& p, c
 }
 
 template <int V>
-__device__ __forceinline__ void saved_chunk(const RowsArgs& A, const Codes<V>& c, float s, float (&x)[V]) {
+__device__ __forceinline__ void saved_chunk(const RowsCore& A, const Codes<V>& c, float s, float (&x)[V]) {
   decode(A.format, c, s, x);
 }
 
 template <class T, int U>
-__global__ __launch_bounds__(kRowThreads) void pack8_kernel(const RowsArgs A) {
+__global__ __launch_bounds__(kRowThreads) void pack8_kernel(const RowsUse<1, 1> A) {
   constexpr int V = kChunk<T>;
   const uint32_t i0 = blockIdx.x * (blockDim.x * U) + threadIdx.x;
   rw4 r[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const Chunk k(A, i0 + u * blockDim.x, V);
-    r[u] = load_chunk<T>(k.at(A.x, sizeof(T)), k.n);
+    r[u] = load_chunk<T>(k.at(A.t[0], sizeof(T)), k.n);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -63,12 +63,12 @@ __global__ __launch_bounds__(kRowThreads) void pack8_kernel(const RowsArgs A) {
     const Chunk k(A, i, V);
     float x[V];
     widen(r[u], x, static_cast<const T*>(nullptr));
-    save_chunk<T, V>(A, A.px, k, i, x);
+    save_chunk<T, V>(A, A.p[0], k, i, x);
   }
 }
 
 template <class T, int U>
-__global__ __launch_bounds__(kRowThreads) void unpack8_kernel(const RowsArgs A) {
+__global__ __launch_bounds__(kRowThreads) void unpack8_kernel(const RowsUse<1, 1> A) {
   constexpr int V = kChunk<T>;
   const uint32_t i0 = blockIdx.x * (blockDim.x * U) + threadIdx.x;
   Codes<V> c[U];
@@ -77,29 +77,29 @@ __global__ __launch_bounds__(kRowThreads) void unpack8_kernel(const RowsArgs A) 
   for (int u = 0; u < U; ++u) {
     const uint32_t i = i0 + u * blockDim.x;
     const Chunk k(A, i, V);
-    c[u] = load_codes<V>(k.at(A.px.codes, 1), k.n);
-    s[u] = k.n > 0 ? A.px.scales[i >> A.lb_log2] : 0.0f;
+    c[u] = load_codes<V>(k.at(A.p[0].codes, 1), k.n);
+    s[u] = k.n > 0 ? A.p[0].scales[i >> A.lb_log2] : 0.0f;
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const Chunk k(A, i0 + u * blockDim.x, V);
     float x[V];
     saved_chunk<V>(A, c[u], s[u], x);
-    if (k.n > 0) store_chunk<T>(k.at(A.y, sizeof(T)), k.n, narrow(x, static_cast<const T*>(nullptr)));
+    if (k.n > 0) store_chunk<T>(k.at(A.t[0], sizeof(T)), k.n, narrow(x, static_cast<const T*>(nullptr)));
   }
 }
 
 // y = act(x) [* z], and x [and z] kept in 8 bits.
 template <class T, bool GATED, bool SAVE, int U>
-__global__ __launch_bounds__(kRowThreads) void act_forward_kernel(const RowsArgs A) {
+__global__ __launch_bounds__(kRowThreads) void act_forward_kernel(const RowsUse<GATED ? 3 : 2, SAVE ? (GATED ? 2 : 1) : 0> A) {
   constexpr int V = kChunk<T>;
   const uint32_t i0 = blockIdx.x * (blockDim.x * U) + threadIdx.x;
   rw4 rx[U], rz[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const Chunk k(A, i0 + u * blockDim.x, V);
-    rx[u] = load_chunk<T>(k.at(A.x, sizeof(T)), k.n);
-    if constexpr (GATED) rz[u] = load_chunk<T>(k.at(A.z, sizeof(T)), k.n);
+    rx[u] = load_chunk<T>(k.at(A.t[0], sizeof(T)), k.n);
+    if constexpr (GATED) rz[u] = load_chunk<T>(k.at(A.t[2], sizeof(T)), k.n);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -107,21 +107,21 @@ __global__ __launch_bounds__(kRowThreads) void act_forward_kernel(const RowsArgs
     const Chunk k(A, i, V);
     float x[V], z[V];
     widen(rx[u], x, static_cast<const T*>(nullptr));
-    if constexpr (SAVE) save_chunk<T, V>(A, A.px, k, i, x);
+    if constexpr (SAVE) save_chunk<T, V>(A, A.p[0], k, i, x);
     act_values(A.act, x);
     if constexpr (GATED) {
       widen(rz[u], z, static_cast<const T*>(nullptr));
-      if constexpr (SAVE) save_chunk<T, V>(A, A.pz, k, i, z);
+      if constexpr (SAVE) save_chunk<T, V>(A, A.p[1], k, i, z);
 #pragma unroll
       for (int e = 0; e < V; ++e) x[e] *= z[e];
     }
-    if (k.n > 0) store_chunk<T>(k.at(A.y, sizeof(T)), k.n, narrow(x, static_cast<const T*>(nullptr)));
+    if (k.n > 0) store_chunk<T>(k.at(A.t[1], sizeof(T)), k.n, narrow(x, static_cast<const T*>(nullptr)));
   }
 }
 
 // dx = dy act'(x) [* z], dz = dy act(x), with x and z from their 8-bit forms.
 template <class T, bool GATED, int U>
-__global__ __launch_bounds__(kRowThreads) void act_backward_kernel(const RowsArgs A) {
+__global__ __launch_bounds__(kRowThreads) void act_backward_kernel(const RowsUse<GATED ? 3 : 2, GATED ? 2 : 1> A) {
   constexpr int V = kChunk<T>;
   const uint32_t i0 = blockIdx.x * (blockDim.x * U) + threadIdx.x;
   rw4 rd[U];
@@ -131,12 +131,12 @@ __global__ __launch_bounds__(kRowThreads) void act_backward_kernel(const RowsArg
   for (int u = 0; u < U; ++u) {
     const uint32_t i = i0 + u * blockDim.x;
     const Chunk k(A, i, V);
-    rd[u] = load_chunk<T>(k.at(A.dy, sizeof(T)), k.n);
-    cx[u] = load_codes<V>(k.at(A.px.codes, 1), k.n);
-    sx[u] = k.n > 0 ? A.px.scales[i >> A.lb_log2] : 0.0f;
+    rd[u] = load_chunk<T>(k.at(A.t[0], sizeof(T)), k.n);
+    cx[u] = load_codes<V>(k.at(A.p[0].codes, 1), k.n);
+    sx[u] = k.n > 0 ? A.p[0].scales[i >> A.lb_log2] : 0.0f;
     if constexpr (GATED) {
-      cz[u] = load_codes<V>(k.at(A.pz.codes, 1), k.n);
-      sz[u] = k.n > 0 ? A.pz.scales[i >> A.lb_log2] : 0.0f;
+      cz[u] = load_codes<V>(k.at(A.p[1].codes, 1), k.n);
+      sz[u] = k.n > 0 ? A.p[1].scales[i >> A.lb_log2] : 0.0f;
     }
   }
 #pragma unroll
@@ -156,9 +156,9 @@ __global__ __launch_bounds__(kRowThreads) void act_backward_kernel(const RowsArg
         slope[e] *= z[e];
         value[e] *= d[e];
       }
-      if (k.n > 0) store_chunk<T>(k.at(A.dz, sizeof(T)), k.n, narrow(value, static_cast<const T*>(nullptr)));
+      if (k.n > 0) store_chunk<T>(k.at(A.t[2], sizeof(T)), k.n, narrow(value, static_cast<const T*>(nullptr)));
     }
-    if (k.n > 0) store_chunk<T>(k.at(A.dx, sizeof(T)), k.n, narrow(slope, static_cast<const T*>(nullptr)));
+    if (k.n > 0) store_chunk<T>(k.at(A.t[1], sizeof(T)), k.n, narrow(slope, static_cast<const T*>(nullptr)));
   }
 }
 
@@ -172,40 +172,62 @@ namespace {
 // quickly.  Past it, workgroups of four waves with U chunks in flight a lane.
 constexpr uint32_t kSmallChunks = 256u * 64u * 8u;
 
-template <class K>
-hipError_t launch_rows(K kernel, const RowsArgs& a, uint32_t threads, uint32_t unroll, hipStream_t s) {
+template <class A>
+hipError_t launch_rows(void (*kernel)(A), A a, uint32_t threads, uint32_t unroll, hipStream_t s) {
   const uint32_t per = threads * unroll;
   const uint32_t grid = a.total / per + (a.total % per ? 1u : 0u);
-  void* args[] = {const_cast<RowsArgs*>(&a)};
+  void* args[] = {&a};
   return hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(grid), dim3(threads), args, 0, s);
 }
 
-template <class K>
-hipError_t launch_rows(K one, K many, uint32_t unroll, const RowsArgs& a, hipStream_t s) {
+// `one`: the kernel with a chunk a lane, `many`: with `unroll` of them.
+template <class A>
+hipError_t launch_rows(void (*one)(A), void (*many)(A), uint32_t unroll, const A& a, hipStream_t s) {
   return a.total <= kSmallChunks ? launch_rows(one, a, 64, 1, s) : launch_rows(many, a, kRowThreads, unroll, s);
+}
+
+// A kernel's arguments out of a call's.
+template <int NT, int NP>
+RowsUse<NT, NP> use(const RowsArgs& a, const RowTensor& t0, const RowTensor& t1, const RowTensor& t2) {
+  RowsUse<NT, NP> u;
+  static_cast<RowsCore&>(u) = a;
+  u.t[0] = t0;
+  if constexpr (NT > 1) u.t[1] = t1;
+  if constexpr (NT > 2) u.t[2] = t2;
+  if constexpr (NP > 0) u.p[0] = a.px;
+  if constexpr (NP > 1) u.p[1] = a.pz;
+  return u;
 }
 
 template <class T>
 hipError_t pack8_t(const RowsArgs& a, hipStream_t s) {
-  return launch_rows(dev::pack8_kernel<T, 1>, dev::pack8_kernel<T, 4>, 4, a, s);
+  return launch_rows<RowsUse<1, 1>>(dev::pack8_kernel<T, 1>, dev::pack8_kernel<T, 4>, 4, use<1, 1>(a, a.x, a.x, a.x), s);
 }
 
 template <class T>
 hipError_t unpack8_t(const RowsArgs& a, hipStream_t s) {
-  return launch_rows(dev::unpack8_kernel<T, 1>, dev::unpack8_kernel<T, 4>, 4, a, s);
+  return launch_rows<RowsUse<1, 1>>(dev::unpack8_kernel<T, 1>, dev::unpack8_kernel<T, 4>, 4, use<1, 1>(a, a.y, a.y, a.y),
+                                    s);
 }
 
-template <class T, bool GATED>
-hipError_t act_forward_t(bool save, const RowsArgs& a, hipStream_t s) {
-  constexpr int U = GATED ? 2 : 4;
-  return save ? launch_rows(dev::act_forward_kernel<T, GATED, true, 1>, dev::act_forward_kernel<T, GATED, true, U>, U, a, s)
-              : launch_rows(dev::act_forward_kernel<T, GATED, false, 1>, dev::act_forward_kernel<T, GATED, false, U>, U, a, s);
+template <class T, bool GATED, bool SAVE>
+hipError_t act_forward_t(const RowsArgs& a, hipStream_t s) {
+  constexpr int U = GATED ? 2 : 4, NT = GATED ? 3 : 2, NP = SAVE ? (GATED ? 2 : 1) : 0;
+  return launch_rows<RowsUse<NT, NP>>(dev::act_forward_kernel<T, GATED, SAVE, 1>, dev::act_forward_kernel<T, GATED, SAVE, U>,
+                                      U, use<NT, NP>(a, a.x, a.y, a.z), s);
+}
+
+template <class T>
+hipError_t act_forward_t(bool gated, bool save, const RowsArgs& a, hipStream_t s) {
+  if (gated) return save ? act_forward_t<T, true, true>(a, s) : act_forward_t<T, true, false>(a, s);
+  return save ? act_forward_t<T, false, true>(a, s) : act_forward_t<T, false, false>(a, s);
 }
 
 template <class T, bool GATED>
 hipError_t act_backward_t(const RowsArgs& a, hipStream_t s) {
-  constexpr int U = GATED ? 2 : 4;
-  return launch_rows(dev::act_backward_kernel<T, GATED, 1>, dev::act_backward_kernel<T, GATED, U>, U, a, s);
+  constexpr int U = GATED ? 2 : 4, NT = GATED ? 3 : 2, NP = GATED ? 2 : 1;
+  return launch_rows<RowsUse<NT, NP>>(dev::act_backward_kernel<T, GATED, 1>, dev::act_backward_kernel<T, GATED, U>, U,
+                                      use<NT, NP>(a, a.dy, a.dx, a.dz), s);
 }
 
 }  // namespace
@@ -223,10 +245,9 @@ hipError_t unpack8_launch(int dt, const RowsArgs& a, hipStream_t s) {
 }
 
 hipError_t act_forward_launch(int dt, bool gated, bool save, const RowsArgs& a, hipStream_t s) {
-  if (dt == kRowF16) return gated ? act_forward_t<_Float16, true>(save, a, s) : act_forward_t<_Float16, false>(save, a, s);
-  if (dt == kRowBF16)
-    return gated ? act_forward_t<dev::bf16_t, true>(save, a, s) : act_forward_t<dev::bf16_t, false>(save, a, s);
-  return gated ? act_forward_t<float, true>(save, a, s) : act_forward_t<float, false>(save, a, s);
+  if (dt == kRowF16) return act_forward_t<_Float16>(gated, save, a, s);
+  if (dt == kRowBF16) return act_forward_t<dev::bf16_t>(gated, save, a, s);
+  return act_forward_t<float>(gated, save, a, s);
 }
 
 hipError_t act_backward_launch(int dt, bool gated, const RowsArgs& a, hipStream_t s) {

@@ -11,9 +11,40 @@ namespace norm {
 template <int I>
 using Int = std::integral_constant<int, I>;
 
-template <class K>
-hipError_t launch(K kernel, const NormArgs& a, uint32_t grid, uint32_t threads, uint32_t lds, hipStream_t s) {
-  void* args[] = {const_cast<NormArgs*>(&a)};
+// A kernel's arguments out of a call's.
+inline void pick(const NormArgs& a, NormStats* u) {
+  static_cast<NormCore&>(*u) = a;
+  u->x = a.x;
+}
+inline void pick(const NormArgs& a, NormForward* u) {
+  static_cast<NormCore&>(*u) = a;
+  u->x = a.x;
+  u->y = a.y;
+}
+inline void pick(const NormArgs& a, NormForwardSaved* u) {
+  pick(a, static_cast<NormForward*>(u));
+  u->codes = a.codes;
+  u->scales = a.scales;
+}
+inline void pick(const NormArgs& a, NormBackward* u) {
+  static_cast<NormCore&>(*u) = a;
+  u->dy = a.dy;
+  u->dx = a.dx;
+  u->x = a.x;
+}
+inline void pick(const NormArgs& a, NormBackwardSaved* u) {
+  static_cast<NormCore&>(*u) = a;
+  u->dy = a.dy;
+  u->dx = a.dx;
+  u->codes = a.codes;
+  u->scales = a.scales;
+}
+
+template <class A>
+hipError_t launch(void (*kernel)(A), const NormArgs& a, uint32_t grid, uint32_t threads, uint32_t lds, hipStream_t s) {
+  std::remove_const_t<A> u;
+  pick(a, &u);
+  void* args[] = {&u};
   return hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(grid), dim3(threads), args, lds, s);
 }
 

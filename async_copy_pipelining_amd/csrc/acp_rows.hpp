@@ -32,12 +32,14 @@ struct Packed {
   float* scales;
 };
 
+// A launch writes its kernel's arguments to memory that the host reaches
+// slowly, at about 2.4 ns a byte (a launch with 540 bytes takes 3.7 us, with
+// 110 bytes 2.6): each kernel takes the tensors that it uses and no others.
+
 // Elementwise row operators: chunk i of the launch is chunk i % cpr of row
 // i / cpr, and row r is index (r / (n1 * n2), r / n2 % n1, r % n2).  cpr is a
 // whole number of scale blocks, so block i >> lb_log2 has chunk i.
-struct RowsArgs {
-  RowTensor x, z, y, dy, dx, dz;
-  Packed px, pz;
+struct RowsCore {
   int64_t c;        // channels of a row
   uint32_t total;   // chunks, those past a row's end included
   Div cpr, n1, n2;
@@ -45,12 +47,26 @@ struct RowsArgs {
   int format, act;
 };
 
+// What the host fills in, and a kernel's own arguments: NT float tensors and
+// NP 8-bit forms.
+struct RowsArgs : RowsCore {
+  RowTensor x, z, y, dy, dx, dz;
+  Packed px, pz;
+};
+template <int NT, int NP>
+struct RowsUse : RowsCore {
+  RowTensor t[NT];
+  Packed p[NP > 0 ? NP : 1];
+};
+template <int NT>
+struct RowsUse<NT, 0> : RowsCore {
+  RowTensor t[NT];
+};
+
 // Group norm.  A workgroup covers `lanes` chunks of a row (channel block
 // blk) and `row_lanes` rows at a time; such steps are dealt out to the runs
 // that a sample's rows are split into.
-struct NormArgs {
-  RowTensor x, y, dy, dx;   // s[0] per sample; row r of a sample at r / row2.d * s[1] + r % row2.d * s[2]
-  RowTensor codes, scales;  // the saved form of x, written (forward) or read (backward)
+struct NormCore {
   const float* gamma;       // nullptr: 1
   const float* beta;        // nullptr: 0
   float* mean;              // [samples, groups]
@@ -70,6 +86,30 @@ struct NormArgs {
   uint32_t col_rows;        // rows of partial column sums
   int lb_log2, group_lanes_log2;
   float eps;
+};
+
+// What the host fills in.  Tensors: s[0] per sample; row r of a sample at
+// r / row2.d * s[1] + r % row2.d * s[2].  codes and scales: the saved form of
+// x, written (forward) or read (backward).
+struct NormArgs : NormCore {
+  RowTensor x, y, dy, dx, codes, scales;
+};
+
+// A kernel's own arguments.
+struct NormStats : NormCore {
+  RowTensor x;
+};
+struct NormForward : NormCore {
+  RowTensor x, y;
+};
+struct NormForwardSaved : NormForward {
+  RowTensor codes, scales;
+};
+struct NormBackward : NormCore {
+  RowTensor dy, dx, x;
+};
+struct NormBackwardSaved : NormCore {
+  RowTensor dy, dx, codes, scales;
 };
 
 // What a chunk may hold and how its row is found: channels of one group; whole
