@@ -62,7 +62,8 @@ template <int PK>
 using BackwardArgs = std::conditional_t<PK != 0, NormBackwardSaved, NormBackward>;
 
 // Two values of each of a lane's channels: (-mean rstd, rstd), or those of
-// dx: (-rstd c1, -rstd c2) with c1 and c2 the group's two means.  WHOLE (the channels are of one group): one pair for all of them.
+// dx: (-rstd c1, -rstd c2) with c1 and c2 the group's two means.  WHOLE (the
+// channels are of one group): one pair for all of them.
 template <int V, bool WHOLE>
 struct Pairs {
   static constexpr int K = WHOLE ? 1 : V;
@@ -124,7 +125,6 @@ __device__ __forceinline__ void times_slope_scaled(const Params<V>& p, const flo
     for (int e = 0; e < V; ++e) {
       const float t = __builtin_fmaf(z[e], p.gamma[e], p.beta[e]);
       const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t));
-      // t is infinite only with s = 0 or 1, where the slope is 0 or 1
       const float m = __builtin_fmaf(s, kLn2, -kLn2);
       dy[e] *= s * __builtin_fmaf(t, m, 1.0f);
     }

@@ -97,7 +97,7 @@ __global__ __launch_bounds__(kSlabThreads) void norm_slab_kernel(const ForwardAr
   constexpr bool WHOLE = KIND == kNormWhole, TAIL = KIND == kNormAny, LINEAR = !TAIL;
   constexpr int V = kChunk<T>, U = kSlabRows;
   extern __shared__ float2 sh[];
-    const Spot w(A, near_group(blockIdx.x, gridDim.x), V);
+  const Spot w(A, near_group(blockIdx.x, gridDim.x), V);
   const Walk<LINEAR> px = walk<T, LINEAR>(A, A.x, w);
   rw4 raw[U];
 #pragma unroll

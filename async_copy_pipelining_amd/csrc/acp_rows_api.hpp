@@ -49,25 +49,52 @@ int64_t elements(const acp::DescData& t) {
   return n;
 }
 
-// A byte range that a call reads or writes.
+// A byte range that a call reads or writes, and the tensor that it belongs to.
 struct Range {
   uint64_t at, bytes;
   const char* what;
+  const acp::DescData* tensor;
 };
 
-Range range_of(const acp::DescData& t, const char* what) { return {t.gbase, tensor_span(t), what}; }
+Range range_of(const acp::DescData& t, const char* what) { return {t.gbase, tensor_span(t), what, &t}; }
 Range range_of(const void* p, int64_t bytes, const char* what) {
-  return {reinterpret_cast<uint64_t>(p), p ? static_cast<uint64_t>(bytes) : 0u, what};
+  return {reinterpret_cast<uint64_t>(p), p ? static_cast<uint64_t>(bytes) : 0u, what, nullptr};
+}
+
+// Whether the rows of two tensors lie side by side in one buffer: equal row
+// pitches, every other stride a multiple of the pitch, and each tensor's rows
+// in their own part of it.
+bool side_by_side(const acp::DescData& a, const acp::DescData& b) {
+  if (a.rank != b.rank || a.rank < 2) return false;
+  const int r = a.rank - 1;
+  uint64_t pitch = 0;
+  for (int d = 0; d < r; ++d) {
+    if (a.shape[d] != b.shape[d]) return false;
+    if (a.shape[d] == 1) continue;
+    const uint64_t s = static_cast<uint64_t>(a.strides[d]) * a.esize;
+    if (s != static_cast<uint64_t>(b.strides[d]) * b.esize) return false;
+    pitch = pitch == 0 || s < pitch ? s : pitch;
+  }
+  if (pitch == 0) return false;
+  for (int d = 0; d < r; ++d)
+    if (a.shape[d] > 1 && static_cast<uint64_t>(a.strides[d]) * a.esize % pitch) return false;
+  const uint64_t from = b.gbase >= a.gbase ? (b.gbase - a.gbase) % pitch : (pitch - (a.gbase - b.gbase) % pitch) % pitch;
+  const uint64_t na = static_cast<uint64_t>(a.shape[r]) * a.esize, nb = static_cast<uint64_t>(b.shape[r]) * b.esize;
+  return from >= na && from + nb <= pitch;
+}
+
+bool meet(const Range& a, const Range& b) {
+  return overlap(a.at, a.bytes, b.at, b.bytes) && !(a.tensor && b.tensor && side_by_side(*a.tensor, *b.tensor));
 }
 
 // Written ranges share no byte with each other or with what is read.
 acp_status check_ranges(const Range* out, int n_out, const Range* in, int n_in) {
   for (int i = 0; i < n_out; ++i) {
     for (int j = i + 1; j < n_out; ++j)
-      if (overlap(out[i].at, out[i].bytes, out[j].at, out[j].bytes))
+      if (meet(out[i], out[j]))
         return ret(ACP_ERR_INVALID, std::string(out[i].what) + " and " + out[j].what + " share memory");
     for (int j = 0; j < n_in; ++j)
-      if (overlap(out[i].at, out[i].bytes, in[j].at, in[j].bytes))
+      if (meet(out[i], in[j]))
         return ret(ACP_ERR_INVALID, std::string(out[i].what) + " and " + in[j].what + " share memory");
   }
   return ACP_OK;

@@ -161,6 +161,40 @@ def test_activation_forward_and_backward(dtype, name):
             assert all(t.untouched() for t in (y, plain, dx))
 
 
+def test_the_halves_of_a_fused_projection():
+    """Gate and operand, their gradients and their codes each side by side in
+    one buffer."""
+    say("halves of one buffer")
+    rows, c = 37, 136
+    both = torch.randn(rows, 2 * c, device=DEV).to(torch.bfloat16)
+    grads = torch.zeros(rows, 2 * c, dtype=torch.bfloat16, device=DEV)
+    codes = torch.zeros(rows, 2 * c, dtype=torch.uint8, device=DEV)
+    y, dy = (torch.randn(rows, c, device=DEV).to(torch.bfloat16) for _ in range(2))
+
+    def half(t, k, name="bf16"):
+        return acp.acp_encode_tiled(name, t[:, k * c:(k + 1) * c], (rows, c), t.stride(), (1, 1))
+
+    scales = torch.zeros(2, rows, 3, device=DEV)
+    sx, sz = (acp.acp_packed8(half(codes, k, "u8"), scales[k], "i8", 64) for k in range(2))
+    yd, dyd = (acp.acp_encode_tiled("bf16", t, (rows, c), (c, 1), (1, 1)) for t in (y, dy))
+    acp.acp_act_forward("silu", yd, half(both, 0), half(both, 1), sx, sz)
+    acp.acp_act_backward("silu", half(grads, 0), half(grads, 1), dyd, sx, sz)
+    torch.cuda.synchronize()
+    v = both.double().cpu().numpy()
+    kept = []
+    for k in range(2):
+        want_codes, want_scales = R.pack(v[:, k * c:(k + 1) * c], "i8", 64, TOP["bf16"])
+        assert np.array_equal(codes[:, k * c:(k + 1) * c].cpu().numpy(), want_codes)
+        assert np.array_equal(scales[k].cpu().numpy(), want_scales)
+        kept.append(R.unpack(want_codes, want_scales, "i8", 64).astype(np.float32).astype(np.float64))
+    d = dy.double().cpu().numpy()
+    wx, wz = R.act_backward("silu", d, kept[0], kept[1])
+    g = grads.double().cpu().numpy()
+    err = act_error("silu", kept[0])
+    close(g[:, :c], wx, np.abs(d * kept[1]) * err + np.abs(wx) * 4 * U + out_step("bf16", wx), "dx")
+    close(g[:, c:], wz, np.abs(d) * err + np.abs(wz) * 4 * U + out_step("bf16", wz), "dz")
+
+
 def test_offsets_past_32_bits():
     """Rows 2.5 GiB apart: byte offsets of the second and third pass 2^31 and 2^32."""
     say("rows 2.5 GiB apart")

@@ -162,6 +162,19 @@ def test_a_gate_without_x_and_z_both_plain_and_saved_is_refused_in_c():
     assert st == INVALID and "not both" in acp.acp_last_error()
 
 
+def test_rows_side_by_side_in_one_buffer_that_do_meet_are_refused():
+    # halves of rows 128 elements apart share no byte; these do
+    def rows(at, shape=(6, 64), pitch=128):
+        return acp.acp_encode_tiled("f16", BASE + 2 * at, shape, (pitch, 1), (1, 1))
+    for other in (rows(63), rows(65), rows(128 * 3 + 32), rows(64, (6, 64), 64), rows(64, (6, 65), 128)):
+        refused(lambda other=other: acp.acp_act_forward("silu", rows(0), other), INVALID,
+                "share memory" if acp.acp_plan_query(other)["dims"][0] == 64 else "differ")
+    # rows of a second dim that does not keep to the pitch
+    a = acp.acp_encode_tiled("f16", BASE, (2, 3, 64), (448, 128, 1), (1, 1, 1))
+    b = acp.acp_encode_tiled("f16", BASE + 128, (2, 3, 64), (448, 128, 1), (1, 1, 1))
+    refused(lambda: acp.acp_act_forward("silu", a, b), INVALID, "share memory")
+
+
 def test_workspace_query():
     # one row a sample, groups of whole lanes: the forward pass needs none
     assert acp.acp_group_norm_workspace(desc(1, (5, 64)), 8) > 0
