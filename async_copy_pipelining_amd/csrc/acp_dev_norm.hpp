@@ -20,6 +20,9 @@
 // * by parts: one kernel leaves partial sums of runs of rows in the
 //   workspace, the next one joins them and makes the second pass.
 // All sums have a fixed order, so results are the same from run to run.
+// Kernels are built for one activation and one 8-bit form each: a wave's code
+// has to come into the instruction cache, and for small tensors that is most
+// of its time.
 //
 // Statistics: a lane sums d = x - k and d^2 where k is a value that it meets
 // itself.  With k a member of the set, the sum of squares is at most about n
@@ -35,10 +38,6 @@
 
 namespace acp {
 namespace dev {
-
-// Kernels are built for one activation and one 8-bit form each: a wave's code
-// has to come into the instruction cache, and for small tensors that is most
-// of its time.
 
 // Where a lane of a workgroup works.
 struct Spot {

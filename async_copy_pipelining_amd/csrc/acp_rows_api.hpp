@@ -1,7 +1,7 @@
 // Entry points of the row operators: 8-bit checkpoints, activations, group
 // norm.  Included by acp_entry.cpp after acp_api.cpp, whose helpers it uses.
 // Host code: checks, the collapse of the tensors' outer dims, and the split of
-// the work; one to three kernels on the caller's stream.
+// the work; one or two kernels on the caller's stream.
 #include <algorithm>
 #include <cmath>
 
@@ -447,7 +447,6 @@ void set_block(acp::NormArgs* A, int64_t lanes, int64_t blocks, int64_t threads)
   A->row_lanes = static_cast<uint32_t>(threads / lanes);
 }
 
-
 // One row a sample, a group in a power of two of a wave's lanes: rows are
 // samples.
 bool plan_row(const NormDims& d, NormPlan* P) {
@@ -498,10 +497,24 @@ bool plan_slab(const NormDims& d, NormPlan* P) {
   while (!fits(lanes, threads)) threads *= 2;
   // few workgroups: more lanes with fewer chunks each
   while (threads < most && d.samples * blocks * threads <= 256 * 512 && 2 * (threads / lanes) < d.rows) threads *= 2;
+  // few workgroups with long lanes, each of which waits for itself alone: by
+  // parts spreads them ([1, 1024, 512] float16, 32 groups 8.8 us, 11.8 as
+  // slabs of eight chunks a lane; [2, 256, 640], six, 9.2 and 8.4; [16, 1024, 512],
+  // 128 workgroups, 15.4 and 13.4)
+  if (!d.backward && d.samples * blocks < 64 && ceil_div(d.rows, threads / lanes) > 6) return false;
+  // backward, blocks of less than 64 bytes, whose column sums take a launch of
+  // their own ([8, 900, 128] float16, 8 groups 10.1 us by parts, 12.4 as slabs
+  // of 32 bytes; [2, 500, 256], blocks of 64 bytes, 9.9 and 10.3)
+  if (d.backward && d.samples > 1 && blocks > 1 && lanes < 4) return false;
   // backward, a lane's values fill so many registers that a CU holds one
-  // workgroup: past one a CU the two passes by parts are faster ([128, 500,
-  // 1024] float16 from 8 bits 110 us; 159 as slabs)
-  if (d.backward && d.samples * blocks * threads > 256 * 512) return false;
+  // workgroup of 512 lanes.  Past one a CU the form is still the fastest from
+  // x itself in blocks of whole 128-byte lines ([512, 256, 1024] float16 206
+  // us, by parts 230; [64, 256, 1024] 35 and 47; [1024, 200, 512] float32 250
+  // and 346), but not where blocks end inside a line ([1024, 144, 320] float16
+  // 126 and 99; [128, 500, 1024] in blocks of 64 bytes 132 and 117) or whose
+  // codes end inside one ([512, 256, 1024] from 8 bits 63 us more)
+  const bool lines = whole && !d.block && lanes % kSlabLanes == 0;
+  if (d.backward && !lines && d.samples * blocks * threads > 256 * 512) return false;
   // LDS that a launch may ask for without raising the kernel's limit
   const int64_t pairs = d.backward ? threads * (d.v + 1) + lanes * d.v * 5 / 2 : threads * (whole ? 1 : d.v);
   if ((pairs + lanes * d.v / d.per + 3) * 8 > 65536) return false;

@@ -337,10 +337,10 @@ acp_status acp_stream_binary(acp_op op, const acp_tile_desc* out, const acp_tile
  * bits.  A written tensor must not overlap itself or share memory with
  * another operand (ACP_ERR_INVALID); tensors whose rows lie side by side in
  * one buffer at one pitch, as the halves of a fused projection do, share
- * none.  Memory between the rows of an output is left as it was.  Zero elements are a call that does nothing.  A call
- * enqueues one to three kernels and, like the others, allocates nothing and
- * can be captured into a HIP graph; all its memory is of the current device,
- * which is the stream's. */
+ * none.  Memory between the rows of an output is left as it was.  Zero
+ * elements are a call that does nothing.  A call enqueues one or two kernels
+ * and, like the others, allocates nothing and can be captured into a HIP
+ * graph; all its memory is of the current device, which is the stream's. */
 
 /* A tensor in 8 bits: one code a value, and one float32 scale for every
  * `block` neighbouring values of a row (the last block of a row may be

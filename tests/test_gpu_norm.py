@@ -196,7 +196,10 @@ def test_forms_and_kinds_are_the_ones_meant():
             ((1, 9000, 16), 1, "f16", "by parts whole", "by parts whole"),
             ((2, 5000, 40), 4, "f16", "by parts split", "by parts split"),
             ((1, 3000, 33), 3, "f16", "by parts any", "by parts any"),
-            ((700, 33, 64), 8, "f16", "slab whole", "by parts whole")):
+            ((700, 33, 64), 8, "f16", "slab whole", "slab whole"),
+            ((1500, 33, 48), 6, "f16", "slab whole", "by parts whole"),
+            ((1, 1024, 512), 32, "f16", "by parts whole", "slab whole"),
+            ((8, 900, 128), 8, "bf16", "by parts whole", "by parts whole")):
         f, b = Case(shape, groups, dtype, "silu").run()
         assert fwd in f and bwd in b, (f, b)
 
