@@ -6,12 +6,12 @@
 // Each element is read and written once: large tensors are bound by HBM
 // (times of the kernels alone; a plain copy reaches 6.0 TB/s), small ones by
 // the launch.  A chunk's address, scale and codes come from its index alone,
-// so a lane has U chunks in flight and no loop.
-//   pack8     [262144, 256] bfloat16, rows 264 elements apart, i8: 36.3 us, 5.6 TB/s
-//   unpack8   the same: 34.5 us, 5.9 TB/s
-//   act_forward   [8192, 5632] bfloat16, gated, both operands saved as i8: 64 us, 5.8 TB/s
-//   act_backward  the same: 59.5 us, 6.2 TB/s
-//   pack8, unpack8 of [64, 1000] float32: 2.4 and 2.7 us
+// so a lane has its one or two chunks in flight and no loop.
+//   pack8     [262144, 256] bfloat16, rows 264 elements apart, i8: 36.9 us, 5.5 TB/s
+//   unpack8   the same: 33.1 us, 6.1 TB/s
+//   act_forward   [8192, 5632] bfloat16, gated, both operands saved as i8: 63.9 us, 5.8 TB/s
+//   act_backward  the same: 59.1 us, 6.3 TB/s
+//   pack8, unpack8 of [64, 1000] float32: 2.4 and 1.9 us
 #include "acp_dev_rows.hpp"
 
 namespace acp {
@@ -103,7 +103,8 @@ __global__ __launch_bounds__(kRowThreads) void unpack8_kernel(const RowsUse<1, 1
 // the bytes that the activation itself moves, where a pass of their own would
 // read the operands again.
 template <class T, bool GATED, bool SAVE, int U>
-__global__ __launch_bounds__(kRowThreads) void act_forward_kernel(const RowsUse<GATED ? 3 : 2, SAVE ? (GATED ? 2 : 1) : 0> A) {
+__global__ __launch_bounds__(kRowThreads) void act_forward_kernel(
+    const RowsUse<GATED ? 3 : 2, SAVE ? (GATED ? 2 : 1) : 0> A) {
   constexpr int V = kChunk<T>;
   const uint32_t i0 = blockIdx.x * (blockDim.x * U) + threadIdx.x;
   rw4 rx[U], rz[U];
@@ -218,14 +219,15 @@ hipError_t pack8_t(const RowsArgs& a, hipStream_t s) {
 
 template <class T>
 hipError_t unpack8_t(const RowsArgs& a, hipStream_t s) {
-  return launch_rows<RowsUse<1, 1>>(dev::unpack8_kernel<T, 1>, dev::unpack8_kernel<T, 2>, use<1, 1>(a, a.y, a.y, a.y), s);
+  return launch_rows<RowsUse<1, 1>>(dev::unpack8_kernel<T, 1>, dev::unpack8_kernel<T, 2>, use<1, 1>(a, a.y, a.y, a.y),
+                                    s);
 }
 
 template <class T, bool GATED, bool SAVE>
 hipError_t act_forward_t(const RowsArgs& a, hipStream_t s) {
   constexpr int NT = GATED ? 3 : 2, NP = SAVE ? (GATED ? 2 : 1) : 0;
-  return launch_rows<RowsUse<NT, NP>>(dev::act_forward_kernel<T, GATED, SAVE, 1>, dev::act_forward_kernel<T, GATED, SAVE, 2>,
-                                      use<NT, NP>(a, a.x, a.y, a.z), s);
+  return launch_rows<RowsUse<NT, NP>>(dev::act_forward_kernel<T, GATED, SAVE, 1>,
+                                      dev::act_forward_kernel<T, GATED, SAVE, 2>, use<NT, NP>(a, a.x, a.y, a.z), s);
 }
 
 template <class T>

@@ -78,7 +78,8 @@ bool side_by_side(const acp::DescData& a, const acp::DescData& b) {
   if (pitch == 0) return false;
   for (int d = 0; d < r; ++d)
     if (a.shape[d] > 1 && static_cast<uint64_t>(a.strides[d]) * a.esize % pitch) return false;
-  const uint64_t from = b.gbase >= a.gbase ? (b.gbase - a.gbase) % pitch : (pitch - (a.gbase - b.gbase) % pitch) % pitch;
+  const uint64_t from =
+      b.gbase >= a.gbase ? (b.gbase - a.gbase) % pitch : (pitch - (a.gbase - b.gbase) % pitch) % pitch;
   const uint64_t na = static_cast<uint64_t>(a.shape[r]) * a.esize, nb = static_cast<uint64_t>(b.shape[r]) * b.esize;
   return from >= na && from + nb <= pitch;
 }
@@ -481,7 +482,8 @@ bool plan_slab(const NormDims& d, NormPlan* P) {
   // a lane's statistics are one pair, or (groups that end inside a chunk) one
   // for each channel of its chunk: those keep to 32 KiB of LDS
   const bool whole = d.per % d.v == 0;
-  const int64_t most = d.backward ? acp::kSlabThreadsBackward : (whole || d.v == 4 ? acp::kSlabThreads : acp::kSlabThreads / 2);
+  const int64_t most = d.backward ? acp::kSlabThreadsBackward
+                                  : (whole || d.v == 4 ? acp::kSlabThreads : acp::kSlabThreads / 2);
   const bool saves = d.block && !d.backward;
   const int64_t cpr = ceil_div(d.c, d.v), align = saves ? d.block / d.v : 1;
   const int64_t unit_c = saves ? lcm64(lcm64(d.per, d.v), d.block) : lcm64(d.per, d.v);
@@ -646,7 +648,8 @@ acp_status norm_geometry(const acp::DescData* const* t, int nt, const NormDims& 
     P.strides[k][1] = !row && o.n >= 2 ? o.stride[k][0] : 0;
     P.strides[k][2] = row ? sample : (o.n >= 1 ? o.stride[k][o.n - 1] : 0);
   }
-  if (static_cast<int64_t>(A.samples) * A.blocks.d * std::max({A.runs.d, P.runs1.d, P.runs2.d}) + d.c / 16 + 1 >= kRowLimit)
+  const int64_t most_runs = std::max({A.runs.d, P.runs1.d, P.runs2.d});
+  if (static_cast<int64_t>(A.samples) * A.blocks.d * most_runs + d.c / 16 + 1 >= kRowLimit)
     return ret(ACP_ERR_UNSUPPORTED, "more than 2^31 workgroups");
   P.text = norm_text(d, P);
   *out = P;
