@@ -356,16 +356,20 @@ __device__ __forceinline__ float normal_tail(float u, float bell) {
   return q * (t * bell);
 }
 
-// u Phi(u) = max(u, 0) - |u| (1 - Phi(|u|))
-__device__ __forceinline__ float gelu(float u, float tail) {
-  return __builtin_fmaf(-__builtin_fabsf(u), tail, __builtin_fmaxf(u, 0.0f));
-}
+// Phi(u)
+__device__ __forceinline__ float normal_cdf(float u, float tail) { return u < 0.0f ? tail : 1.0f - tail; }
 
-// act(u)
-template <int ACT>
+// act(u).  FINITE: u is no infinity, and u Phi(u) = max(u, 0) - |u| (1 -
+// Phi(|u|)) takes two operations less of the VALU time that bounds a large
+// norm with GELU ([128, 500, 1024] float16 2 to 4 % faster, timed in turn).
+template <int ACT, bool FINITE>
 __device__ __forceinline__ float act_value(float u) {
   if constexpr (ACT == kActSilu) return u * sigmoid(u);
-  if constexpr (ACT == kActGelu) return gelu(u, normal_tail(u, normal_bell(u)));
+  if constexpr (ACT == kActGelu) {
+    const float tail = normal_tail(u, normal_bell(u));
+    if constexpr (FINITE) return __builtin_fmaf(-__builtin_fabsf(u), tail, __builtin_fmaxf(u, 0.0f));
+    return u * normal_cdf(u, tail);
+  }
   return u;
 }
 
@@ -378,24 +382,25 @@ __device__ __forceinline__ void act_both(float u, float* value, float* slope) {
     *slope = s * (1.0f + u * (1.0f - s));
   } else if constexpr (ACT == kActGelu) {
     const float bell = normal_bell(u), tail = normal_tail(u, bell);
-    *value = gelu(u, tail);
-    *slope = __builtin_fmaf(u * 0.398942280401432678f, bell, u < 0.0f ? tail : 1.0f - tail);
+    const float cdf = normal_cdf(u, tail);
+    *value = u * cdf;
+    *slope = __builtin_fmaf(u * 0.398942280401432678f, bell, cdf);
   } else {
     *value = u;
     *slope = 1.0f;
   }
 }
 
-template <int ACT, int V>
+template <int ACT, int V, bool FINITE = true>
 __device__ __forceinline__ void act_values(float (&u)[V]) {
 #pragma unroll
-  for (int k = 0; k < V; ++k) u[k] = act_value<ACT>(u[k]);
+  for (int k = 0; k < V; ++k) u[k] = act_value<ACT, FINITE>(u[k]);
 }
 
 template <int V>
 __device__ __forceinline__ void act_values(int act, float (&u)[V]) {
-  if (act == kActSilu) act_values<kActSilu, V>(u);
-  else if (act == kActGelu) act_values<kActGelu, V>(u);
+  if (act == kActSilu) act_values<kActSilu, V, false>(u);
+  else if (act == kActGelu) act_values<kActGelu, V, false>(u);
 }
 
 // value = act(u) and slope = act'(u), channel by channel

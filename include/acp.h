@@ -374,7 +374,8 @@ acp_status acp_pack8(const acp_packed8* out, const acp_tile_desc* x, void* hip_s
  * the output's type. */
 acp_status acp_unpack8(const acp_tile_desc* out, const acp_packed8* in, void* hip_stream);
 
-/* Activations: SILU u / (1 + e^-u), GELU u (1 + erf(u / sqrt 2)) / 2. */
+/* Activations: SILU u / (1 + e^-u), GELU u (1 + erf(u / sqrt 2)) / 2.  Both are
+ * infinite at +infinity, and NaN at -infinity as the formulas are. */
 typedef enum { ACP_ACT_NONE = 0, ACP_ACT_SILU = 1, ACP_ACT_GELU = 2 } acp_activation;
 
 /* out = act(x), or act(x) * z where z is not NULL, computed in float32 and
@@ -410,7 +411,8 @@ acp_status acp_group_norm_workspace(const acp_tile_desc* x, int groups, int64_t*
  *   save         x in 8 bits, written in the pass that normalises; NULL: not
  *                kept
  * A group with a NaN or an infinity, or whose squared deviations overflow
- * float32, gives NaN throughout. */
+ * float32, gives NaN throughout; so does GELU where gamma and beta take its
+ * argument past float32's range. */
 acp_status acp_group_norm(const acp_tile_desc* y, const acp_tile_desc* x, const float* gamma, const float* beta,
                           int groups, float eps, acp_activation act, float* mean, float* rstd,
                           const acp_packed8* save, void* workspace, int64_t workspace_bytes, void* hip_stream);

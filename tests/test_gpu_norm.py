@@ -204,6 +204,14 @@ def test_forms_and_kinds_are_the_ones_meant():
         assert fwd in f and bwd in b, (f, b)
 
 
+def test_backward_slabs_that_walk_many_samples():
+    for dtype in DTYPES:
+        for shape, groups, fmt in (((2100, 5, 64), 8, None), ((1900, 5, 64), 8, "i8"), ((1900, 3, 32), 2, None)):
+            f, b = Case(shape, groups, dtype, "silu", fmt=fmt).run("many samples")
+            assert "slab" in b and int(b.split("runs ")[1]) < shape[0], b
+        Case((2100, 5, 64), 8, dtype, "silu", fmt="i8").run("many samples by parts")
+
+
 @pytest.mark.parametrize("name", ["none", "silu", "gelu"])
 def test_strided_rows_at_odd_offsets(name):
     for k, (shape, groups, pitch) in enumerate([((3, 10, 40), 4, 43), ((2, 3, 5, 24), 3, 25), ((9, 64), 2, 67),

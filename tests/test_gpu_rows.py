@@ -161,6 +161,52 @@ def test_activation_forward_and_backward(dtype, name):
             assert all(t.untouched() for t in (y, plain, dx))
 
 
+@pytest.mark.parametrize("name", ["none", "silu", "gelu"])
+def test_activations_of_values_that_are_not_finite(name):
+    """As the formulas in float64; the largest finite values too."""
+    say(f"activation {name} of infinities")
+    for dtype in DTYPES:
+        v = np.array([[np.inf, -np.inf, np.nan, TOP[dtype], -TOP[dtype], 0.0, -0.0, 1.0, -1.0, 40.0, -40.0]])
+        b, y = Buffer(v.shape, dtype, DEV, values=v), Buffer(v.shape, dtype, DEV)
+        z = Buffer(v.shape, dtype, DEV, values=np.full(v.shape, -2.0))
+        acp.acp_act_forward(name, y.desc, b.desc)
+        g = Buffer(v.shape, dtype, DEV)
+        acp.acp_act_forward(name, g.desc, b.desc, z.desc)
+        torch.cuda.synchronize()
+        u = b.values()
+        with np.errstate(all="ignore"):
+            want = R.act(name, u)
+            gated = want * -2.0
+        # a product past the type's largest value is an infinity
+        gated[np.abs(gated) > TOP[dtype]] *= np.inf
+        for out, w in ((y, want), (g, gated)):
+            got = out.values()
+            fin = np.isfinite(w)
+            assert np.array_equal(got[~fin], w[~fin], equal_nan=True), (dtype, got, w)
+            w, got = np.where(fin, w, 0.0), np.where(fin, got, 0.0)
+            close(got, w, 2 * act_error(name, np.where(fin, u, 0.0)) + np.abs(w) * 2 * U + out_step(dtype, w), dtype)
+
+
+def test_many_ragged_rows_of_a_gated_activation():
+    """More than 2^20 chunks, two to a lane, the last row's block cut short:
+    against the same rows taken few at a time."""
+    say("2^20 chunks and more")
+    rows, c = 2003, 4200
+    x, z, dy = (torch.randn(rows, c, device=DEV).to(torch.float16) for _ in range(3))
+    out = {}
+    for step in (rows, 501):
+        y, dx, dz = (torch.zeros_like(x) for _ in range(3))
+        for at in range(0, rows, step):
+            n = min(step, rows - at)
+            sx, sz = Saved((n, c), "i8", 64, DEV), Saved((n, c), "i8", 64, DEV)
+            d = [acp.acp_encode_tiled("f16", t[at:at + n], (n, c), (c, 1), (1, 1)) for t in (y, x, z, dx, dz, dy)]
+            acp.acp_act_forward("gelu", d[0], d[1], d[2], sx.packed, sz.packed)
+            acp.acp_act_backward("gelu", d[3], d[4], d[5], sx.packed, sz.packed)
+            torch.cuda.synchronize()
+        out[step] = torch.stack([y, dx, dz])
+    assert torch.equal(out[rows].view(torch.int16), out[501].view(torch.int16))
+
+
 def test_the_halves_of_a_fused_projection():
     """Gate and operand, their gradients and their codes each side by side in
     one buffer."""
