@@ -22,8 +22,11 @@ struct Source {
       : codes(walk_codes<V, LINEAR>(A, A.codes, w)), scales(walk_scales<LINEAR>(A, A.scales, w)) {}
   template <bool KEEP>
   __device__ __forceinline__ void load(const NormCore& A, uint32_t k, int n, Raw* r) const {
-    r->codes = load_codes<V, KEEP, TAIL>(codes.at(A, k), n);
+    r->codes = load_codes<V, KEEP, TAIL>(codes.at(A, k), n, A.c >= V);
     r->s = n > 0 ? *reinterpret_cast<const float*>(scales.at(A, k)) : 0.0f;
+  }
+  __device__ static __forceinline__ void place(const NormCore& A, int n, Raw* r) {
+    place_codes<V, TAIL>(&r->codes, n, A.c >= V);
   }
   // z = x rstd - mu rstd, one fma from a code, whose scale joins rstd.  The
   // rounding of mu rstd moves z by half an ulp of it, as the rounding of mu to
@@ -48,7 +51,10 @@ struct Source<T, KIND, 0> {
   __device__ __forceinline__ Source(const NormBackward& A, const Spot& w) : x(walk<T, LINEAR>(A, A.x, w)) {}
   template <bool KEEP>
   __device__ __forceinline__ void load(const NormCore& A, uint32_t k, int n, Raw* r) const {
-    r->raw = load_chunk<T, KEEP, TAIL>(x.at(A, k), n);
+    r->raw = load_chunk<T, KEEP, TAIL>(x.at(A, k), n, A.c >= V);
+  }
+  __device__ static __forceinline__ void place(const NormCore& A, int n, Raw* r) {
+    place_tail<T, TAIL>(&r->raw, n, A.c >= V);
   }
   template <class P>
   __device__ static __forceinline__ void z(const Raw& r, const P& st, float (&v)[V]) {
@@ -253,7 +259,7 @@ __global__ __launch_bounds__(kRowThreadsBackward) void norm_row_backward_kernel(
   auto load = [&](uint32_t k, int u) {
     const int n = w.channels(A, k);
     src.template load<false>(A, k, n, &rx[u]);
-    rd[u] = load_chunk<T, false, false>(pd.at(A, k), n);
+    rd[u] = load_chunk<T, false, false>(pd.at(A, k), n, A.c >= V);
     const uint64_t at = static_cast<uint64_t>(w.r0 + w.rl + k * w.step) * A.groups + g;
     stat[u] = n > 0 ? make_float2(A.mean[at], A.rstd[at]) : make_float2(0.0f, 0.0f);
   };
@@ -350,7 +356,7 @@ __global__ __launch_bounds__(kSlabThreadsBackward) void norm_slab_backward_kerne
       if (u * A.row_lanes < w.rows) {
         const int n = w.channels(A, u);
         src.template load<false>(A, u, n, &rx[u]);
-        rd[u] = load_chunk<T, false, TAIL>(pd.at(A, u), n);
+        rd[u] = load_chunk<T, false, TAIL>(pd.at(A, u), n, A.c >= V);
       }
     }
     Pairs<V, WHOLE> st;
@@ -362,6 +368,8 @@ __global__ __launch_bounds__(kSlabThreadsBackward) void norm_slab_backward_kerne
     for (int u = 0; u < U; ++u) {
       if (u * A.row_lanes >= w.rows) break;
       float z[V];
+      src.place(A, w.channels(A, u), &rx[u]);
+      place_tail<T, TAIL>(&rd[u], w.channels(A, u), A.c >= V);
       src.z(rx[u], st, z);
       widen(rd[u], a[u], static_cast<const T*>(nullptr));
       times_slope<ACT>(p, z, a[u]);
@@ -432,7 +440,7 @@ __global__ __launch_bounds__(kRowThreads) void norm_sums_kernel(const BackwardAr
   for (int u = 0; u < U; ++u) {
     const int n = w.channels(A, u);
     src.template load<true>(A, u, n, &rx[u]);
-    rd[u] = load_chunk<T, true, TAIL>(pd.at(A, u), n);
+    rd[u] = load_chunk<T, true, TAIL>(pd.at(A, u), n, A.c >= V);
   }
   Params<V> p(A, w.c, w.valid);
   float2* chan = lds + blockDim.x * (V + 1);
@@ -450,11 +458,13 @@ __global__ __launch_bounds__(kRowThreads) void norm_sums_kernel(const BackwardAr
       for (int u = 0; u < U; ++u) {
         if ((k0 + u) * w.step >= w.rows) break;
         float z[V], a[V];
+        src.place(A, w.channels(A, k0 + u), &rx[u]);
+        place_tail<T, TAIL>(&rd[u], w.channels(A, k0 + u), A.c >= V);
         src.z(rx[u], st, z);
         widen(rd[u], a, static_cast<const T*>(nullptr));
         const int next = w.channels(A, k0 + U + u);
         src.template load<true>(A, k0 + U + u, next, &rx[u]);
-        rd[u] = load_chunk<T, true, TAIL>(pd.at(A, k0 + U + u), next);
+        rd[u] = load_chunk<T, true, TAIL>(pd.at(A, k0 + U + u), next, A.c >= V);
         times_slope_scaled<ACT>(p, z, a);
         if (w.channels(A, k0 + u) > 0) {
 #pragma unroll
@@ -535,7 +545,7 @@ __global__ __launch_bounds__(kRowThreads) void norm_dx_kernel(const BackwardArgs
   for (int u = 0; u < U; ++u) {
     const int n = w.channels(A, u);
     src.template load<false>(A, u, n, &rx[u]);
-    rd[u] = load_chunk<T, false, TAIL>(pd.at(A, u), n);
+    rd[u] = load_chunk<T, false, TAIL>(pd.at(A, u), n, A.c >= V);
   }
   Params<V> p(A, w.c, w.valid);
   Pairs<V, WHOLE> st, cf;
@@ -560,11 +570,13 @@ __global__ __launch_bounds__(kRowThreads) void norm_dx_kernel(const BackwardArgs
       const int n = w.channels(A, k0 + u);
       if (n == 0) return;
       float z[V], a[V];
+      src.place(A, n, &rx[u]);
+      place_tail<T, TAIL>(&rd[u], n, A.c >= V);
       src.z(rx[u], st, z);
       widen(rd[u], a, static_cast<const T*>(nullptr));
       const int next = w.channels(A, k0 + U + u);
       src.template load<false>(A, k0 + U + u, next, &rx[u]);
-      rd[u] = load_chunk<T, false, TAIL>(pd.at(A, k0 + U + u), next);
+      rd[u] = load_chunk<T, false, TAIL>(pd.at(A, k0 + U + u), next, A.c >= V);
       times_slope_scaled<ACT>(p, z, a);
 #pragma unroll
       for (int e = 0; e < V; ++e)

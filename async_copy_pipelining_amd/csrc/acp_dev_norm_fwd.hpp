@@ -52,7 +52,7 @@ __global__ __launch_bounds__(kRowThreads) void norm_row_kernel(const ForwardArgs
   const Walk<true> px = walk<T, true>(A, A.x, w), py = walk<T, true>(A, A.y, w);
   rw4 raw[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) raw[u] = load_chunk<T, false, false>(px.at(A, u), w.channels(A, u));
+  for (int u = 0; u < U; ++u) raw[u] = load_chunk<T, false, false>(px.at(A, u), w.channels(A, u), A.c >= V);
   const Saver<T, kNormWhole, PK> saver(A, w);
   const Params<V> p(A, w.c, w.valid);
   const float inv = 1.0f / static_cast<float>(A.per_group);
@@ -66,7 +66,7 @@ __global__ __launch_bounds__(kRowThreads) void norm_row_kernel(const ForwardArgs
       const int n = w.channels(A, k0 + u);
       float x[V];
       widen(raw[u], x, static_cast<const T*>(nullptr));
-      raw[u] = load_chunk<T, false, false>(px.at(A, k0 + U + u), w.channels(A, k0 + U + u));
+      raw[u] = load_chunk<T, false, false>(px.at(A, k0 + U + u), w.channels(A, k0 + U + u), A.c >= V);
       if constexpr (PK != 0) saver.save(A, w, k0 + u, n, x);
       float sum = 0.0f;
 #pragma unroll
@@ -111,12 +111,13 @@ __global__ __launch_bounds__(kSlabThreads) void norm_slab_kernel(const ForwardAr
   rw4 raw[U];
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    if (u * A.row_lanes < w.rows) raw[u] = load_chunk<T, false, TAIL>(px.at(A, u), w.channels(A, u));
+    if (u * A.row_lanes < w.rows) raw[u] = load_chunk<T, false, TAIL>(px.at(A, u), w.channels(A, u), A.c >= V);
   LaneStats<V, WHOLE> st;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if (u * A.row_lanes >= w.rows) break;
     float x[V];
+    place_tail<T, TAIL>(&raw[u], w.channels(A, u), A.c >= V);
     widen(raw[u], x, static_cast<const T*>(nullptr));
     if (u == 0) st.first(x);
     if (w.channels(A, u) > 0) st.add(x);
@@ -190,10 +191,11 @@ __global__ __launch_bounds__(kRowThreads) void norm_stats_kernel(const NormStats
     for (uint32_t k0 = 0; k0 * w.step < w.rows; k0 += U) {
       rw4 raw[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) raw[u] = load_chunk<T, true, TAIL>(px.at(A, k0 + u), w.channels(A, k0 + u));
+      for (int u = 0; u < U; ++u) raw[u] = load_chunk<T, true, TAIL>(px.at(A, k0 + u), w.channels(A, k0 + u), A.c >= V);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         float x[V];
+        place_tail<T, TAIL>(&raw[u], w.channels(A, k0 + u), A.c >= V);
         widen(raw[u], x, static_cast<const T*>(nullptr));
         if (k0 == 0 && u == 0) st.first(x);
         if (w.channels(A, k0 + u) > 0) st.add(x);
@@ -280,7 +282,7 @@ __global__ __launch_bounds__(kRowThreads) void norm_apply_kernel(const ForwardAr
   const Saver<T, KIND, PK> saver(A, w);
   rw4 raw[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) raw[u] = load_chunk<T, false, TAIL>(px.at(A, u), w.channels(A, u));
+  for (int u = 0; u < U; ++u) raw[u] = load_chunk<T, false, TAIL>(px.at(A, u), w.channels(A, u), A.c >= V);
   const Params<V> p(A, w.c, w.valid);
   const uint32_t width = A.lanes.d * V;
   const BlockGroups b(A, w.blk, width);
@@ -317,8 +319,9 @@ __global__ __launch_bounds__(kRowThreads) void norm_apply_kernel(const ForwardAr
       if ((k0 + u) * w.step >= w.rows) break;
       const int n = w.channels(A, k0 + u);
       float x[V];
+      place_tail<T, TAIL>(&raw[u], n, A.c >= V);
       widen(raw[u], x, static_cast<const T*>(nullptr));
-      raw[u] = load_chunk<T, false, TAIL>(px.at(A, k0 + U + u), w.channels(A, k0 + U + u));
+      raw[u] = load_chunk<T, false, TAIL>(px.at(A, k0 + U + u), w.channels(A, k0 + U + u), A.c >= V);
       if constexpr (PK != 0) saver.save(A, w, k0 + u, n, x);
 #pragma unroll
       for (int e = 0; e < V; ++e) x[e] = __builtin_fmaf(x[e] - mu[e], scale[e], p.beta[e]);

@@ -38,7 +38,7 @@ struct Chunk {
   }
 };
 
-template <class T, int V>
+template <class T, int V, bool TAIL>
 __device__ __forceinline__ void save_chunk(const RowsCore& A, const Packed& p, const Chunk& k, uint32_t i,
                                            const float (&v)[V]) {
   float x[V];
@@ -47,7 +47,7 @@ __device__ __forceinline__ void save_chunk(const RowsCore& A, const Packed& p, c
   const float s = block_scale(A.format, block_amax(x, A.lb_log2));
   const Codes<V> c = encode<T>(A.format, x, s);
   if (k.n > 0) {
-    store_codes<V>(k.at(p.codes, 1), k.n, c);
+    store_codes<V, TAIL>(k.at(p.codes, 1), k.n, c);
     if ((i & ((1u << A.lb_log2) - 1u)) == 0) p.scales[i >> A.lb_log2] = s;
   }
 }
@@ -57,7 +57,7 @@ __device__ __forceinline__ void saved_chunk(const RowsCore& A, const Codes<V>& c
   decode(A.format, c, s, x);
 }
 
-template <class T, int U>
+template <class T, int U, bool TAIL>
 __global__ __launch_bounds__(kRowThreads) void pack8_kernel(const RowsUse<1, 1> A) {
   constexpr int V = kChunk<T>;
   const uint32_t i0 = blockIdx.x * (blockDim.x * U) + threadIdx.x;
@@ -65,19 +65,20 @@ __global__ __launch_bounds__(kRowThreads) void pack8_kernel(const RowsUse<1, 1> 
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const Chunk k(A, i0 + u * blockDim.x, V);
-    r[u] = load_chunk<T>(k.at(A.t[0], sizeof(T)), k.n);
+    r[u] = load_chunk<T, false, TAIL>(k.at(A.t[0], sizeof(T)), k.n, A.c >= V);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const uint32_t i = i0 + u * blockDim.x;
     const Chunk k(A, i, V);
     float x[V];
+    place_tail<T, TAIL>(&r[u], k.n, A.c >= V);
     widen(r[u], x, static_cast<const T*>(nullptr));
-    save_chunk<T, V>(A, A.p[0], k, i, x);
+    save_chunk<T, V, TAIL>(A, A.p[0], k, i, x);
   }
 }
 
-template <class T, int U>
+template <class T, int U, bool TAIL>
 __global__ __launch_bounds__(kRowThreads) void unpack8_kernel(const RowsUse<1, 1> A) {
   constexpr int V = kChunk<T>;
   const uint32_t i0 = blockIdx.x * (blockDim.x * U) + threadIdx.x;
@@ -87,22 +88,23 @@ __global__ __launch_bounds__(kRowThreads) void unpack8_kernel(const RowsUse<1, 1
   for (int u = 0; u < U; ++u) {
     const uint32_t i = i0 + u * blockDim.x;
     const Chunk k(A, i, V);
-    c[u] = load_codes<V>(k.at(A.p[0].codes, 1), k.n);
+    c[u] = load_codes<V, false, TAIL>(k.at(A.p[0].codes, 1), k.n, A.c >= V);
     s[u] = k.n > 0 ? A.p[0].scales[i >> A.lb_log2] : 0.0f;
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const Chunk k(A, i0 + u * blockDim.x, V);
     float x[V];
+    place_codes<V, TAIL>(&c[u], k.n, A.c >= V);
     saved_chunk<V>(A, c[u], s[u], x);
-    if (k.n > 0) store_chunk<T>(k.at(A.t[0], sizeof(T)), k.n, narrow(x, static_cast<const T*>(nullptr)));
+    if (k.n > 0) store_chunk<T, TAIL>(k.at(A.t[0], sizeof(T)), k.n, narrow(x, static_cast<const T*>(nullptr)));
   }
 }
 
 // y = act(x) [* z], and x [and z] kept in 8 bits: the codes cost a third of
 // the bytes that the activation itself moves, where a pass of their own would
 // read the operands again.
-template <class T, bool GATED, bool SAVE, int U>
+template <class T, bool GATED, bool SAVE, int U, bool TAIL>
 __global__ __launch_bounds__(kRowThreads) void act_forward_kernel(
     const RowsUse<GATED ? 3 : 2, SAVE ? (GATED ? 2 : 1) : 0> A) {
   constexpr int V = kChunk<T>;
@@ -111,30 +113,32 @@ __global__ __launch_bounds__(kRowThreads) void act_forward_kernel(
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const Chunk k(A, i0 + u * blockDim.x, V);
-    rx[u] = load_chunk<T>(k.at(A.t[0], sizeof(T)), k.n);
-    if constexpr (GATED) rz[u] = load_chunk<T>(k.at(A.t[2], sizeof(T)), k.n);
+    rx[u] = load_chunk<T, false, TAIL>(k.at(A.t[0], sizeof(T)), k.n, A.c >= V);
+    if constexpr (GATED) rz[u] = load_chunk<T, false, TAIL>(k.at(A.t[2], sizeof(T)), k.n, A.c >= V);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const uint32_t i = i0 + u * blockDim.x;
     const Chunk k(A, i, V);
     float x[V], z[V];
+    place_tail<T, TAIL>(&rx[u], k.n, A.c >= V);
     widen(rx[u], x, static_cast<const T*>(nullptr));
-    if constexpr (SAVE) save_chunk<T, V>(A, A.p[0], k, i, x);
+    if constexpr (SAVE) save_chunk<T, V, TAIL>(A, A.p[0], k, i, x);
     act_values(A.act, x);
     if constexpr (GATED) {
+      place_tail<T, TAIL>(&rz[u], k.n, A.c >= V);
       widen(rz[u], z, static_cast<const T*>(nullptr));
-      if constexpr (SAVE) save_chunk<T, V>(A, A.p[1], k, i, z);
+      if constexpr (SAVE) save_chunk<T, V, TAIL>(A, A.p[1], k, i, z);
 #pragma unroll
       for (int e = 0; e < V; ++e) x[e] *= z[e];
     }
-    if (k.n > 0) store_chunk<T>(k.at(A.t[1], sizeof(T)), k.n, narrow(x, static_cast<const T*>(nullptr)));
+    if (k.n > 0) store_chunk<T, TAIL>(k.at(A.t[1], sizeof(T)), k.n, narrow(x, static_cast<const T*>(nullptr)));
   }
 }
 
 // dx = dy act'(x) [* z], dz = dy act(x), with x and z from their 8-bit forms.
 // Value and slope share their exponential (silu) or tail (gelu).
-template <class T, bool GATED, int U>
+template <class T, bool GATED, int U, bool TAIL>
 __global__ __launch_bounds__(kRowThreads) void act_backward_kernel(const RowsUse<GATED ? 3 : 2, GATED ? 2 : 1> A) {
   constexpr int V = kChunk<T>;
   const uint32_t i0 = blockIdx.x * (blockDim.x * U) + threadIdx.x;
@@ -145,11 +149,11 @@ __global__ __launch_bounds__(kRowThreads) void act_backward_kernel(const RowsUse
   for (int u = 0; u < U; ++u) {
     const uint32_t i = i0 + u * blockDim.x;
     const Chunk k(A, i, V);
-    rd[u] = load_chunk<T>(k.at(A.t[0], sizeof(T)), k.n);
-    cx[u] = load_codes<V>(k.at(A.p[0].codes, 1), k.n);
+    rd[u] = load_chunk<T, false, TAIL>(k.at(A.t[0], sizeof(T)), k.n, A.c >= V);
+    cx[u] = load_codes<V, false, TAIL>(k.at(A.p[0].codes, 1), k.n, A.c >= V);
     sx[u] = k.n > 0 ? A.p[0].scales[i >> A.lb_log2] : 0.0f;
     if constexpr (GATED) {
-      cz[u] = load_codes<V>(k.at(A.p[1].codes, 1), k.n);
+      cz[u] = load_codes<V, false, TAIL>(k.at(A.p[1].codes, 1), k.n, A.c >= V);
       sz[u] = k.n > 0 ? A.p[1].scales[i >> A.lb_log2] : 0.0f;
     }
   }
@@ -157,6 +161,8 @@ __global__ __launch_bounds__(kRowThreads) void act_backward_kernel(const RowsUse
   for (int u = 0; u < U; ++u) {
     const Chunk k(A, i0 + u * blockDim.x, V);
     float d[V], x[V], value[V], slope[V];
+    place_tail<T, TAIL>(&rd[u], k.n, A.c >= V);
+    place_codes<V, TAIL>(&cx[u], k.n, A.c >= V);
     widen(rd[u], d, static_cast<const T*>(nullptr));
     saved_chunk<V>(A, cx[u], sx[u], x);
     act_pairs(A.act, x, value, slope);
@@ -164,21 +170,25 @@ __global__ __launch_bounds__(kRowThreads) void act_backward_kernel(const RowsUse
     for (int e = 0; e < V; ++e) slope[e] *= d[e];
     if constexpr (GATED) {
       float z[V];
+      place_codes<V, TAIL>(&cz[u], k.n, A.c >= V);
       saved_chunk<V>(A, cz[u], sz[u], z);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         slope[e] *= z[e];
         value[e] *= d[e];
       }
-      if (k.n > 0) store_chunk<T>(k.at(A.t[2], sizeof(T)), k.n, narrow(value, static_cast<const T*>(nullptr)));
+      if (k.n > 0) store_chunk<T, TAIL>(k.at(A.t[2], sizeof(T)), k.n, narrow(value, static_cast<const T*>(nullptr)));
     }
-    if (k.n > 0) store_chunk<T>(k.at(A.t[1], sizeof(T)), k.n, narrow(slope, static_cast<const T*>(nullptr)));
+    if (k.n > 0) store_chunk<T, TAIL>(k.at(A.t[1], sizeof(T)), k.n, narrow(slope, static_cast<const T*>(nullptr)));
   }
 }
 
 }  // namespace dev
 
 namespace {
+
+template <int I>
+using Int = std::integral_constant<int, I>;
 
 // Up to this many chunks lanes take one each, so that a call spreads over the
 // CUs and a wave's code is short enough to come in quickly; past it two, for
@@ -189,14 +199,18 @@ namespace {
 // with four).
 constexpr uint32_t kOneChunk = 1u << 20;
 
-template <class A>
-hipError_t launch_rows(void (*one)(A), void (*two)(A), const A& a, hipStream_t s) {
-  const bool few = a.total <= kOneChunk;
-  const uint32_t per = kRowThreads * (few ? 1u : 2u);
+// `kernel(one, tail)`: the kernel with one chunk a lane or two, for rows whose
+// last chunk is cut short or not.
+template <class T, class A, class F>
+hipError_t launch_rows(const A& a, hipStream_t s, F kernel) {
+  const bool one = a.total <= kOneChunk, tail = a.c % dev::kChunk<T> != 0;
+  const uint32_t per = kRowThreads * (one ? 1u : 2u);
   const uint32_t grid = a.total / per + (a.total % per ? 1u : 0u);
   A u = a;
   void* args[] = {&u};
-  return hipLaunchKernel(reinterpret_cast<const void*>(few ? one : two), dim3(grid), dim3(kRowThreads), args, 0, s);
+  auto pick = [&](auto t) { return one ? kernel(Int<1>(), t) : kernel(Int<2>(), t); };
+  return hipLaunchKernel(reinterpret_cast<const void*>(tail ? pick(std::true_type()) : pick(std::false_type())),
+                         dim3(grid), dim3(kRowThreads), args, 0, s);
 }
 
 // A kernel's arguments out of a call's.
@@ -214,20 +228,21 @@ RowsUse<NT, NP> use(const RowsArgs& a, const RowTensor& t0, const RowTensor& t1,
 
 template <class T>
 hipError_t pack8_t(const RowsArgs& a, hipStream_t s) {
-  return launch_rows<RowsUse<1, 1>>(dev::pack8_kernel<T, 1>, dev::pack8_kernel<T, 2>, use<1, 1>(a, a.x, a.x, a.x), s);
+  return launch_rows<T>(use<1, 1>(a, a.x, a.x, a.x), s,
+                        [](auto u, auto tail) { return dev::pack8_kernel<T, u(), tail()>; });
 }
 
 template <class T>
 hipError_t unpack8_t(const RowsArgs& a, hipStream_t s) {
-  return launch_rows<RowsUse<1, 1>>(dev::unpack8_kernel<T, 1>, dev::unpack8_kernel<T, 2>, use<1, 1>(a, a.y, a.y, a.y),
-                                    s);
+  return launch_rows<T>(use<1, 1>(a, a.y, a.y, a.y), s,
+                        [](auto u, auto tail) { return dev::unpack8_kernel<T, u(), tail()>; });
 }
 
 template <class T, bool GATED, bool SAVE>
 hipError_t act_forward_t(const RowsArgs& a, hipStream_t s) {
   constexpr int NT = GATED ? 3 : 2, NP = SAVE ? (GATED ? 2 : 1) : 0;
-  return launch_rows<RowsUse<NT, NP>>(dev::act_forward_kernel<T, GATED, SAVE, 1>,
-                                      dev::act_forward_kernel<T, GATED, SAVE, 2>, use<NT, NP>(a, a.x, a.y, a.z), s);
+  return launch_rows<T>(use<NT, NP>(a, a.x, a.y, a.z), s,
+                        [](auto u, auto tail) { return dev::act_forward_kernel<T, GATED, SAVE, u(), tail()>; });
 }
 
 template <class T>
@@ -239,8 +254,8 @@ hipError_t act_forward_t(bool gated, bool save, const RowsArgs& a, hipStream_t s
 template <class T, bool GATED>
 hipError_t act_backward_t(const RowsArgs& a, hipStream_t s) {
   constexpr int NT = GATED ? 3 : 2, NP = GATED ? 2 : 1;
-  return launch_rows<RowsUse<NT, NP>>(dev::act_backward_kernel<T, GATED, 1>, dev::act_backward_kernel<T, GATED, 2>,
-                                      use<NT, NP>(a, a.dy, a.dx, a.dz), s);
+  return launch_rows<T>(use<NT, NP>(a, a.dy, a.dx, a.dz), s,
+                        [](auto u, auto tail) { return dev::act_backward_kernel<T, GATED, u(), tail()>; });
 }
 
 }  // namespace
