@@ -204,6 +204,14 @@ def test_forms_and_kinds_are_the_ones_meant():
         assert fwd in f and bwd in b, (f, b)
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_rows_of_every_length_to_a_few_chunks(dtype):
+    for c in range(1, 21):
+        for rows in (9, 3000):
+            Case((2, rows, c), 1 if c % 3 else 3, dtype, ("none", "silu", "gelu")[c % 3], seed=c, pitch=c + c % 2,
+                 fmt=(None, "i8", "e4m3")[c % 3], block=32).run("every length")
+
+
 def test_backward_slabs_that_walk_many_samples():
     for dtype in DTYPES:
         for shape, groups, fmt in (((2100, 5, 64), 8, None), ((1900, 5, 64), 8, "i8"), ((1900, 3, 32), 2, None)):

@@ -187,11 +187,12 @@ def test_activations_of_values_that_are_not_finite(name):
             close(got, w, 2 * act_error(name, np.where(fin, u, 0.0)) + np.abs(w) * 2 * U + out_step(dtype, w), dtype)
 
 
-def test_many_ragged_rows_of_a_gated_activation():
+@pytest.mark.parametrize("c", [4200, 4203])
+def test_many_ragged_rows_of_a_gated_activation(c):
     """More than 2^20 chunks, two to a lane, the last row's block cut short:
     against the same rows taken few at a time."""
     say("2^20 chunks and more")
-    rows, c = 2003, 4200
+    rows = 2003
     x, z, dy = (torch.randn(rows, c, device=DEV).to(torch.float16) for _ in range(3))
     out = {}
     for step in (rows, 501):
@@ -205,6 +206,32 @@ def test_many_ragged_rows_of_a_gated_activation():
             torch.cuda.synchronize()
         out[step] = torch.stack([y, dx, dz])
     assert torch.equal(out[rows].view(torch.int16), out[501].view(torch.int16))
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_rows_of_every_length_to_a_few_chunks(dtype):
+    for c in range(1, 21):
+        fmt = ("i8", "e4m3")[c % 2]
+        say(f"rows of {c} {dtype} {fmt}")
+        x, z, dy = draw((5, c), dtype, c), draw((5, c), dtype, 30 + c, c + 1), draw((5, c), dtype, 60 + c)
+        y, back, dx, dz = (Buffer((5, c), dtype, DEV, c + j, j) for j in range(4))
+        sx, sz = Saved((5, c), fmt, 32, DEV), Saved((5, c), fmt, 32, DEV, c + 3, 1)
+        acp.acp_act_forward("silu", y.desc, x.desc, z.desc, sx.packed, sz.packed)
+        acp.acp_unpack8(back.desc, sx.packed)
+        acp.acp_act_backward("silu", dx.desc, dz.desc, dy.desc, sx.packed, sz.packed)
+        torch.cuda.synchronize()
+        v, zv, d = x.values(), z.values(), dy.values()
+        check_saved(sx, v, c, dtype)
+        check_saved(sz, zv, c, dtype)
+        xs, zs = (R.unpack(*t.host(), fmt, 32).astype(np.float32).astype(np.float64) for t in (sx, sz))
+        close(back.values(), xs, np.abs(xs) * U + out_step(dtype, xs), "unpacked")
+        want = R.act("silu", v) * zv
+        close(y.values(), want, np.abs(zv) * act_error("silu", v) + np.abs(want) * 2 * U + out_step(dtype, want), "y")
+        wx, wz = R.act_backward("silu", d, xs, zs)
+        err = np.abs(d) * act_error("silu", xs)
+        close(dx.values(), wx, np.abs(zs) * err + np.abs(wx) * 4 * U + out_step(dtype, wx), "dx")
+        close(dz.values(), wz, err + np.abs(wz) * 4 * U + out_step(dtype, wz), "dz")
+        assert all(t.untouched() for t in (y, back, dx, dz))
 
 
 def test_the_halves_of_a_fused_projection():
