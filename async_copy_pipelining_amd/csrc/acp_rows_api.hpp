@@ -516,7 +516,12 @@ bool plan_slab(const NormDims& d, NormPlan* P) {
   // 126 and 99; [128, 500, 1024] in blocks of 64 bytes 132 and 117) or whose
   // codes end inside one ([512, 256, 1024] from 8 bits 63 us more)
   const bool lines = whole && !d.block && lanes % kSlabLanes == 0;
-  if (d.backward && !lines && d.samples * blocks * threads > 256 * 512) return false;
+  // Samples of a few rows: by parts, each would leave as many bytes of sums as
+  // it has data ([4924, 232] float16, 8 groups 66 us by parts, 27 as slabs;
+  // [4000, 3, 333] bfloat16 78 and 46, but with ten rows 91 and 95; from 8 bits
+  // [4000, 4, 640] forward and backward 86 and 95)
+  const bool few_rows = d.rows <= (d.block ? 1 : 4);
+  if (d.backward && !lines && !few_rows && d.samples * blocks * threads > 256 * 512) return false;
   // LDS that a launch may ask for without raising the kernel's limit
   const int64_t pairs = d.backward ? threads * (d.v + 1) + lanes * d.v * 5 / 2 : threads * (whole ? 1 : d.v);
   if ((pairs + lanes * d.v / d.per + 3) * 8 > 65536) return false;

@@ -218,6 +218,9 @@ def test_backward_slabs_that_walk_many_samples():
             f, b = Case(shape, groups, dtype, "silu", fmt=fmt).run("many samples")
             assert "slab" in b and int(b.split("runs ")[1]) < shape[0], b
         Case((2100, 5, 64), 8, dtype, "silu", fmt="i8").run("many samples by parts")
+        for shape, groups, fmt in (((4924, 232), 8, None), ((4924, 232), 8, "i8"), ((3000, 3, 333), 9, None)):
+            f, b = Case(shape, groups, dtype, "gelu", fmt=fmt).run("many short samples")
+            assert "slab" in b, b
 
 
 @pytest.mark.parametrize("name", ["none", "silu", "gelu"])
