@@ -78,7 +78,9 @@ __global__ __launch_bounds__(kRowThreads) void norm_row_kernel(const ForwardArgs
         x[e] -= m;
         sq = __builtin_fmaf(x[e], x[e], sq);
       }
-      const float rstd = rsqrt_any(__builtin_fmaf(sum_lanes(sq, A.group_lanes_log2), inv, A.eps));
+      sq = sum_lanes(sq, A.group_lanes_log2);
+      // squares past float32: NaN, as join_lanes has it, not a root of zero
+      const float rstd = rsqrt_any(__builtin_fmaf(sq - sq == 0.0f ? sq : as_float(0x7FC00000u), inv, A.eps));
       if (n > 0 && lead) {
         const uint64_t at = static_cast<uint64_t>(w.r0 + w.rl + (k0 + u) * w.step) * A.groups + g;
         if (A.mean) A.mean[at] = m;
