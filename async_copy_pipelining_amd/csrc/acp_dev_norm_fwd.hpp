@@ -68,10 +68,12 @@ __global__ __launch_bounds__(kRowThreads) void norm_row_kernel(const ForwardArgs
       widen(raw[u], x, static_cast<const T*>(nullptr));
       raw[u] = load_chunk<T, false, false>(px.at(A, k0 + U + u), w.channels(A, k0 + U + u), A.c >= V);
       if constexpr (PK != 0) saver.save(A, w, k0 + u, n, x);
+      // 1 / channels is a power of two here: each term divided by it keeps its
+      // bits, and no sum of finite values is past float32
       float sum = 0.0f;
 #pragma unroll
-      for (int e = 0; e < V; ++e) sum += x[e];
-      const float m = sum_lanes(sum, A.group_lanes_log2) * inv;
+      for (int e = 0; e < V; ++e) sum = __builtin_fmaf(x[e], inv, sum);
+      const float m = sum_lanes(sum, A.group_lanes_log2);
       float sq = 0.0f;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
