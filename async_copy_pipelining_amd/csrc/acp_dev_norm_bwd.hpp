@@ -103,7 +103,7 @@ __device__ __forceinline__ void times_slope(const Params<V>& p, const float (&z)
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       float value, slope;
-      act_both<ACT>(__builtin_fmaf(z[e], p.gamma[e], p.beta[e]), &value, &slope);
+      act_both<ACT, kFine<V>>(__builtin_fmaf(z[e], p.gamma[e], p.beta[e]), &value, &slope);
       dy[e] *= slope;
     }
   }

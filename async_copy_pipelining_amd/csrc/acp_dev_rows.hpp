@@ -369,29 +369,55 @@ __device__ __forceinline__ uint32_t block_amax(const float (&x)[V], int lb) {
 constexpr int kActNone = 0, kActSilu = 1, kActGelu = 2;
 
 // 1 / (1 + e^-u): the hardware exponential and reciprocal, each within an
-// ulp; the argument's rounding adds |u| 2^-24 relative, under 2^-20 where the
-// result is not negligible.
+// ulp.  Below zero the argument's rounding and its constant's add 1.25 |u| 2^-24
+// relative: 2^-20 at u = -10, where the result is 5e-5.
 __device__ __forceinline__ float sigmoid(float u) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u * -1.44269504088896341f));
 }
 
 // e^(-u^2 / 2), and the normal distribution's tail from it:
-// 1 - Phi(|u|) = e^(-u^2 / 2) (a1 t + ... + a5 t^5) / 2 with
-// t = 1 / (1 + p |u| / sqrt 2), formula 7.1.26 of Abramowitz and Stegun's
-// Handbook of Mathematical Functions, whose erf is off by at most 1.5e-7.
-// One exponential and one reciprocal; it keeps its digits for large negative
-// u, where 1 + erf loses them.
+//   1 - Phi(|u|) = e^(-u^2 / 2) (a1 t + ... + an t^n),  t = 1 / (1 + p |u|),
+// the form of formula 7.1.26 in Abramowitz and Stegun's Handbook of
+// Mathematical Functions.  Its constants there bound the absolute error of erf
+// and leave the tail 5e-5 off at |u| = 3 and 2e-2 at 10, relative to itself;
+// those below were fitted to the tail's relative error over |u| <= 14.5, since
+// u Phi(u) below zero is as small as the tail.  What is left beside float32's
+// roundings:
+//   FINE  (float32)  3.5e-8 everywhere, nine terms, and a bell whose argument
+//         keeps what its products round off: the tail is within 2^-20
+//   else  (16 bits)  2.9e-7 (1 + 4 u^2), six terms; the bell's argument adds
+//         2^-24 * 1.5 u^2.  1e-5 at |u| = 2, 1.5e-4 at 13, where half a step of
+//         float16 is 4.9e-4
+// Past |u| = 13.2 the bell is below float32's normal range and so is the tail.
+template <bool FINE>
 __device__ __forceinline__ float normal_bell(float u) {
-  return __builtin_amdgcn_exp2f(u * u * -0.721347520444481704f);
+  constexpr double kExact = -0.72134752044448170368;  // -log2(e) / 2
+  constexpr float kHigh = static_cast<float>(kExact);
+  const float sq = u * u, arg = sq * kHigh;
+  const float bell = __builtin_amdgcn_exp2f(arg);
+  if constexpr (!FINE) return bell;
+  constexpr float kLow = static_cast<float>(kExact - static_cast<double>(kHigh));
+  float off = __builtin_fmaf(sq, kHigh, -arg);
+  off = __builtin_fmaf(__builtin_fmaf(u, u, -sq), kHigh, off);
+  off = __builtin_fmaf(sq, kLow, off);
+  // where the bell is zero its argument may be infinite, and `off` a NaN
+  return bell > 0.0f ? __builtin_fmaf(bell * 0.693147180559945309f, off, bell) : bell;
 }
 
 // 1 - Phi(|u|)
+template <bool FINE>
 __device__ __forceinline__ float normal_tail(float u, float bell) {
-  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(__builtin_fabsf(u), 0.3275911f * 0.707106781186547524f, 1.0f));
-  float q = __builtin_fmaf(t, 1.061405429f * 0.5f, -1.453152027f * 0.5f);
-  q = __builtin_fmaf(t, q, 1.421413741f * 0.5f);
-  q = __builtin_fmaf(t, q, -0.284496736f * 0.5f);
-  q = __builtin_fmaf(t, q, 0.254829592f * 0.5f);
+  constexpr int N = FINE ? 9 : 6;
+  constexpr float kP = FINE ? 0.34f : 0.42f;
+  constexpr float k[9] = {FINE ? 0.135621578f : 0.166697279f,   FINE ? 0.136092231f : 0.179843664f,
+                          FINE ? 0.115351737f : 0.0705016926f,  FINE ? 0.114713445f : 0.260967582f,
+                          FINE ? -0.043105863f : -0.23618038f,  FINE ? 0.199716911f : 0.0581701808f,
+                          -0.270870388f,                        0.138356715f,
+                          -0.02587636f};
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(__builtin_fabsf(u), kP, 1.0f));
+  float q = k[N - 1];
+#pragma unroll
+  for (int e = N - 2; e >= 0; --e) q = __builtin_fmaf(t, q, k[e]);
   return q * (t * bell);
 }
 
@@ -401,11 +427,12 @@ __device__ __forceinline__ float normal_cdf(float u, float tail) { return u < 0.
 // act(u).  FINITE: u is no infinity, and u Phi(u) = max(u, 0) - |u| (1 -
 // Phi(|u|)) takes two operations less of the VALU time that bounds a large
 // norm with GELU ([128, 500, 1024] float16 2 to 4 % faster, timed in turn).
-template <int ACT, bool FINITE>
+// FINE: as normal_bell's.
+template <int ACT, bool FINITE, bool FINE>
 __device__ __forceinline__ float act_value(float u) {
   if constexpr (ACT == kActSilu) return u * sigmoid(u);
   if constexpr (ACT == kActGelu) {
-    const float tail = normal_tail(u, normal_bell(u));
+    const float tail = normal_tail<FINE>(u, normal_bell<FINE>(u));
     if constexpr (FINITE) return __builtin_fmaf(-__builtin_fabsf(u), tail, __builtin_fmaxf(u, 0.0f));
     return u * normal_cdf(u, tail);
   }
@@ -413,14 +440,14 @@ __device__ __forceinline__ float act_value(float u) {
 }
 
 // act(u) and act'(u)
-template <int ACT>
+template <int ACT, bool FINE>
 __device__ __forceinline__ void act_both(float u, float* value, float* slope) {
   if constexpr (ACT == kActSilu) {
     const float s = sigmoid(u);
     *value = u * s;
     *slope = s * (1.0f + u * (1.0f - s));
   } else if constexpr (ACT == kActGelu) {
-    const float bell = normal_bell(u), tail = normal_tail(u, bell);
+    const float bell = normal_bell<FINE>(u), tail = normal_tail<FINE>(u, bell);
     const float cdf = normal_cdf(u, tail);
     *value = u * cdf;
     *slope = __builtin_fmaf(u * 0.398942280401432678f, bell, cdf);
@@ -430,10 +457,14 @@ __device__ __forceinline__ void act_both(float u, float* value, float* slope) {
   }
 }
 
+// a chunk of float32, whose results keep what a 16-bit type rounds off
+template <int V>
+constexpr bool kFine = V == kChunk<float>;
+
 template <int ACT, int V, bool FINITE = true>
 __device__ __forceinline__ void act_values(float (&u)[V]) {
 #pragma unroll
-  for (int k = 0; k < V; ++k) u[k] = act_value<ACT, FINITE>(u[k]);
+  for (int k = 0; k < V; ++k) u[k] = act_value<ACT, FINITE, kFine<V>>(u[k]);
 }
 
 template <int V>
@@ -447,13 +478,13 @@ template <int V>
 __device__ __forceinline__ void act_pairs(int act, const float (&u)[V], float (&value)[V], float (&slope)[V]) {
   if (act == kActSilu) {
 #pragma unroll
-    for (int k = 0; k < V; ++k) act_both<kActSilu>(u[k], &value[k], &slope[k]);
+    for (int k = 0; k < V; ++k) act_both<kActSilu, kFine<V>>(u[k], &value[k], &slope[k]);
   } else if (act == kActGelu) {
 #pragma unroll
-    for (int k = 0; k < V; ++k) act_both<kActGelu>(u[k], &value[k], &slope[k]);
+    for (int k = 0; k < V; ++k) act_both<kActGelu, kFine<V>>(u[k], &value[k], &slope[k]);
   } else {
 #pragma unroll
-    for (int k = 0; k < V; ++k) act_both<kActNone>(u[k], &value[k], &slope[k]);
+    for (int k = 0; k < V; ++k) act_both<kActNone, kFine<V>>(u[k], &value[k], &slope[k]);
   }
 }
 
