@@ -5,7 +5,9 @@ through ctypes; all work happens in ``libacp.so`` (hand-written HIP kernels
 for gfx950).  Pointer arguments accept an ``int`` device address or any
 object with ``data_ptr()`` (a torch tensor); stream arguments accept an
 ``int`` handle or an object with ``cuda_stream`` (a torch stream).  A non-OK
-status raises ``AcpError`` carrying the status and ``acp_last_error()``.
+status raises ``AcpError`` carrying the status and ``acp_last_error()``.  The
+row operators' float32 arrays and workspaces, which have no descriptor, are
+checked here where they are tensors: type, length, no gaps.
 
 Importing this package fails when ``libacp.so`` has not been built: there is
 no fallback path.
@@ -13,6 +15,7 @@ no fallback path.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -27,9 +30,10 @@ try:
     # torch bundles its own HIP runtime under the same soname; loading torch
     # first makes libacp.so bind to that copy, so torch-allocated memory and
     # streams and acp's launches live in one runtime.
-    import torch  # noqa: F401
+    import torch
+    _Tensor, _F32 = torch.Tensor, torch.float32
 except ImportError:  # pragma: no cover - acp itself does not need torch
-    pass
+    _Tensor, _F32 = (), None
 
 _lib = ctypes.CDLL(LIB_PATH)
 
@@ -63,7 +67,9 @@ class AcpError(RuntimeError):
 
 
 class acp_tile_desc(ctypes.Structure):
+    """``shape`` is set by acp_encode_tiled; None: not encoded here."""
     _fields_ = [("opaque", ctypes.c_ubyte * 256)]
+    shape = None
 
 
 class acp_plan_info(ctypes.Structure):
@@ -88,7 +94,10 @@ class acp_packed8(ctypes.Structure):
     _fields_ = [("codes", _DESC_P), ("scales", _P), ("format", ctypes.c_int32), ("block", ctypes.c_int32)]
 
     def __init__(self, codes: acp_tile_desc, scales, fmt, block: int):
-        super().__init__(ctypes.pointer(codes), _ptr(scales),
+        shape, n = codes.shape, 0
+        if shape and block > 0:
+            n = math.prod(shape[:-1]) * -(-shape[-1] // block)
+        super().__init__(ctypes.pointer(codes), _floats(scales, n, "the scales"),
                          FORMATS[fmt] if isinstance(fmt, str) else int(fmt), int(block))
 
 
@@ -173,6 +182,7 @@ def acp_encode_tiled(dtype, gbase, shape, strides, box, swizzle=ACP_SWIZZLE_NONE
     d = acp_tile_desc()
     _check(_lib.acp_encode_tiled(ctypes.byref(d), dt, r, _ptr(gbase), (ctypes.c_int64 * r)(*shape),
                                  (ctypes.c_int64 * r)(*strides), (ctypes.c_int32 * r)(*box), int(swizzle), int(oob)))
+    d.shape = tuple(shape)
     return d
 
 
@@ -237,11 +247,42 @@ def acp_stream_binary(op, out: acp_tile_desc, x: acp_tile_desc, z: acp_tile_desc
 # kept short: ctypes passes a structure by reference where a pointer is
 # declared, addresses and streams are asked for directly, and a status is
 # looked at only when it is not ACP_OK.
-def _addr(x) -> int | None:
-    try:
-        return x.data_ptr()
-    except AttributeError:
-        return x if x is None else int(x)
+def _refuse(reason: str) -> None:
+    raise AcpError(ACP_ERR_INVALID, reason)
+
+
+def _floats(x, n: int, what: str) -> int | None:
+    """Address of a float32 tensor of at least n values; an address or None as it is.
+
+    The library sees addresses alone: a parameter of another type, or one that
+    is too short, would be read past its end.
+    """
+    if not isinstance(x, _Tensor):
+        return _ptr(x)
+    if x.dtype is not _F32:
+        _refuse(f"{what} must be float32, not {x.dtype}")
+    if x.nbytes < 4 * n:
+        _refuse(f"{what} holds {x.numel()} values, {n} are needed")
+    if not x.is_contiguous():
+        _refuse(f"{what} has gaps between its values")
+    return x.data_ptr()
+
+
+def _space(x, nbytes: int) -> int | None:
+    """Address of a workspace of nbytes, checked likewise."""
+    if not isinstance(x, _Tensor):
+        return _ptr(x)
+    if x.nbytes < nbytes:
+        _refuse(f"the workspace holds {x.nbytes} bytes, not {nbytes}")
+    if not x.is_contiguous():
+        _refuse("the workspace has gaps between its values")
+    return x.data_ptr()
+
+
+def _counts(x: acp_tile_desc, groups: int) -> tuple[int, int]:
+    """Values of a parameter and of a statistic of a norm over x (0: not known here)."""
+    shape = x.shape if x is not None else None
+    return (shape[-1], shape[0] * groups) if shape else (0, 0)
 
 
 def _handle(s) -> int | None:
@@ -290,8 +331,10 @@ def acp_group_norm_workspace(x: acp_tile_desc, groups: int) -> int:
 def acp_group_norm(y: acp_tile_desc, x: acp_tile_desc, gamma, beta, groups: int, eps: float, act="none", mean=None,
                    rstd=None, save: acp_packed8 | None = None, workspace=None, workspace_bytes: int = 0,
                    stream=None) -> None:
-    st = _lib.acp_group_norm(y, x, _addr(gamma), _addr(beta), groups, eps, _act(act), _addr(mean), _addr(rstd), save,
-                             _addr(workspace), workspace_bytes, _handle(stream))
+    c, n = _counts(x, groups)
+    st = _lib.acp_group_norm(y, x, _floats(gamma, c, "gamma"), _floats(beta, c, "beta"), groups, eps, _act(act),
+                             _floats(mean, n, "mean"), _floats(rstd, n, "rstd"), save,
+                             _space(workspace, workspace_bytes), workspace_bytes, _handle(stream))
     if st:
         _check(st)
 
@@ -300,9 +343,11 @@ def acp_group_norm_backward(dx: acp_tile_desc, dgamma, dbeta, dy: acp_tile_desc,
                             mean, rstd, gamma, beta, groups: int, act="none", workspace=None,
                             workspace_bytes: int = 0, stream=None) -> None:
     plain, saved = (None, x) if isinstance(x, acp_packed8) else (x, None)
-    st = _lib.acp_group_norm_backward(dx, _addr(dgamma), _addr(dbeta), dy, plain, saved, _addr(mean), _addr(rstd),
-                                      _addr(gamma), _addr(beta), groups, _act(act), _addr(workspace),
-                                      workspace_bytes, _handle(stream))
+    c, n = _counts(dy, groups)
+    st = _lib.acp_group_norm_backward(dx, _floats(dgamma, c, "dgamma"), _floats(dbeta, c, "dbeta"), dy, plain, saved,
+                                      _floats(mean, n, "mean"), _floats(rstd, n, "rstd"), _floats(gamma, c, "gamma"),
+                                      _floats(beta, c, "beta"), groups, _act(act),
+                                      _space(workspace, workspace_bytes), workspace_bytes, _handle(stream))
     if st:
         _check(st)
 
