@@ -209,11 +209,9 @@ __device__ __forceinline__ void write_channels(const NormCore& A, const Spot& w,
 }
 
 // dbeta and dgamma: column sums of col_rows rows of partial sums, `step`
-// floats apart.  A workgroup takes 16 of the 2 c columns, 16 lanes each, so
+// floats apart.  A workgroup takes kColumns of the 2 c columns, 16 lanes each, so
 // that few rounds of loads follow one another: 4.1 us for 128 rows of 8192
 // columns, mostly latency.
-constexpr uint32_t kColumns = 16;
-
 __device__ __forceinline__ void sum_columns(const NormCore& A, uint32_t wg, uint64_t step) {
   constexpr uint32_t S = kRowThreads / kColumns;
   __shared__ float sh[kRowThreads];

@@ -11,7 +11,7 @@ __global__ __launch_bounds__(kRowThreads) void norm_columns_kernel(const NormCor
 
 }  // namespace dev
 
-uint32_t norm_column_grid(const NormArgs& a) { return a.dgamma || a.dbeta ? (2u * a.c + dev::kColumns - 1u) / dev::kColumns : 0u; }
+uint32_t norm_column_grid(const NormArgs& a) { return a.dgamma || a.dbeta ? (2u * a.c + kColumns - 1u) / kColumns : 0u; }
 
 hipError_t norm_columns_launch(const NormArgs& a, hipStream_t s) {
   const uint32_t grid = norm_column_grid(a);

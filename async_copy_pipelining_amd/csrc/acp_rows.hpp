@@ -154,5 +154,6 @@ constexpr int kSlabRowsBackward = 4;  // ... of a backward slab
 constexpr int kSlabThreads = 1024;    // largest workgroup of a forward slab
 constexpr int kSlabThreadsBackward = 512;
 constexpr int kRowThreadsBackward = 512;
+constexpr uint32_t kColumns = 16;     // columns that a workgroup adds up
 
 }  // namespace acp

@@ -402,6 +402,7 @@ struct NormPlan {
   acp::NormArgs A{};
   acp::NormShape K{};
   acp::Div runs1{}, runs2{};  // by parts: runs of the two passes
+  int64_t grid = 0;           // workgroups of its largest launch, but for the sums of columns
   int64_t workspace = 0, coef_at = 0;
   int64_t strides[4][3] = {};  // of the tensors, as RowTensor has them
   std::string text;            // acp_last_kernel's
@@ -466,7 +467,8 @@ bool plan_row(const NormDims& d, NormPlan* P) {
   A.samples = 1;
   A.rows = static_cast<uint32_t>(d.samples);
   A.group_lanes_log2 = log2_of(gl);
-  A.main_grid = static_cast<uint32_t>(blocks * runs);
+  P->grid = blocks * runs;
+  A.main_grid = static_cast<uint32_t>(P->grid);
   A.col_rows = static_cast<uint32_t>(runs);
   P->K.threads = static_cast<uint32_t>(threads);
   P->workspace = d.backward ? runs * 2 * d.c * 4 : 0;
@@ -533,7 +535,8 @@ bool plan_slab(const NormDims& d, NormPlan* P) {
   A.runs = div_by(static_cast<uint64_t>(runs));
   A.samples = static_cast<uint32_t>(d.samples);
   A.rows = static_cast<uint32_t>(d.rows);
-  A.main_grid = static_cast<uint32_t>(d.backward ? blocks * runs : d.samples * blocks);
+  P->grid = d.backward ? blocks * runs : d.samples * blocks;
+  A.main_grid = static_cast<uint32_t>(P->grid);
   A.col_rows = static_cast<uint32_t>(runs);
   P->K.threads = static_cast<uint32_t>(threads);
   P->workspace = d.backward && runs > 1 ? runs * 2 * d.c * 4 : 0;
@@ -554,7 +557,9 @@ bool plan_parts(const NormDims& d, NormPlan* P) {
   const int64_t first = cached ? both : kNormPartial, second = cached ? both : kNormApply;
   const int64_t runs = split_rows(d.rows, A.row_lanes, std::min(kNormMaxRuns, first / each), 2);
   P->runs1 = div_by(static_cast<uint64_t>(runs));
-  P->runs2 = div_by(static_cast<uint64_t>(split_rows(d.rows, A.row_lanes, second / each, 2)));
+  const int64_t runs2 = split_rows(d.rows, A.row_lanes, second / each, 2);
+  P->runs2 = div_by(static_cast<uint64_t>(runs2));
+  P->grid = d.samples * blocks * std::max(runs, runs2);
   A.parts = static_cast<uint32_t>(runs);
   A.samples = static_cast<uint32_t>(d.samples);
   A.rows = static_cast<uint32_t>(d.rows);
@@ -653,9 +658,12 @@ acp_status norm_geometry(const acp::DescData* const* t, int nt, const NormDims& 
     P.strides[k][1] = !row && o.n >= 2 ? o.stride[k][0] : 0;
     P.strides[k][2] = row ? sample : (o.n >= 1 ? o.stride[k][o.n - 1] : 0);
   }
-  const int64_t most_runs = std::max({A.runs.d, P.runs1.d, P.runs2.d});
-  if (static_cast<int64_t>(A.samples) * A.blocks.d * most_runs + d.c / 16 + 1 >= kRowLimit)
-    return ret(ACP_ERR_UNSUPPORTED, "more than 2^31 workgroups");
+  // a launch has fewer than 2^32 lanes; backward by parts the columns are in
+  // the second pass's, else in one of their own
+  const int64_t columns = d.backward ? ceil_div(2 * d.c, acp::kColumns) : 0;
+  const int64_t wg = P.form == kFormParts ? P.grid + columns : P.grid;
+  if (std::max(wg * int64_t(P.K.threads), columns * acp::kRowThreads) >= int64_t(1) << 32)
+    return ret(ACP_ERR_UNSUPPORTED, "a launch of 2^32 lanes");
   P.text = norm_text(d, P);
   *out = P;
   return ACP_OK;

@@ -332,7 +332,9 @@ acp_status acp_stream_binary(acp_op op, const acp_tile_desc* out, const acp_tile
  * the swizzle of a descriptor are not used, and a base needs only its
  * element's alignment.  The innermost dim is the row; the outer dims have to
  * join into at most three (group norm: the dims between the first and the
- * last into at most two), else ACP_ERR_UNSUPPORTED.  Sums and statistics are
+ * last into at most two), else ACP_ERR_UNSUPPORTED; so are calls that would
+ * take 2^31 chunks of 16 bytes or, group norm, a launch of 2^32 lanes (2^24 to
+ * 2^26 workgroups, of which a sample takes one or more).  Sums and statistics are
  * held in float32 and added in a fixed order: the same call gives the same
  * bits.  A written tensor must not overlap itself or share memory with
  * another operand (ACP_ERR_INVALID); tensors whose rows lie side by side in
