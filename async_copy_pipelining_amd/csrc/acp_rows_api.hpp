@@ -623,20 +623,25 @@ std::string norm_text(const NormDims& d, const NormPlan& P) {
          (P.form == kFormParts ? "+" + std::to_string(P.runs2.d) : std::string());
 }
 
+// The first form that holds.  `row_linear` and `slab_linear` say of such a plan
+// whether the tensors' strides allow it.
+template <class R, class S>
+NormPlan choose_form(const NormDims& d, R row_linear, S slab_linear) {
+  const int env = norm_form_env();
+  NormPlan row, slab, parts;
+  if (env < 1 && plan_row(d, &row) && row_linear(row)) return row;
+  if (env < 2 && plan_slab(d, &slab) && slab_linear(slab)) return slab;
+  plan_parts(d, &parts);
+  return parts;
+}
+
 // The form, split and strides of a norm over `t` (of one shape).
 acp_status norm_geometry(const acp::DescData* const* t, int nt, const NormDims& d, NormPlan* out) {
   Collapsed o;
   if (!collapse(t, nt, 1, 2, &o))
     return ret(ACP_ERR_UNSUPPORTED, "the inner row dims of these strides do not join into two");
-  NormPlan P;
-  const int env = norm_form_env();
-  bool done = env < 1 && plan_row(d, &P) && norm_linear(o, nt, d, P, true, t);
-  if (!done) P = NormPlan();
-  if (!done && env < 2) done = plan_slab(d, &P) && norm_linear(o, nt, d, P, false, t);
-  if (!done) {
-    P = NormPlan();
-    plan_parts(d, &P);
-  }
+  NormPlan P = choose_form(d, [&](const NormPlan& p) { return norm_linear(o, nt, d, p, true, t); },
+                           [&](const NormPlan& p) { return norm_linear(o, nt, d, p, false, t); });
   const bool row = P.form == kFormRow;
   acp::NormArgs& A = P.A;
   const bool linear = P.form != kFormParts || norm_linear(o, nt, d, P, false, t);
@@ -722,24 +727,26 @@ acp_status group_norm_workspace(const acp_tile_desc* x, int groups, int64_t* byt
   if (!bytes) return ret(ACP_ERR_INVALID, "null argument");
   const acp_status st = load_float(x, "x", &xd);
   if (st != ACP_OK) return st;
-  // the strides of the other tensors decide about the form: the most of all.
-  // Only a forward pass by parts splits its work by the scale block
+  // The most of the forms that calls take: the other tensors' strides may turn
+  // a norm per row into a slab, and a slab of several rows into parts; a form is
+  // never asked for that no call takes (by parts, samples of one row would leave
+  // two to four times their own bytes)
   NormDims d;
-  const acp_status sd = norm_dims(xd, groups, 0, true, &d);
+  const acp_status sd = norm_dims(xd, groups, 0, false, &d);
   if (sd != ACP_OK) return sd;
   int64_t need = 0;
-  auto most = [&](bool (*plan)(const NormDims&, NormPlan*)) {
-    NormPlan P;
-    if (plan(d, &P)) need = std::max(need, P.workspace);
+  auto calls = [&](bool row_linear, bool slab_linear) {
+    for (bool backward : {false, true})
+      for (int block : {0, 32, 64, 128, 256}) {
+        d.backward = backward;
+        d.block = block;
+        need = std::max(need, choose_form(d, [&](const NormPlan&) { return row_linear; },
+                                          [&](const NormPlan&) { return slab_linear; }).workspace);
+      }
   };
-  most(plan_row);
-  most(plan_slab);
-  most(plan_parts);
-  d.backward = false;
-  for (int block : {0, 32, 64, 128, 256}) {
-    d.block = block;
-    most(plan_parts);
-  }
+  calls(true, true);
+  calls(false, true);
+  if (d.rows > 1) calls(false, false);
   *bytes = need;
   return ret(ACP_OK);
 }

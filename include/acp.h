@@ -398,7 +398,10 @@ acp_status acp_act_backward(acp_activation act, const acp_tile_desc* dx, const a
                             const acp_tile_desc* dy, const acp_packed8* x, const acp_packed8* z, void* hip_stream);
 
 /* Bytes of workspace that acp_group_norm and acp_group_norm_backward need at
- * most for tensors of x's shape and dtype, saved in 8 bits or not (may be 0).
+ * most for tensors of x's shape and dtype, whatever their strides, saved in 8
+ * bits or not (may be 0).  Token rows in groups of 2^k chunks of 16 bytes, up to
+ * 64, take 8 bytes a channel for up to 1024 workgroups; other samples of one or
+ * few rows up to four times their tensor.
  * The caller owns the workspace (device memory, 16-byte aligned, any
  * contents); it holds nothing between calls, and calls that may run at the
  * same time (other streams, graphs replayed together) need one each. */

@@ -36,3 +36,46 @@ def test_many_short_samples_are_not_refused():
     refused(lambda: grad(dx=at(1, shape), dy=at(2, shape), x=at(3, shape), groups=2, workspace_bytes=8),
             INVALID, "workspace")
     assert acp.acp_group_norm_workspace(at(1, shape), 2) > 0
+
+
+def test_the_workspace_query_asks_for_what_a_call_may_use():
+    """Token rows take no parts: [16384, 4096] in heads of 64 channels needs 8
+    bytes a channel for each of at most 1024 workgroups, whatever the strides of
+    the other tensors, and so does any number of rows."""
+    for rows in (8192, 16384, 131072, 1 << 20):
+        need = acp.acp_group_norm_workspace(at(1, (rows, 4096), "bf16"), 64)
+        assert 0 < need <= 1024 * 8 * 4096 and need <= rows * 4096 * 2
+    assert acp.acp_group_norm_workspace(at(1, (131072, 4096), "bf16"), 64) < 131072 * 4096 * 2 // 25
+    # a token norm whose groups no wave holds goes by parts if it fits no slab: its query says so
+    assert acp.acp_group_norm_workspace(at(1, (8192, 4096), "bf16"), 1) >= 8192 * 8 * 4096
+
+
+def test_the_workspace_query_covers_every_call():
+    """Each call's own check against the query, for contiguous tensors, rows
+    further apart and windows of maps: one byte less than the query may be
+    refused, the query itself is not (the refusal met instead is of dx over dy,
+    or of y over x)."""
+    for shape in ((1, 64), (5, 64), (300, 1000), (4096, 512), (3, 1, 2040), (8192, 4096), (70, 3, 64), (2, 9, 2056),
+                  (4, 20000, 64), (2, 6, 7, 16), (3, 40, 9, 64), (700, 33, 64), (1500, 33, 48), (4000, 4, 640),
+                  (2, 3, 5, 24), (128, 500, 1024), (4000, 10, 333)):
+        for dtype in ("f16", "f32"):
+            for groups in {g for g in (1, 2, 3, 8, 9, 32, 64) if shape[-1] % g == 0}:
+                need = acp.acp_group_norm_workspace(at(1, shape, dtype), groups)
+                ws = dict(workspace=BASE << 30, workspace_bytes=need)
+
+                def strided(k, step):
+                    out, st = [1], step
+                    for ext in reversed(shape[1:-1]):
+                        out.append(st)
+                        st *= ext + (1 if len(out) == 2 and step > shape[-1] else 0)  # a window: row dims do not join
+                    return acp.acp_encode_tiled(dtype, BASE * FAR * k, shape, (st,) + tuple(reversed(out)),
+                                                (1,) * len(shape))
+                for step in (shape[-1], shape[-1] + 24, 1 << 24):
+                    x = strided(1, step)
+                    refused(lambda: norm(y=x, x=x, groups=groups, **ws), INVALID, "y and x share memory")
+                    dx = at(2, shape, dtype)
+                    refused(lambda: grad(dx=x, dy=x, x=dx, groups=groups, **ws), INVALID, "dx and dy share memory")
+                    for block in (32, 256):
+                        p = packed(FAR * 4, shape, block=block, scales=BASE << 32)
+                        refused(lambda: norm(y=x, x=x, groups=groups, save=p, **ws), INVALID, "y and x share memory")
+                        refused(lambda: grad(dx=x, dy=x, x=p, groups=groups, **ws), INVALID, "dx and dy share memory")
