@@ -61,14 +61,14 @@ Range range_of(const void* p, int64_t bytes, const char* what) {
   return {reinterpret_cast<uint64_t>(p), p ? static_cast<uint64_t>(bytes) : 0u, what, nullptr};
 }
 
-// Whether the rows of two tensors lie side by side in one buffer: equal row
-// pitches, every other stride a multiple of the pitch, and each tensor's rows
-// in their own part of it.
-bool side_by_side(const acp::DescData& a, const acp::DescData& b) {
-  if (a.rank != b.rank || a.rank < 2) return false;
-  const int r = a.rank - 1;
+// Whether two tensors lie side by side in one buffer: taken as blocks of their
+// dims [k, rank), which repeat at equal strides of the dims before, all a
+// multiple of one pitch, each tensor's blocks in their own part of it.  k the
+// innermost dim: rows, as the halves of a fused projection; fewer dims before:
+// stacked tensors, as [:, 0] and [:, 1] of [batch, 2, ...].
+bool side_by_side(const acp::DescData& a, const acp::DescData& b, int k) {
   uint64_t pitch = 0;
-  for (int d = 0; d < r; ++d) {
+  for (int d = 0; d < k; ++d) {
     if (a.shape[d] != b.shape[d]) return false;
     if (a.shape[d] == 1) continue;
     const uint64_t s = static_cast<uint64_t>(a.strides[d]) * a.esize;
@@ -76,12 +76,24 @@ bool side_by_side(const acp::DescData& a, const acp::DescData& b) {
     pitch = pitch == 0 || s < pitch ? s : pitch;
   }
   if (pitch == 0) return false;
-  for (int d = 0; d < r; ++d)
+  for (int d = 0; d < k; ++d)
     if (a.shape[d] > 1 && static_cast<uint64_t>(a.strides[d]) * a.esize % pitch) return false;
+  auto block = [k](const acp::DescData& t) {
+    uint64_t n = t.esize;
+    for (int d = k; d < t.rank; ++d)
+      n += static_cast<uint64_t>(t.shape[d] - 1) * static_cast<uint64_t>(t.strides[d]) * t.esize;
+    return n;
+  };
   const uint64_t from =
       b.gbase >= a.gbase ? (b.gbase - a.gbase) % pitch : (pitch - (a.gbase - b.gbase) % pitch) % pitch;
-  const uint64_t na = static_cast<uint64_t>(a.shape[r]) * a.esize, nb = static_cast<uint64_t>(b.shape[r]) * b.esize;
-  return from >= na && from + nb <= pitch;
+  return from >= block(a) && from + block(b) <= pitch;
+}
+
+bool side_by_side(const acp::DescData& a, const acp::DescData& b) {
+  if (a.rank != b.rank) return false;
+  for (int k = a.rank - 1; k > 0; --k)
+    if (side_by_side(a, b, k)) return true;
+  return false;
 }
 
 bool meet(const Range& a, const Range& b) {

@@ -337,9 +337,10 @@ acp_status acp_stream_binary(acp_op op, const acp_tile_desc* out, const acp_tile
  * 2^26 workgroups, of which a sample takes one or more).  Sums and statistics are
  * held in float32 and added in a fixed order: the same call gives the same
  * bits.  A written tensor must not overlap itself or share memory with
- * another operand (ACP_ERR_INVALID); tensors whose rows lie side by side in
- * one buffer at one pitch, as the halves of a fused projection do, share
- * none.  Memory between the rows of an output is left as it was.  Zero
+ * another operand (ACP_ERR_INVALID); tensors whose rows, or blocks of their
+ * inner dims, lie side by side in one buffer at one pitch, as the halves of a
+ * fused projection or [:, 0] and [:, 1] of [batch, 2, ...] do, share none.
+ * Other operands whose address ranges meet are taken to share memory.  Memory between the rows of an output is left as it was.  Zero
  * elements are a call that does nothing.  A call enqueues one or two kernels
  * and, like the others, allocates nothing and can be captured into a HIP
  * graph; all its memory is of the current device, which is the stream's. */
