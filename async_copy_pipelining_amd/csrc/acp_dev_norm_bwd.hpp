@@ -28,14 +28,13 @@ struct Source {
   __device__ static __forceinline__ void place(const NormCore& A, int n, Raw* r) {
     place_codes<V, TAIL>(&r->codes, n, A.c >= V);
   }
-  // z = x rstd - mu rstd, one fma from a code, whose scale joins rstd.  The
-  // rounding of mu rstd moves z by half an ulp of it, as the rounding of mu to
-  // float32 has done already.
+  // z = (x - mu) rstd from a code and its scale, whose product the fma does not
+  // round
   template <class P>
   __device__ static __forceinline__ void z(const Raw& r, const P& st, float (&v)[V]) {
     decode(PK - 1, r.codes, 1.0f, v);
 #pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = __builtin_fmaf(v[e], st.second(e) * r.s, st.first(e));
+    for (int e = 0; e < V; ++e) v[e] = __builtin_fmaf(v[e], r.s, st.first(e)) * st.second(e);
   }
 };
 
@@ -60,14 +59,14 @@ struct Source<T, KIND, 0> {
   __device__ static __forceinline__ void z(const Raw& r, const P& st, float (&v)[V]) {
     widen(r.raw, v, static_cast<const T*>(nullptr));
 #pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = __builtin_fmaf(v[e], st.second(e), st.first(e));
+    for (int e = 0; e < V; ++e) v[e] = (v[e] + st.first(e)) * st.second(e);
   }
 };
 
 template <int PK>
 using BackwardArgs = std::conditional_t<PK != 0, NormBackwardSaved, NormBackward>;
 
-// Two values of each of a lane's channels: (-mean rstd, rstd), or those of
+// Two values of each of a lane's channels: (-mean, rstd), or those of
 // dx: (-rstd c1, -rstd c2) with c1 and c2 the group's two means.  WHOLE (the
 // channels are of one group): one pair for all of them.
 template <int V, bool WHOLE>
@@ -89,10 +88,7 @@ struct Pairs {
   }
   __device__ __forceinline__ void load_stats(const NormCore& A, uint32_t n, uint32_t c, int valid) {
     const uint64_t row = static_cast<uint64_t>(n) * A.groups;
-    load(A, c, valid, [&](uint32_t g) {
-      const float r = A.rstd[row + g];
-      return make_float2(-A.mean[row + g] * r, r);
-    });
+    load(A, c, valid, [&](uint32_t g) { return make_float2(-A.mean[row + g], A.rstd[row + g]); });
   }
 };
 
@@ -275,7 +271,7 @@ __global__ __launch_bounds__(kRowThreadsBackward) void norm_row_backward_kernel(
         const int n = w.channels(A, k0 + u);
         float x[V], a[V];
         Pairs<V, true> st;
-        st.p[0] = -stat[u].x * stat[u].y;
+        st.p[0] = -stat[u].x;
         st.q[0] = stat[u].y;
         src.z(rx[u], st, x);
         widen(rd[u], a, static_cast<const T*>(nullptr));
