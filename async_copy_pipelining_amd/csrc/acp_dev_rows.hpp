@@ -381,39 +381,29 @@ __device__ __forceinline__ float sigmoid(float u) {
 // Mathematical Functions.  Its constants there bound the absolute error of erf
 // and leave the tail 5e-5 off at |u| = 3 and 2e-2 at 10, relative to itself;
 // those below were fitted to the tail's relative error over |u| <= 14.5, since
-// u Phi(u) below zero is as small as the tail.  What is left beside float32's
-// roundings:
-//   FINE  (float32)  3.5e-8 everywhere, nine terms, and a bell whose argument
-//         keeps what its products round off: the tail is within 2^-20
-//   else  (16 bits)  2.9e-7 (1 + 4 u^2), six terms; the bell's argument adds
-//         2^-24 * 1.5 u^2.  1e-5 at |u| = 2, 1.5e-4 at 13, where half a step of
-//         float16 is 4.9e-4
+// u Phi(u) below zero is as small as the tail.  What is left, relative to it:
+//   FINE  (float32)  1.7e-7 everywhere, eight terms
+//   else  (16 bits)  2.9e-7 (1 + 4 u^2), six terms: 1e-5 at |u| = 2, 1.5e-4 at 13,
+//         where half a step of float16 is 4.9e-4
+// and float32's roundings, (16 + 1.5 u^2) 2^-24, the second term the bell's
+// argument's.  A bell whose argument keeps what its products round off, and nine
+// terms, leave 2^-21 of float32 at 4 to 6 us more of VALU work on [8192, 4096]
+// float32 (norm and GELU 57 us for 53, with five terms 51; GELU and its backward
+// pass, saved in i8, 107 for 101, 100).
 // Past |u| = 13.2 the bell is below float32's normal range and so is the tail.
-template <bool FINE>
 __device__ __forceinline__ float normal_bell(float u) {
-  constexpr double kExact = -0.72134752044448170368;  // -log2(e) / 2
-  constexpr float kHigh = static_cast<float>(kExact);
-  const float sq = u * u, arg = sq * kHigh;
-  const float bell = __builtin_amdgcn_exp2f(arg);
-  if constexpr (!FINE) return bell;
-  constexpr float kLow = static_cast<float>(kExact - static_cast<double>(kHigh));
-  float off = __builtin_fmaf(sq, kHigh, -arg);
-  off = __builtin_fmaf(__builtin_fmaf(u, u, -sq), kHigh, off);
-  off = __builtin_fmaf(sq, kLow, off);
-  // where the bell is zero its argument may be infinite, and `off` a NaN
-  return bell > 0.0f ? __builtin_fmaf(bell * 0.693147180559945309f, off, bell) : bell;
+  return __builtin_amdgcn_exp2f(u * u * -0.721347520444481704f);
 }
 
 // 1 - Phi(|u|)
 template <bool FINE>
 __device__ __forceinline__ float normal_tail(float u, float bell) {
-  constexpr int N = FINE ? 9 : 6;
-  constexpr float kP = FINE ? 0.34f : 0.42f;
-  constexpr float k[9] = {FINE ? 0.135621578f : 0.166697279f,   FINE ? 0.136092231f : 0.179843664f,
-                          FINE ? 0.115351737f : 0.0705016926f,  FINE ? 0.114713445f : 0.260967582f,
-                          FINE ? -0.043105863f : -0.23618038f,  FINE ? 0.199716911f : 0.0581701808f,
-                          -0.270870388f,                        0.138356715f,
-                          -0.02587636f};
+  constexpr int N = FINE ? 8 : 6;
+  constexpr float kP = FINE ? 0.3f : 0.42f;
+  constexpr float k[8] = {FINE ? 0.119632013f : 0.166697279f,   FINE ? 0.120712139f : 0.179843664f,
+                          FINE ? 0.100175977f : 0.0705016926f,  FINE ? 0.127691671f : 0.260967582f,
+                          FINE ? -0.0520338044f : -0.23618038f, FINE ? 0.204556525f : 0.0581701808f,
+                          -0.156158313f,                        0.0354237035f};
   const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(__builtin_fabsf(u), kP, 1.0f));
   float q = k[N - 1];
 #pragma unroll
@@ -427,12 +417,12 @@ __device__ __forceinline__ float normal_cdf(float u, float tail) { return u < 0.
 // act(u).  FINITE: u is no infinity, and u Phi(u) = max(u, 0) - |u| (1 -
 // Phi(|u|)) takes two operations less of the VALU time that bounds a large
 // norm with GELU ([128, 500, 1024] float16 2 to 4 % faster, timed in turn).
-// FINE: as normal_bell's.
+// FINE: as normal_tail's.
 template <int ACT, bool FINITE, bool FINE>
 __device__ __forceinline__ float act_value(float u) {
   if constexpr (ACT == kActSilu) return u * sigmoid(u);
   if constexpr (ACT == kActGelu) {
-    const float tail = normal_tail<FINE>(u, normal_bell<FINE>(u));
+    const float tail = normal_tail<FINE>(u, normal_bell(u));
     if constexpr (FINITE) return __builtin_fmaf(-__builtin_fabsf(u), tail, __builtin_fmaxf(u, 0.0f));
     return u * normal_cdf(u, tail);
   }
@@ -447,7 +437,7 @@ __device__ __forceinline__ void act_both(float u, float* value, float* slope) {
     *value = u * s;
     *slope = s * (1.0f + u * (1.0f - s));
   } else if constexpr (ACT == kActGelu) {
-    const float bell = normal_bell<FINE>(u), tail = normal_tail<FINE>(u, bell);
+    const float bell = normal_bell(u), tail = normal_tail<FINE>(u, bell);
     const float cdf = normal_cdf(u, tail);
     *value = u * cdf;
     *slope = __builtin_fmaf(u * 0.398942280401432678f, bell, cdf);

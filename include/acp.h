@@ -380,9 +380,9 @@ acp_status acp_unpack8(const acp_tile_desc* out, const acp_packed8* in, void* hi
 /* Activations: SILU u / (1 + e^-u), GELU u (1 + erf(u / sqrt 2)) / 2.  Both are
  * infinite at +infinity, and NaN at -infinity as the formulas are.  Below zero
  * their values keep their own digits, before the output's rounding: SILU is
- * within (1.25 |u| + 8) 2^-24 of itself, GELU within 2^-20 for f32 tensors and
- * within 3e-7 (1 + 4 u^2) + (1.5 u^2 + 16) 2^-24 for 16-bit ones, as long as it is
- * in float32's normal range (u > -13). */
+ * within (1.25 |u| + 8) 2^-24 of itself, GELU within (1.5 u^2 + 16) 2^-24, and
+ * 3e-7 (1 + 4 u^2) more for 16-bit tensors, as long as it is in float32's normal
+ * range (u > -13). */
 typedef enum { ACP_ACT_NONE = 0, ACP_ACT_SILU = 1, ACP_ACT_GELU = 2 } acp_activation;
 
 /* out = act(x), or act(x) * z where z is not NULL, computed in float32 and

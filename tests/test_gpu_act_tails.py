@@ -3,11 +3,11 @@ values: act and act' below zero fall off as fast as their exponentials, where
 a bound on the absolute error sees nothing.
 
 Bounds count roundings in u = 2^-24, half a step of float32.
-* float32 GELU: |v| Phi(v) and its factors within 16 u (a fit within 0.6 u; the
-  reciprocal 2, its argument 1, nine steps of the polynomial whose terms do not
-  cancel below a third of their sum 3, the bell 6, three products), whatever v.
-* 16-bit GELU: a fit within 2.9e-7 (1 + 4 v^2), and the bell's argument, whose
-  0.72 v^2 has three roundings: 1.5 v^2 u; 16 u beside.
+* GELU: |v| Phi(v) and its factors within (16 + 1.5 v^2) u: the reciprocal 2,
+  its argument 1, the polynomial's steps, whose terms do not cancel below a third
+  of their sum, 4, a fit of float32 2.8 (1.7e-7), the exponential 2, three
+  products; and the bell's argument, whose 0.72 v^2 has three roundings.  The fit
+  for 16-bit types is within 2.9e-7 (1 + 4 v^2).
 * SiLU: the exponential's argument has a rounding and its constant's own,
   1.25 |v| u; the exponential, 1 +, 1 / and the product 8 u."""
 import math
@@ -35,7 +35,7 @@ def tail_error(name, dtype, v):
     """Relative error of act(v), v < 0, before the output's own rounding."""
     if name == "silu":
         return (1.25 * np.abs(v) + 8) * U
-    return 16 * U + (0.0 if dtype == "f32" else 2.9e-7 * (1 + 4 * v * v) + 1.5 * v * v * U)
+    return (16 + 1.5 * v * v) * U + (0.0 if dtype == "f32" else 2.9e-7 * (1 + 4 * v * v))
 
 
 def slope(name, v):
