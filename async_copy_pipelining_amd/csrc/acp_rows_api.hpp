@@ -726,8 +726,8 @@ void set_tensor(const NormPlan& P, int k, const acp::DescData& d, acp::RowTensor
 
 bool misaligned4(const void* p) { return reinterpret_cast<uint64_t>(p) % 4 != 0; }
 
-acp_status check_workspace(const void* workspace, int64_t bytes, int64_t need) {
-  if (need == 0) return ACP_OK;
+acp_status check_workspace(const void* workspace, int64_t bytes, int64_t need, int64_t samples) {
+  if (need == 0 || samples == 0) return ACP_OK;
   if (!workspace || bytes < need)
     return ret(ACP_ERR_INVALID, "the workspace is smaller than acp_group_norm_workspace says");
   if (reinterpret_cast<uint64_t>(workspace) % 16) return ret(ACP_ERR_INVALID, "the workspace is not 16-byte aligned");
@@ -788,7 +788,7 @@ acp_status group_norm(const acp_tile_desc* y, const acp_tile_desc* x, const floa
     set_tensor(P, 2, cd, &A.codes);
     A.scales.p = reinterpret_cast<char*>(save->scales);
   }
-  if ((st = check_workspace(workspace, workspace_bytes, P.workspace)) != ACP_OK) return st;
+  if ((st = check_workspace(workspace, workspace_bytes, P.workspace, d.samples)) != ACP_OK) return st;
   if (self_overlap(yd) || (save && self_overlap(cd))) return ret(ACP_ERR_INVALID, "an output overlaps itself");
   const int64_t stat = d.samples * groups * 4;
   Range w[6] = {range_of(yd, "y"), range_of(mean, stat, "mean"), range_of(rstd, stat, "rstd"),
@@ -853,7 +853,7 @@ acp_status group_norm_backward(const acp_tile_desc* dx, float* dgamma, float* db
   set_tensor(P, 1, dxd, &A.dx);
   set_tensor(P, 2, *t[2], x ? &A.x : &A.codes);
   if (saved) A.scales.p = reinterpret_cast<char*>(saved->scales);
-  if ((st = check_workspace(workspace, workspace_bytes, P.workspace)) != ACP_OK) return st;
+  if ((st = check_workspace(workspace, workspace_bytes, P.workspace, d.samples)) != ACP_OK) return st;
   if (self_overlap(dxd)) return ret(ACP_ERR_INVALID, "an output overlaps itself");
   const int64_t stat = d.samples * groups * 4;
   const Range w[] = {range_of(dxd, "dx"), range_of(dgamma, d.c * 4, "dgamma"), range_of(dbeta, d.c * 4, "dbeta"),

@@ -79,3 +79,12 @@ def test_the_workspace_query_covers_every_call():
                         p = packed(FAR * 4, shape, block=block, scales=BASE << 32)
                         refused(lambda: norm(y=x, x=x, groups=groups, save=p, **ws), INVALID, "y and x share memory")
                         refused(lambda: grad(dx=x, dy=x, x=p, groups=groups, **ws), INVALID, "dx and dy share memory")
+
+
+def test_no_samples_need_no_workspace():
+    for shape, groups in (((0, 64), 8), ((0, 4096), 64), ((0, 5, 64), 8), ((0, 20000, 64), 8), ((0, 4096), 1)):
+        e = [desc(k, shape) for k in (1, 2, 3)]
+        norm(y=e[0], x=e[1], groups=groups, workspace=None, workspace_bytes=0)
+        assert acp.acp_last_kernel() == "none"
+        grad(dx=e[0], dy=e[1], x=e[2], groups=groups, dgamma=None, dbeta=None, workspace=None, workspace_bytes=0)
+        assert acp.acp_last_kernel() == "none"
