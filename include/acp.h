@@ -340,8 +340,11 @@ acp_status acp_stream_binary(acp_op op, const acp_tile_desc* out, const acp_tile
  * another operand (ACP_ERR_INVALID); tensors whose rows, or blocks of their
  * inner dims, lie side by side in one buffer at one pitch, as the halves of a
  * fused projection or [:, 0] and [:, 1] of [batch, 2, ...] do, share none.
- * Other operands whose address ranges meet are taken to share memory.  Memory between the rows of an output is left as it was.  Zero
- * elements are a call that does nothing.  A call enqueues one or two kernels
+ * Other operands whose address ranges meet are taken to share memory.  Memory
+ * between the rows of an output is left as it was.  Tensors without elements
+ * are a call that does nothing (their descriptors still take an address); a
+ * norm of no samples leaves dgamma and dbeta zero, a norm without rows or
+ * channels is refused (ACP_ERR_INVALID).  A call enqueues one or two kernels
  * and, like the others, allocates nothing and can be captured into a HIP
  * graph; all its memory is of the current device, which is the stream's. */
 
@@ -434,7 +437,8 @@ acp_status acp_group_norm(const acp_tile_desc* y, const acp_tile_desc* x, const 
  *   dx = rstd * (gamma a - M(gamma a) - z M(gamma a z)),  M the mean over a
  *        sample's group
  * dgamma and dbeta (device float32 [channels]) are written, not added to;
- * NULL: not wanted. */
+ * NULL: not wanted.  Where gamma and beta take the activation's argument past
+ * 2^127, the gradients may be NaN. */
 acp_status acp_group_norm_backward(const acp_tile_desc* dx, float* dgamma, float* dbeta, const acp_tile_desc* dy,
                                    const acp_tile_desc* x, const acp_packed8* saved, const float* mean,
                                    const float* rstd, const float* gamma, const float* beta, int groups,

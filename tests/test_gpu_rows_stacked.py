@@ -60,3 +60,49 @@ def test_norm_and_its_gradient_in_one_buffer(shape, groups):
     assert all(same(a, b) for a, b in zip(*got))
     assert all(same(whole[:, k], own[k]) for k in range(4)) and same(whole[:, 4], keep)
     assert bool((own[3] != 0).any())
+
+
+@pytest.mark.parametrize("shape, groups", [((5, 40, 64), 4), ((3, 5000, 16), 2), ((4, 700, 40), 5), ((6, 9, 7, 24), 3)])
+def test_norm_of_rows_before_samples(shape, groups):
+    """[time, batch, channels] in memory, samples the batch: rows lie further
+    apart than samples, alike in every tensor or only in some."""
+    print(f"[gpu] time first {shape}", flush=True)
+    flat = (shape[0], -1, shape[-1])
+    x, dy = (torch.randn(shape, device=DEV).to(torch.float16).reshape(flat) for _ in range(2))
+    time_first = lambda t: t.transpose(0, 1).contiguous().transpose(0, 1)  # noqa: E731
+    got = []
+    for order in ((0, 0, 0, 0), (1, 1, 1, 1), (1, 0, 0, 1), (0, 1, 1, 0)):
+        y, dx = torch.zeros_like(x), torch.zeros_like(x)
+        t = [time_first(v) if o else v.contiguous() for v, o in zip((x, y, dy, dx), order)]
+        d = [enc(v) for v in t]
+        mean, rstd = (torch.zeros(shape[0], groups, device=DEV) for _ in range(2))
+        dgamma, dbeta = (torch.zeros(shape[-1], device=DEV) for _ in range(2))
+        n = acp.acp_group_norm_workspace(d[0], groups)
+        work = torch.zeros(n + 16, dtype=torch.uint8, device=DEV)
+        h = torch.cuda.current_stream()
+        acp.acp_group_norm(d[1], d[0], None, None, groups, 1e-5, "silu", mean, rstd, None, work, n, h)
+        acp.acp_group_norm_backward(d[3], dgamma, dbeta, d[2], d[0], mean, rstd, None, None, groups, "silu", work, n, h)
+        torch.cuda.synchronize()
+        got.append((t[1].contiguous(), t[3].contiguous(), mean, rstd, dgamma, dbeta))
+    assert all(same(a, b) for other in got[1:] for a, b in zip(got[0], other))
+    assert bool((got[0][1] != 0).any())
+
+
+def test_activation_and_checkpoint_with_outer_dims_in_another_order():
+    print("[gpu] outer dims in another order", flush=True)
+    x, z = (torch.randn(4, 6, 3, 100, device=DEV).to(torch.bfloat16) for _ in range(2))
+    NAMES[torch.bfloat16] = "bf16"
+    got = []
+    for perm in ((0, 1, 2, 3), (1, 0, 2, 3), (2, 1, 0, 3), (1, 2, 0, 3)):
+        back = tuple(perm.index(k) for k in range(4))
+        order = lambda t: t.permute(perm).contiguous().permute(back)  # noqa: E731
+        y, out, codes = order(torch.zeros_like(x)), order(torch.zeros_like(x)), order(x.view(torch.uint8)[..., :100])
+        scales = torch.zeros(4, 6, 3, 4, device=DEV)
+        p = acp.acp_packed8(enc(codes), scales, "e4m3", 32)
+        h = torch.cuda.current_stream()
+        acp.acp_act_forward("gelu", enc(y), enc(order(x)), enc(z), stream=h)
+        acp.acp_pack8(p, enc(order(x)), h)
+        acp.acp_unpack8(enc(out), p, h)
+        torch.cuda.synchronize()
+        got.append((y.contiguous(), out.contiguous(), codes.contiguous(), scales))
+    assert all(same(a, b) for other in got[1:] for a, b in zip(got[0], other))
