@@ -28,13 +28,12 @@ struct Source {
   __device__ static __forceinline__ void place(const NormCore& A, int n, Raw* r) {
     place_codes<V, TAIL>(&r->codes, n, A.c >= V);
   }
-  // z = (x - mu) rstd from a code and its scale, whose product the fma does not
-  // round
+  // x - mu from a code and its scale, whose product the fma does not round
   template <class P>
-  __device__ static __forceinline__ void z(const Raw& r, const P& st, float (&v)[V]) {
+  __device__ static __forceinline__ void centre(const Raw& r, const P& st, float (&v)[V]) {
     decode(PK - 1, r.codes, 1.0f, v);
 #pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = __builtin_fmaf(v[e], r.s, st.first(e)) * st.second(e);
+    for (int e = 0; e < V; ++e) v[e] = __builtin_fmaf(v[e], r.s, st.first(e));
   }
 };
 
@@ -56,10 +55,10 @@ struct Source<T, KIND, 0> {
     place_tail<T, TAIL>(&r->raw, n, A.c >= V);
   }
   template <class P>
-  __device__ static __forceinline__ void z(const Raw& r, const P& st, float (&v)[V]) {
+  __device__ static __forceinline__ void centre(const Raw& r, const P& st, float (&v)[V]) {
     widen(r.raw, v, static_cast<const T*>(nullptr));
 #pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = (v[e] + st.first(e)) * st.second(e);
+    for (int e = 0; e < V; ++e) v[e] += st.first(e);
   }
 };
 
@@ -86,13 +85,20 @@ struct Pairs {
       q[e] = v.y;
     }
   }
+  // the second value times st's
+  __device__ __forceinline__ void scale(const Pairs& st) {
+#pragma unroll
+    for (int e = 0; e < K; ++e) q[e] *= st.q[e];
+  }
   __device__ __forceinline__ void load_stats(const NormCore& A, uint32_t n, uint32_t c, int valid) {
     const uint64_t row = static_cast<uint64_t>(n) * A.groups;
     load(A, c, valid, [&](uint32_t g) { return make_float2(-A.mean[row + g], A.rstd[row + g]); });
   }
 };
 
-// a = dy act'(z gamma + beta) in the place of dy
+// a = dy act'(z gamma + beta) in the place of dy.  Where the rows of a lane are
+// of one sample, z is left as x - mu and rstd is in gamma, in the sums of a z once
+// they are made, and in the coefficients of dx.
 template <int ACT, int V>
 __device__ __forceinline__ void times_slope(const Params<V>& p, const float (&z)[V], float (&dy)[V]) {
   if constexpr (ACT != kActNone) {
@@ -103,6 +109,12 @@ __device__ __forceinline__ void times_slope(const Params<V>& p, const float (&z)
       dy[e] *= slope;
     }
   }
+}
+
+template <int V, bool WHOLE>
+__device__ __forceinline__ void scale_gamma(const Pairs<V, WHOLE>& st, Params<V>* p) {
+#pragma unroll
+  for (int e = 0; e < V; ++e) p->gamma[e] *= st.second(e);
 }
 
 // The same where nothing else needs gamma and beta: for silu they are scaled
@@ -273,7 +285,9 @@ __global__ __launch_bounds__(kRowThreadsBackward) void norm_row_backward_kernel(
         Pairs<V, true> st;
         st.p[0] = -stat[u].x;
         st.q[0] = stat[u].y;
-        src.z(rx[u], st, x);
+        src.centre(rx[u], st, x);
+#pragma unroll
+        for (int e = 0; e < V; ++e) x[e] *= st.q[0];
         widen(rd[u], a, static_cast<const T*>(nullptr));
         load(k0 + U + u, u);
         times_slope<ACT>(p, x, a);
@@ -307,8 +321,8 @@ __global__ __launch_bounds__(kRowThreadsBackward) void norm_row_backward_kernel(
 // samples run, run + runs, ... and leaves its per-channel sums in
 // part[run][2][c].  Small calls are bound by latency, where three barriers a
 // sample cost less than a second pass ([2, 16, 16, 640] float16 from e4m3 10.7
-// us, and 1.6 us for the columns); [512, 256, 1024] float16 from x 206 us with
-// silu (805 MB, 3.9 TB/s): a CU holds one workgroup of 512 lanes, so its loads
+// us, and 1.6 us for the columns); [512, 256, 1024] float16 from x 211 us with
+// silu (805 MB, 3.8 TB/s): a CU holds one workgroup of 512 lanes, so its loads
 // and its stores take turns.  Eight chunks a lane with the slope computed
 // twice took 200 us there, but 282 us for 192 on [4096, 64, 512] bfloat16 and
 // 9.8 for 8.7 on [64, 32, 512].
@@ -355,6 +369,8 @@ __global__ __launch_bounds__(kSlabThreadsBackward) void norm_slab_backward_kerne
     }
     Pairs<V, WHOLE> st;
     st.load_stats(A, w.n, w.c, w.valid);
+    Params<V> ps = p;
+    scale_gamma(st, &ps);
     float sa[V], sz[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) sa[e] = sz[e] = 0.0f;
@@ -364,9 +380,9 @@ __global__ __launch_bounds__(kSlabThreadsBackward) void norm_slab_backward_kerne
       float z[V];
       src.place(A, w.channels(A, u), &rx[u]);
       place_tail<T, TAIL>(&rd[u], w.channels(A, u), A.c >= V);
-      src.z(rx[u], st, z);
+      src.centre(rx[u], st, z);
       widen(rd[u], a[u], static_cast<const T*>(nullptr));
-      times_slope<ACT>(p, z, a[u]);
+      times_slope<ACT>(ps, z, a[u]);
       if (w.channels(A, u) > 0) {
 #pragma unroll
         for (int e = 0; e < V; ++e) {
@@ -375,6 +391,8 @@ __global__ __launch_bounds__(kSlabThreadsBackward) void norm_slab_backward_kerne
         }
       }
     }
+#pragma unroll
+    for (int e = 0; e < V; ++e) sz[e] *= st.second(e);
     channel_sums<V>(A, lds, chan, sa, sz);
     for (uint32_t ch = threadIdx.x; ch < width; ch += blockDim.x)
       sums[ch] = make_float2(sums[ch].x + chan[ch].x, sums[ch].y + chan[ch].y);
@@ -388,15 +406,16 @@ __global__ __launch_bounds__(kSlabThreadsBackward) void norm_slab_backward_kerne
     __syncthreads();
     Pairs<V, WHOLE> cf;
     cf.load(A, w.c, w.valid, [&](uint32_t g) { return coef[g - b.g0]; });
+    cf.scale(st);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (u * A.row_lanes >= w.rows) break;
       const int n = w.channels(A, u);
       float z[V], d[V];
-      src.z(rx[u], st, z);
+      src.centre(rx[u], st, z);
 #pragma unroll
       for (int e = 0; e < V; ++e)
-        d[e] = __builtin_fmaf(a[u][e], p.gamma[e] * st.second(e), __builtin_fmaf(z[e], cf.second(e), cf.first(e)));
+        d[e] = __builtin_fmaf(a[u][e], ps.gamma[e], __builtin_fmaf(z[e], cf.second(e), cf.first(e)));
       store_chunk<T, TAIL>(px.at(A, u), n, narrow(d, static_cast<const T*>(nullptr)));
     }
   }
@@ -440,9 +459,10 @@ __global__ __launch_bounds__(kRowThreads) void norm_sums_kernel(const BackwardAr
   float2* chan = lds + blockDim.x * (V + 1);
   float* gl = reinterpret_cast<float*>(chan + A.lanes.d * V);
   put_gamma<V>(w, p, gl);
-  scale_params<ACT>(&p);
   Pairs<V, WHOLE> st;
   st.load_stats(A, w.n, w.c, w.valid);
+  scale_gamma(st, &p);
+  scale_params<ACT>(&p);
   float sa[V], sz[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) sa[e] = sz[e] = 0.0f;
@@ -454,7 +474,7 @@ __global__ __launch_bounds__(kRowThreads) void norm_sums_kernel(const BackwardAr
         float z[V], a[V];
         src.place(A, w.channels(A, k0 + u), &rx[u]);
         place_tail<T, TAIL>(&rd[u], w.channels(A, k0 + u), A.c >= V);
-        src.z(rx[u], st, z);
+        src.centre(rx[u], st, z);
         widen(rd[u], a, static_cast<const T*>(nullptr));
         const int next = w.channels(A, k0 + U + u);
         src.template load<true>(A, k0 + U + u, next, &rx[u]);
@@ -470,6 +490,8 @@ __global__ __launch_bounds__(kRowThreads) void norm_sums_kernel(const BackwardAr
       }
     }
   }
+#pragma unroll
+  for (int e = 0; e < V; ++e) sz[e] *= st.second(e);
   const uint32_t width = A.lanes.d * V;
   channel_sums<V>(A, lds, chan, sa, sz);
   write_channels(A, w, width, A.part + (static_cast<uint64_t>(w.n) * A.runs.d + w.run) * 2u * A.c, chan);
@@ -554,9 +576,11 @@ __global__ __launch_bounds__(kRowThreads) void norm_dx_kernel(const BackwardArgs
   __syncthreads();
   if (w.valid == 0) return;
   cf.load(A, w.c, w.valid, [&](uint32_t g) { return coef[g - b.g0]; });
+  cf.scale(st);
+  scale_gamma(st, &p);
   float scale[V];
 #pragma unroll
-  for (int e = 0; e < V; ++e) scale[e] = p.gamma[e] * st.second(e);
+  for (int e = 0; e < V; ++e) scale[e] = p.gamma[e];
   scale_params<ACT>(&p);
   for (uint32_t k0 = 0; k0 * w.step < w.rows; k0 += U) {
 #pragma unroll
@@ -566,7 +590,7 @@ __global__ __launch_bounds__(kRowThreads) void norm_dx_kernel(const BackwardArgs
       float z[V], a[V];
       src.place(A, n, &rx[u]);
       place_tail<T, TAIL>(&rd[u], n, A.c >= V);
-      src.z(rx[u], st, z);
+      src.centre(rx[u], st, z);
       widen(rd[u], a, static_cast<const T*>(nullptr));
       const int next = w.channels(A, k0 + U + u);
       src.template load<false>(A, k0 + U + u, next, &rx[u]);

@@ -524,7 +524,7 @@ bool plan_slab(const NormDims& d, NormPlan* P) {
   if (d.backward && d.samples > 1 && blocks > 1 && lanes < 4) return false;
   // backward, a lane's values fill so many registers that a CU holds one
   // workgroup of 512 lanes.  Past one a CU the form is still the fastest from
-  // x itself in blocks of whole 128-byte lines ([512, 256, 1024] float16 206
+  // x itself in blocks of whole 128-byte lines ([512, 256, 1024] float16 211
   // us, by parts 230; [64, 256, 1024] 35 and 47; [1024, 200, 512] float32 250
   // and 346), but not where blocks end inside a line ([1024, 144, 320] float16
   // 126 and 99; [128, 500, 1024] in blocks of 64 bytes 132 and 117) or whose
