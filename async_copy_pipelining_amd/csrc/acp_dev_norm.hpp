@@ -29,7 +29,10 @@
 // times the sum of squared deviations, so the subtraction that removes the
 // mean loses at most a factor n of the lane's few rows, whatever the data's
 // offset or outliers.  Lanes and parts are joined the same way, each as
-// (mean, sum of squared deviations) about the first one's mean.
+// (mean, sum of squared deviations) about the first one's mean.  Per row the
+// group's sum is taken whole and the squares about its mean: that sum rounds at
+// the size of the mean, a few 2^-24 of it (a second mean of what is left took 3
+// to 6 % more time for float32).
 #pragma once
 
 #include <type_traits>

@@ -218,7 +218,7 @@ __device__ __forceinline__ void write_channels(const NormCore& A, const Spot& w,
 
 // dbeta and dgamma: column sums of col_rows rows of partial sums, `step`
 // floats apart.  A workgroup takes kColumns of the 2 c columns, 16 lanes each, so
-// that few rounds of loads follow one another: 4.1 us for 128 rows of 8192
+// that few rounds of loads follow one another: 4.6 us for 128 rows of 8192
 // columns, mostly latency.
 __device__ __forceinline__ void sum_columns(const NormCore& A, uint32_t wg, uint64_t step) {
   constexpr uint32_t S = kRowThreads / kColumns;
@@ -248,8 +248,8 @@ __device__ __forceinline__ void sum_columns(const NormCore& A, uint32_t wg, uint
 // One row a sample.  The group sums are taken here; the per-channel sums of
 // this workgroup's rows stay in registers until the end and go to
 // part[run][2][c], which norm_columns_kernel adds up.  Bound by HBM: [8192,
-// 4096] bfloat16 in heads of 64 channels 36.9 us (205 MB, 5.5 TB/s), and 4.1 us
-// for the columns.
+// 4096] bfloat16 in heads of 64 channels 38.0 us (205 MB, 5.4 TB/s), and 4.6 us
+// for the columns (medians of 30 traced calls).
 template <class T, int PK, int ACT>
 __global__ __launch_bounds__(kRowThreadsBackward) void norm_row_backward_kernel(const BackwardArgs<PK> A) {
   constexpr int V = kChunk<T>, U = kRowUnroll;
@@ -320,9 +320,10 @@ __global__ __launch_bounds__(kRowThreadsBackward) void norm_row_backward_kernel(
 // kSlabRowsBackward chunks, so dy and x are read once.  A workgroup walks
 // samples run, run + runs, ... and leaves its per-channel sums in
 // part[run][2][c].  Small calls are bound by latency, where three barriers a
-// sample cost less than a second pass ([2, 16, 16, 640] float16 from e4m3 10.7
-// us, and 1.6 us for the columns); [512, 256, 1024] float16 from x 211 us with
-// silu (805 MB, 3.8 TB/s): a CU holds one workgroup of 512 lanes, so its loads
+// sample cost less than a second pass ([2, 16, 16, 640] float16 from e4m3 11.1
+// us, and 3.9 us for the columns, medians of 30 traced calls); [512, 256, 1024]
+// float16 from x 211 us with silu (805 MB, 3.8 TB/s; the vector units issue 44 %
+// of the time): a CU holds one workgroup of 512 lanes, so its loads
 // and its stores take turns.  Eight chunks a lane with the slope computed
 // twice took 200 us there, but 282 us for 192 on [4096, 64, 512] bfloat16 and
 // 9.8 for 8.7 on [64, 32, 512].
@@ -437,8 +438,9 @@ __global__ __launch_bounds__(kSlabThreadsBackward) void norm_slab_backward_kerne
 // and sum gamma a z, into coef[n][g][run][piece].  The loads keep the data in
 // the caches for the second pass; each chunk's place takes the one U steps on
 // as soon as it is used.  [128, 500, 1024] float16 from i8, silu: 45 to 54 us
-// (197 MB, 3.6 to 4.4 TB/s; the VALU issues 62 % of the time, on decoding and
-// the slope); [3, 37, 41, 352] float32, groups of 11 channels: 8.0 us.
+// (197 MB, 3.6 to 4.4 TB/s; the vector units issue 67 % of the time, on decoding
+// and the slope); [3, 37, 41, 352] float32, groups of 11 channels: 8.3 us (median
+// of 30 traced calls).
 template <class T, int KIND, int PK, int ACT>
 __global__ __launch_bounds__(kRowThreads) void norm_sums_kernel(const BackwardArgs<PK> A) {
   constexpr bool WHOLE = KIND == kNormWhole, TAIL = KIND == kNormAny, LINEAR = !TAIL;
@@ -540,8 +542,9 @@ __device__ __forceinline__ float2 join_sums(const NormCore& A, uint32_t n, uint3
 }
 
 // dx.  The first workgroups add up dgamma and dbeta.  The first chunks are on
-// their way while the parts are joined.  Bound by HBM: [128, 500, 1024] float16
-// from i8, silu 54 us (328 MB, 6.1 TB/s); [3, 37, 41, 352] float32 7.5 us.
+// their way while the parts are joined.  Bound by HBM and VALU work alike:
+// [128, 500, 1024] float16 from i8, silu 54 to 59 us (328 MB, 5.6 to 6.1 TB/s; the
+// vector units issue 74 % of the time); [3, 37, 41, 352] float32 8.5 us.
 template <class T, int KIND, int PK, int ACT>
 __global__ __launch_bounds__(kRowThreads) void norm_dx_kernel(const BackwardArgs<PK> A) {
   constexpr bool WHOLE = KIND == kNormWhole, TAIL = KIND == kNormAny, LINEAR = !TAIL;

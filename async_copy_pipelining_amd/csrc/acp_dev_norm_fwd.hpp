@@ -43,8 +43,8 @@ using ForwardArgs = std::conditional_t<PK != 0, NormForwardSaved, NormForward>;
 // lanes of a wave, so mean and variance are two trains of cross-lane moves on
 // values that stay in registers, with no LDS and no barrier.  Each chunk's
 // place takes the one U steps on as soon as it is used.  Bound by HBM:
-// [16384, 4096] bfloat16 in heads of 64 channels 48.4 us, 5.7 TB/s; [32, 2048]
-// float16 3.1 us, where the launch is all of it.
+// [16384, 4096] bfloat16 in heads of 64 channels 48.9 us, 5.7 TB/s; [32, 2048]
+// float16 3.7 us, where the launch is all of it (medians of 30 traced calls).
 template <class T, int PK, int ACT>
 __global__ __launch_bounds__(kRowThreads) void norm_row_kernel(const ForwardArgs<PK> A) {
   constexpr int V = kChunk<T>, U = kRowUnroll;
@@ -102,9 +102,10 @@ __global__ __launch_bounds__(kRowThreads) void norm_row_kernel(const ForwardArgs
 // kSlabRows chunks, so x is read once.  A workgroup's loads, its join and its
 // stores follow one another; the other workgroups of the CU fill the gaps.
 // [128, 500, 1024] float16, 32 groups: 53 us without an activation (4.9 TB/s
-// in row segments of 128 bytes), 64 us with gelu (its VALU work, which the
-// stores do not all hide), 77 us with silu and an i8 form saved (327 MB, 4.2
-// TB/s; 94 to 120 us with 16 chunks in each of 512 lanes).
+// in row segments of 128 bytes), 65 us with gelu (68 us traced, in which the
+// vector units issue 68 % of the time and 16 waves a CU wait 45 % of theirs), 78
+// to 90 us traced with silu and an i8 form saved (330 MB, 3.7 to 4.2 TB/s; 94 to
+// 120 us with 16 chunks in each of 512 lanes).
 template <class T, int KIND, int PK, int ACT>
 __global__ __launch_bounds__(kSlabThreads) void norm_slab_kernel(const ForwardArgs<PK> A) {
   constexpr bool WHOLE = KIND == kNormWhole, TAIL = KIND == kNormAny, LINEAR = !TAIL;
@@ -181,8 +182,8 @@ __global__ __launch_bounds__(kSlabThreads) void norm_slab_kernel(const ForwardAr
 // Statistics of a run of rows: (mean, sum of squared deviations) of every
 // group's piece in this channel block, into part[n][g][run][piece].  The
 // loads keep the data in the caches for the second pass.  [4, 64, 64, 320]
-// bfloat16, groups of 10 channels: 6.2 us for 10.5 MB, of which about 2.5 us
-// pass before a kernel's first loads arrive.
+// bfloat16, groups of 10 channels: 6.4 us (median of 30 traced calls) for 10.5
+// MB, of which about 2.5 us pass before a kernel's first loads arrive.
 template <class T, int KIND>
 __global__ __launch_bounds__(kRowThreads) void norm_stats_kernel(const NormStats A) {
   constexpr bool WHOLE = KIND == kNormWhole, TAIL = KIND == kNormAny, LINEAR = !TAIL;
@@ -275,7 +276,7 @@ __device__ __forceinline__ float2 join_parts(const NormCore& A, uint32_t n, uint
 // y, and where asked mean, rstd and the 8-bit form of x.  The first chunks
 // are on their way while the parts are joined, by every workgroup for its own
 // groups, which saves a launch of about 2.5 us.  [4, 64, 64, 320] bfloat16
-// with silu: 8.2 us, x from the L2s.
+// with silu: 8.9 us (median of 30 traced calls); x passes the L2s once more.
 template <class T, int KIND, int PK, int ACT>
 __global__ __launch_bounds__(kRowThreads) void norm_apply_kernel(const ForwardArgs<PK> A) {
   constexpr bool WHOLE = KIND == kNormWhole, TAIL = KIND == kNormAny, LINEAR = !TAIL;

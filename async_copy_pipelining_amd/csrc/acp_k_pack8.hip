@@ -4,14 +4,14 @@
 // cross-lane moves, so nothing goes through LDS.
 //
 // Each element is read and written once: large tensors are bound by HBM
-// (times of the kernels alone; a plain copy reaches 6.0 TB/s), small ones by
-// the launch.  A chunk's address, scale and codes come from its index alone,
-// so a lane has its one or two chunks in flight and no loop.
-//   pack8     [262144, 256] bfloat16, rows 264 elements apart, i8: 36.9 us, 5.5 TB/s
-//   unpack8   the same: 33.1 us, 6.1 TB/s
-//   act_forward   [8192, 5632] bfloat16, gated, both operands saved as i8: 63.9 us, 5.8 TB/s
-//   act_backward  the same: 59.1 us, 6.3 TB/s
-//   pack8, unpack8 of [64, 1000] float32: 2.4 and 1.9 us
+// (a plain copy reaches 6.0 TB/s), small ones by the launch.  A chunk's
+// address, scale and codes come from its index alone, so a lane has its one
+// or two chunks in flight and no loop.  Least and median of 30 traced calls:
+//   pack8     [262144, 256] bfloat16, rows 264 elements apart, i8: 36.8 and 37.5 us, 5.4 TB/s
+//   unpack8   the same: 32.2 and 34.2 us, 5.9 TB/s (both in a row of calls 69.0 us, 5.9 TB/s)
+//   act_forward   [8192, 5632] bfloat16, gated, both operands saved as i8: 65.1 and 73.8 us, 5.0 TB/s
+//   act_backward  the same: 59.4 and 61.5 us, 6.0 TB/s (both in a row of calls 126 us, 5.9 TB/s)
+//   pack8, unpack8 of [64, 1000] float32: 2.5 and 2.8, 2.6 and 2.8 us
 #include "acp_dev_rows.hpp"
 
 namespace acp {

@@ -391,9 +391,9 @@ enum NormForm { kFormRow, kFormSlab, kFormParts };
 //   with eight, whose parts the next pass has to read), at most 256 a sample;
 //   the pass that writes the result: sixteen a CU (176 us; 180 with four);
 // * by parts, tensors that the eight L2s hold together: the same split for
-//   both passes, so that a workgroup of the second finds its data in the L2
-//   that the first brought it to ([4, 64, 64, 320] bfloat16 14.7 us with 512
-//   workgroups in both; 16.3 with 512 and 1024, 21.5 with 1024 and 2048).
+//   both passes, a workgroup of the second where one of the first was ([4, 64,
+//   64, 320] bfloat16 14.7 us with 512 workgroups in both; 16.3 with 512 and 1024,
+//   21.5 with 1024 and 2048; x passes the L2s a second time all the same).
 //   Few bytes take few workgroups, and so few parts ([3, 37, 41, 352] float32
 //   backward 17.3 us with 256, 18.1 with 512);
 // * per row: four a CU, forward (50 us; 52 with two, 61 with sixteen); backward
@@ -536,7 +536,10 @@ bool plan_slab(const NormDims& d, NormPlan* P) {
   // [4000, 4, 640] forward and backward 86 and 95)
   const bool few_rows = d.rows <= (d.block ? 1 : 4);
   if (d.backward && !lines && !few_rows && d.samples * blocks * threads > 256 * 512) return false;
-  // LDS that a launch may ask for without raising the kernel's limit
+  // LDS that a launch may ask for without raising the kernel's limit.  Backward,
+  // 16-bit rows of more than 2048 channels in one group need more and go by
+  // parts, one row a sample at eight times their floor ([16384, 4096] bfloat16,
+  // one group 554 us, floor 67)
   const int64_t pairs = d.backward ? threads * (d.v + 1) + lanes * d.v * 5 / 2 : threads * (whole ? 1 : d.v);
   if ((pairs + lanes * d.v / d.per + 3) * 8 > 65536) return false;
   P->form = kFormSlab;
