@@ -31,9 +31,9 @@ try:
     # first makes libacp.so bind to that copy, so torch-allocated memory and
     # streams and acp's launches live in one runtime.
     import torch
-    _Tensor, _F32 = torch.Tensor, torch.float32
+    _Tensor, _F32, _F64, _I32 = torch.Tensor, torch.float32, torch.float64, torch.int32
 except ImportError:  # pragma: no cover - acp itself does not need torch
-    _Tensor, _F32 = (), None
+    _Tensor, _F32, _F64, _I32 = (), None, None, None
 
 _lib = ctypes.CDLL(LIB_PATH)
 
@@ -56,6 +56,12 @@ ACP_PACK_I8, ACP_PACK_E4M3 = range(2)
 FORMATS = {"i8": ACP_PACK_I8, "e4m3": ACP_PACK_E4M3}
 ACP_ACT_NONE, ACP_ACT_SILU, ACP_ACT_GELU = range(3)
 ACTIVATIONS = {"none": ACP_ACT_NONE, "silu": ACP_ACT_SILU, "gelu": ACP_ACT_GELU}
+# acp_rotary_layout / acp_rotary_scaling
+ACP_ROTARY_HALVES, ACP_ROTARY_PAIRS = range(2)
+ROTARY_LAYOUTS = {"halves": ACP_ROTARY_HALVES, "pairs": ACP_ROTARY_PAIRS}
+ACP_ROTARY_PLAIN, ACP_ROTARY_LINEAR, ACP_ROTARY_BASE, ACP_ROTARY_BANDS = range(4)
+ROTARY_SCALINGS = {"plain": ACP_ROTARY_PLAIN, "linear": ACP_ROTARY_LINEAR, "base": ACP_ROTARY_BASE,
+                   "bands": ACP_ROTARY_BANDS}
 ACP_MAX_RANK = 5
 
 
@@ -103,6 +109,41 @@ class acp_packed8(ctypes.Structure):
 
 _PACKED_P = ctypes.POINTER(acp_packed8)
 
+
+class acp_rotary(ctypes.Structure):
+    """Rotary positions: float64 frequencies, turned channels, layout, scale of cos and sin."""
+    _fields_ = [("frequencies", _P), ("rotated", ctypes.c_int32), ("layout", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+    def __init__(self, frequencies, rotated: int, layout="halves", scale: float = 1.0):
+        super().__init__(_array(frequencies, max(0, int(rotated)) // 2, _F64, "the frequencies"), int(rotated),
+                         ROTARY_LAYOUTS[layout] if isinstance(layout, str) else int(layout), scale)
+
+
+class acp_paged_cache(ctypes.Structure):
+    """Keys and values of a cache, each a descriptor or an 8-bit form."""
+    _fields_ = [("k", _DESC_P), ("v", _DESC_P), ("k8", _PACKED_P), ("v8", _PACKED_P)]
+
+    def __init__(self, k, v):
+        super().__init__()
+        for name, x in (("k", k), ("v", v)):
+            if x is not None:
+                setattr(self, name + "8" if isinstance(x, acp_packed8) else name, ctypes.pointer(x))
+
+
+class acp_sequences(ctypes.Structure):
+    """The sequences of a batch: int32 lengths, pages and (None: one token each) starts."""
+    _fields_ = [("starts", _P), ("lengths", _P), ("pages", _P), ("sequences", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("max_length", ctypes.c_int32)]
+
+    def __init__(self, lengths, pages, sequences: int, max_pages: int, starts=None, max_length: int = 0):
+        super().__init__(_array(starts, sequences + 1, _I32, "starts"), _array(lengths, sequences, _I32, "lengths"),
+                         _array(pages, sequences * max_pages, _I32, "pages"), sequences, max_pages, max_length)
+
+
+_ROTARY_P = ctypes.POINTER(acp_rotary)
+_CACHE_P = ctypes.POINTER(acp_paged_cache)
+_SEQUENCES_P = ctypes.POINTER(acp_sequences)
+
 _SIGS = {
     "acp_abi_version": ([], _I),
     "acp_last_error": ([], ctypes.c_char_p),
@@ -125,6 +166,13 @@ _SIGS = {
                        _I),
     "acp_group_norm_backward": ([_DESC_P, _P, _P, _DESC_P, _DESC_P, _PACKED_P, _P, _P, _P, _P, _I, _I, _P,
                                  ctypes.c_int64, _P], _I),
+    "acp_rotary_frequencies": ([_P, _I, ctypes.c_double, _I] + [ctypes.c_double] * 4, _I),
+    "acp_rotate": ([_DESC_P, _DESC_P, _DESC_P, _DESC_P, _P, _ROTARY_P, _I, _P], _I),
+    "acp_head_norm": ([_DESC_P, _DESC_P, _P, _DESC_P, _DESC_P, _P, ctypes.c_float, _P, _ROTARY_P, _P], _I),
+    "acp_head_norm_workspace": ([_DESC_P, _DESC_P, ctypes.POINTER(ctypes.c_int64)], _I),
+    "acp_head_norm_backward": ([_DESC_P, _P, _DESC_P, _DESC_P, _P, _DESC_P, _P, _DESC_P, _DESC_P, _P, ctypes.c_float,
+                                _P, _ROTARY_P, _P, ctypes.c_int64, _P], _I),
+    "acp_cache_append": ([_CACHE_P, _DESC_P, _DESC_P, _SEQUENCES_P, _ROTARY_P, _DESC_P, _DESC_P, _P], _I),
     "acp_debug_lds_image": ([_DESC_P, ctypes.c_int64, _I, _P, _P], _I),
     "acp_debug_ring_trace": ([_I, _I, _I, _I, _P, _P], _I),
     "acp_debug_stream_copy": ([_P, _P, ctypes.c_int64, _I, _P], _I),
@@ -251,21 +299,25 @@ def _refuse(reason: str) -> None:
     raise AcpError(ACP_ERR_INVALID, reason)
 
 
-def _floats(x, n: int, what: str) -> int | None:
-    """Address of a float32 tensor of at least n values; an address or None as it is.
+def _array(x, n: int, dtype, what: str) -> int | None:
+    """Address of a tensor of at least n values of dtype; an address or None as it is.
 
-    The library sees addresses alone: a parameter of another type, or one that
+    The library sees addresses alone: an array of another type, or one that
     is too short, would be read past its end.
     """
     if not isinstance(x, _Tensor):
         return _ptr(x)
-    if x.dtype is not _F32:
-        _refuse(f"{what} must be float32, not {x.dtype}")
-    if x.nbytes < 4 * n:
+    if x.dtype is not dtype:
+        _refuse(f"{what} must be {str(dtype).removeprefix('torch.')}, not {x.dtype}")
+    if x.numel() < n:
         _refuse(f"{what} holds {x.numel()} values, {n} are needed")
     if not x.is_contiguous():
         _refuse(f"{what} has gaps between its values")
     return x.data_ptr()
+
+
+def _floats(x, n: int, what: str) -> int | None:
+    return _array(x, n, _F32, what)
 
 
 def _space(x, nbytes: int) -> int | None:
@@ -348,6 +400,71 @@ def acp_group_norm_backward(dx: acp_tile_desc, dgamma, dbeta, dy: acp_tile_desc,
                                       _floats(mean, n, "mean"), _floats(rstd, n, "rstd"), _floats(gamma, c, "gamma"),
                                       _floats(beta, c, "beta"), groups, _act(act),
                                       _space(workspace, workspace_bytes), workspace_bytes, _handle(stream))
+    if st:
+        _check(st)
+
+
+def acp_rotary_frequencies(rotated: int, base: float = 10000.0, scaling="plain", factor: float = 1.0,
+                           length: float = 0.0, low: float = 1.0, high: float = 32.0) -> list[float]:
+    """The frequencies of the turned pairs, for a float64 tensor on the device."""
+    out = (ctypes.c_double * max(1, int(rotated) // 2))()
+    _check(_lib.acp_rotary_frequencies(out, int(rotated), base,
+                                       ROTARY_SCALINGS[scaling] if isinstance(scaling, str) else int(scaling), factor,
+                                       length, low, high))
+    return list(out)
+
+
+def _tokens(x: acp_tile_desc) -> int:
+    """Tokens of [..., heads, channels] (0: not known here)."""
+    shape = x.shape if x is not None else None
+    return math.prod(shape[:-2]) if shape else 0
+
+
+def _channels(x: acp_tile_desc) -> int:
+    shape = x.shape if x is not None else None
+    return shape[-1] if shape else 0
+
+
+def acp_rotate(yq: acp_tile_desc, q: acp_tile_desc, yk: acp_tile_desc | None, k: acp_tile_desc | None, positions,
+               rotary: acp_rotary, backward: bool = False, stream=None) -> None:
+    st = _lib.acp_rotate(yq, q, yk, k, _array(positions, _tokens(q), _I32, "positions"), rotary, 1 if backward else 0,
+                         _handle(stream))
+    if st:
+        _check(st)
+
+
+def acp_head_norm(yq: acp_tile_desc, q: acp_tile_desc, wq, yk: acp_tile_desc | None, k: acp_tile_desc | None, wk,
+                  eps: float, positions=None, rotary: acp_rotary | None = None, stream=None) -> None:
+    c = _channels(q)
+    st = _lib.acp_head_norm(yq, q, _floats(wq, c, "wq"), yk, k, _floats(wk, c, "wk"), eps,
+                            _array(positions, _tokens(q), _I32, "positions"), rotary, _handle(stream))
+    if st:
+        _check(st)
+
+
+def acp_head_norm_workspace(q: acp_tile_desc, k: acp_tile_desc | None = None) -> int:
+    n = ctypes.c_int64()
+    _check(_lib.acp_head_norm_workspace(q, k, ctypes.byref(n)))
+    return n.value
+
+
+def acp_head_norm_backward(dq: acp_tile_desc, dwq, dyq: acp_tile_desc, q: acp_tile_desc, wq, dk: acp_tile_desc | None,
+                           dwk, dyk: acp_tile_desc | None, k: acp_tile_desc | None, wk, eps: float, positions=None,
+                           rotary: acp_rotary | None = None, workspace=None, workspace_bytes: int = 0,
+                           stream=None) -> None:
+    c = _channels(q)
+    st = _lib.acp_head_norm_backward(dq, _floats(dwq, c, "dwq"), dyq, q, _floats(wq, c, "wq"), dk,
+                                     _floats(dwk, c, "dwk"), dyk, k, _floats(wk, c, "wk"), eps,
+                                     _array(positions, _tokens(q), _I32, "positions"), rotary,
+                                     _space(workspace, workspace_bytes), workspace_bytes, _handle(stream))
+    if st:
+        _check(st)
+
+
+def acp_cache_append(cache: acp_paged_cache, k: acp_tile_desc, v: acp_tile_desc, sequences: acp_sequences,
+                     rotary: acp_rotary | None = None, yq: acp_tile_desc | None = None, q: acp_tile_desc | None = None,
+                     stream=None) -> None:
+    st = _lib.acp_cache_append(cache, k, v, sequences, rotary, yq, q, _handle(stream))
     if st:
         _check(st)
 

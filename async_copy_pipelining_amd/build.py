@@ -41,6 +41,9 @@ SOURCES = [
     ("acp_k_norm_f16.hip", True),
     ("acp_k_norm_bf16.hip", True),
     ("acp_k_norm_f32.hip", True),
+    ("acp_k_heads.hip", True),
+    ("acp_k_heads_bwd.hip", True),
+    ("acp_k_append.hip", True),
 ]
 
 

@@ -3,3 +3,4 @@
 // the device attributes of acp_api.cpp.
 #include "acp_api.cpp"
 #include "acp_rows_api.hpp"
+#include "acp_heads_api.hpp"

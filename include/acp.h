@@ -16,6 +16,12 @@
  *   acp_act_forward, acp_act_backward         (gated) activations that keep their operands in 8 bits
  *   acp_group_norm, acp_group_norm_backward   group norm with an activation, channels last
  *
+ * and over the heads of an attention layer's tensors:
+ *
+ *   acp_rotate                               rotary positions, and their backward pass
+ *   acp_head_norm, acp_head_norm_backward    norms of queries and keys, with the rotation
+ *   acp_cache_append                         new keys and values into a paged cache
+ *
  * plus the host-side descriptor encoder / planner they share.  The method
  * follows four pages:
  *   [tma]    "copy_async -> tma"            (TVM TIRx docs)
@@ -443,6 +449,134 @@ acp_status acp_group_norm_backward(const acp_tile_desc* dx, float* dgamma, float
                                    const acp_tile_desc* x, const acp_packed8* saved, const float* mean,
                                    const float* rstd, const float* gamma, const float* beta, int groups,
                                    acp_activation act, void* workspace, int64_t workspace_bytes, void* hip_stream);
+
+/* ------------------------------------------------------------------------
+ * Head operators: what lies between the projections of an attention layer and
+ * its output.  Their tensors are [..., heads, channels] of f16, bf16 or f32:
+ * the dims before the heads are tokens, in row-major order, and have to join
+ * into at most two.  All tensors of a call have one type and the same token
+ * dims; keys may have fewer heads than queries.  Bases need only their
+ * element's alignment.  What is said of the row operators holds here too:
+ * overlaps (but an output may be the very tensor that it is made from: the
+ * same address, shape and strides), empty tensors, workspaces, fixed order of
+ * all sums, streams and graphs.  A head goes up to 1024 channels (f32: 512;
+ * somewhat fewer where turned and other channels end inside chunks), else
+ * ACP_ERR_UNSUPPORTED. */
+
+/* Rotary positions.  At position p the pair i of a head's first `rotated`
+ * channels turns by the angle p * frequencies[i]:
+ *   (a, b) -> scale * (a cos - b sin, b cos + a sin)
+ *   ACP_ROTARY_HALVES  a and b are channels i and i + rotated / 2
+ *   ACP_ROTARY_PAIRS   a and b are channels 2 i and 2 i + 1
+ * The other channels stay as they are.  Angles are formed in float64, so far
+ * positions lose nothing; cos and sin are good to 2^-22. */
+typedef enum { ACP_ROTARY_HALVES = 0, ACP_ROTARY_PAIRS = 1 } acp_rotary_layout;
+
+typedef struct {
+  const double* frequencies; /* device, rotated / 2, radians a position */
+  int32_t rotated;           /* even, 2 up to the head's channels */
+  int32_t layout;            /* acp_rotary_layout */
+  float scale;               /* of cos and sin, finite; 1 but for some ways to lengthen a context */
+} acp_rotary;
+
+/* Frequencies of a rotation, written to host memory (rotated / 2 values, for
+ * the caller to put on the device): f_i = base^(-2 i / rotated), then
+ *   ACP_ROTARY_PLAIN   as they are
+ *   ACP_ROTARY_LINEAR  f_i / factor: positions factor times as dense
+ *   ACP_ROTARY_BASE    base * factor^(rotated / (rotated - 2)) in the base's
+ *                      place: the slowest pair turns factor times as slowly,
+ *                      the fastest as before
+ *   ACP_ROTARY_BANDS   f_i (m + (1 - m) / factor), m = (t - low) / (high - low)
+ *                      within 0 and 1, t = length f_i / 2 pi the turns that the
+ *                      pair makes in the context of `length` positions that a
+ *                      model was trained on: pairs of at least `high` turns are
+ *                      kept, of at most `low` are slowed down by the factor
+ * factor >= 1; length, low and high are used by ACP_ROTARY_BANDS alone. */
+typedef enum { ACP_ROTARY_PLAIN = 0, ACP_ROTARY_LINEAR = 1, ACP_ROTARY_BASE = 2, ACP_ROTARY_BANDS = 3 } acp_rotary_scaling;
+
+acp_status acp_rotary_frequencies(double* frequencies, int rotated, double base, acp_rotary_scaling scaling,
+                                  double factor, double length, double low, double high);
+
+/* yq = q and yk = k turned by each token's position, in one launch.
+ *   yk, k      NULL: queries alone
+ *   positions  device int32, one a token; NULL: a token's index in the last of
+ *              the token dims
+ *   backward   not 0: turned back, by minus the angle.  With gradients in the
+ *              place of q and k that is the backward pass
+ * Computed in float32 and rounded once. */
+acp_status acp_rotate(const acp_tile_desc* yq, const acp_tile_desc* q, const acp_tile_desc* yk, const acp_tile_desc* k,
+                      const int32_t* positions, const acp_rotary* rotary, int backward, void* hip_stream);
+
+/* Norm of every head of queries and keys, then the rotation, in one pass:
+ *   y = R (x * rstd * w),  rstd = 1 / sqrt(mean of x^2 over the head + eps)
+ *   wq, wk     device float32 [channels]; NULL: 1
+ *   eps        finite, >= 0
+ *   rotary     NULL: no rotation; else positions as acp_rotate has them
+ * A head with a NaN or an infinity, or whose squares' sum overflows float32,
+ * gives NaN throughout, channels that are not turned included; squares below
+ * float32's range count as zero. */
+acp_status acp_head_norm(const acp_tile_desc* yq, const acp_tile_desc* q, const float* wq, const acp_tile_desc* yk,
+                         const acp_tile_desc* k, const float* wk, float eps, const int32_t* positions,
+                         const acp_rotary* rotary, void* hip_stream);
+
+/* Bytes of workspace that acp_head_norm_backward needs at most. */
+acp_status acp_head_norm_workspace(const acp_tile_desc* q, const acp_tile_desc* k, int64_t* bytes);
+
+/* Its backward pass, from the gradients of its outputs and its inputs:
+ *   g = R^T dy,  dw = sum over tokens and heads of g * x * rstd
+ *   dx = rstd * (g w - x rstd^2 M(g w x)),  M the mean over the head
+ * dwq and dwk (device float32 [channels]) are written, not added to; NULL: not
+ * wanted.  The workspace is not read where neither is. */
+acp_status acp_head_norm_backward(const acp_tile_desc* dq, float* dwq, const acp_tile_desc* dyq,
+                                  const acp_tile_desc* q, const float* wq, const acp_tile_desc* dk, float* dwk,
+                                  const acp_tile_desc* dyk, const acp_tile_desc* k, const float* wk, float eps,
+                                  const int32_t* positions, const acp_rotary* rotary, void* workspace,
+                                  int64_t workspace_bytes, void* hip_stream);
+
+/* A paged cache of keys and values: descriptors [pages, positions of a page,
+ * heads, channels] with any strides (so pages may hold heads or positions
+ * first), of the calls' type, or both in 8 bits: the same descriptors of u8
+ * codes, with one scale a row (a block of at least the channels), scales packed
+ * [pages, positions, heads]. */
+typedef struct {
+  const acp_tile_desc* k;
+  const acp_tile_desc* v;
+  const acp_packed8* k8; /* in the place of k and v, which are NULL then */
+  const acp_packed8* v8;
+} acp_paged_cache;
+
+/* The sequences of a batch.  All arrays are device int32.
+ *   starts      [sequences + 1], ascending: sequence s has the tokens from
+ *               starts[s] up to before starts[s + 1], none where these are
+ *               equal.  NULL: token s is the one token of sequence s
+ *   lengths     [sequences]: positions of the sequence, its tokens here, which
+ *               are the last of them, included
+ *   pages       [sequences, max_pages], packed: position p lies in the page
+ *               pages[s][p / positions of a page]
+ *   max_length  no sequence is longer, where the caller knows it (0: not
+ *               known).  Work is split by it; results do not depend on it
+ * Nothing of it is read on the host, so a captured graph may be replayed with
+ * other contents.  A page number outside the cache, or a position past
+ * max_pages, is a position without a page: what is appended there is left
+ * out, and attention does not see it. */
+typedef struct {
+  const int32_t* starts;
+  const int32_t* lengths;
+  const int32_t* pages;
+  int32_t sequences;
+  int32_t max_pages;
+  int32_t max_length;
+} acp_sequences;
+
+/* Writes the new keys, turned by their positions (rotary NULL: as they are),
+ * and the new values [tokens, kv heads, channels] into the pages of their
+ * positions, and where q is given the queries, turned, to yq.  8-bit caches:
+ * codes and scales as acp_pack8 has them, of the turned keys in float32.
+ * Tokens of no sequence leave all outputs as they were; of two tokens with one
+ * place in the cache, one is written. */
+acp_status acp_cache_append(const acp_paged_cache* cache, const acp_tile_desc* k, const acp_tile_desc* v,
+                            const acp_sequences* sequences, const acp_rotary* rotary, const acp_tile_desc* yq,
+                            const acp_tile_desc* q, void* hip_stream);
 
 /* Test export: the raw LDS bytes of tile `tile_index` of `src` after its
  * direct-to-LDS load, written to `out_bytes` (device, tile_bytes long). */

@@ -26,6 +26,8 @@ Modules
               elementwise, streamed fma, store with reduce-add, row sums).
 ``rows``      the row operators in binary64: 8-bit checkpoints, activations,
               group norm with an activation and its backward pass.
+``heads``     the head operators in binary64: rotary positions, norms of heads
+              and their backward pass, paged caches, attention over them.
 
 Only ``tests/``, ``__graft_entry__.smoke()`` and the ``cpu_baseline`` leg of
 ``bench.py`` may import this package.  It shares no code with the HIP path
