@@ -173,6 +173,8 @@ _SIGS = {
     "acp_head_norm_backward": ([_DESC_P, _P, _DESC_P, _DESC_P, _P, _DESC_P, _P, _DESC_P, _DESC_P, _P, ctypes.c_float,
                                 _P, _ROTARY_P, _P, ctypes.c_int64, _P], _I),
     "acp_cache_append": ([_CACHE_P, _DESC_P, _DESC_P, _SEQUENCES_P, _ROTARY_P, _DESC_P, _DESC_P, _P], _I),
+    "acp_cache_attention_workspace": ([_DESC_P, _CACHE_P, _SEQUENCES_P, ctypes.POINTER(ctypes.c_int64)], _I),
+    "acp_cache_attention": ([_DESC_P, _DESC_P, _CACHE_P, _SEQUENCES_P, ctypes.c_float, _P, ctypes.c_int64, _P], _I),
     "acp_debug_lds_image": ([_DESC_P, ctypes.c_int64, _I, _P, _P], _I),
     "acp_debug_ring_trace": ([_I, _I, _I, _I, _P, _P], _I),
     "acp_debug_stream_copy": ([_P, _P, ctypes.c_int64, _I, _P], _I),
@@ -465,6 +467,20 @@ def acp_cache_append(cache: acp_paged_cache, k: acp_tile_desc, v: acp_tile_desc,
                      rotary: acp_rotary | None = None, yq: acp_tile_desc | None = None, q: acp_tile_desc | None = None,
                      stream=None) -> None:
     st = _lib.acp_cache_append(cache, k, v, sequences, rotary, yq, q, _handle(stream))
+    if st:
+        _check(st)
+
+
+def acp_cache_attention_workspace(q: acp_tile_desc, cache: acp_paged_cache, sequences: acp_sequences) -> int:
+    n = ctypes.c_int64()
+    _check(_lib.acp_cache_attention_workspace(q, cache, sequences, ctypes.byref(n)))
+    return n.value
+
+
+def acp_cache_attention(out: acp_tile_desc, q: acp_tile_desc, cache: acp_paged_cache, sequences: acp_sequences,
+                        scale: float, workspace=None, workspace_bytes: int = 0, stream=None) -> None:
+    st = _lib.acp_cache_attention(out, q, cache, sequences, scale, _space(workspace, workspace_bytes),
+                                  workspace_bytes, _handle(stream))
     if st:
         _check(st)
 

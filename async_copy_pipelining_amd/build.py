@@ -44,6 +44,11 @@ SOURCES = [
     ("acp_k_heads.hip", True),
     ("acp_k_heads_bwd.hip", True),
     ("acp_k_append.hip", True),
+    ("acp_k_attn_step_f16.hip", True),
+    ("acp_k_attn_step_bf16.hip", True),
+    ("acp_k_attn_prompt_f16.hip", True),
+    ("acp_k_attn_prompt_bf16.hip", True),
+    ("acp_k_attn_join.hip", True),
 ]
 
 

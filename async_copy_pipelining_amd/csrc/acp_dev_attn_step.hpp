@@ -1,0 +1,440 @@
+// Attention of few rows for each of the cache's heads: single tokens, short
+// chunks.  Bound by reading the cache.
+//
+// The rows that share keys, padded to 16, are columns of the products
+// S^T = K Q^T and O^T = V^T P^T (16x16x32 matrix instructions), so that a row's
+// scores lie in one lane's registers and three others', and the weights of S^T
+// are the second product's operand as they are: its sum over keys takes them in
+// the order in which the first leaves them.
+//
+// Each of the four waves takes every fourth step of 32 keys with sums of its
+// own; they meet once, at the end.  A lane loads its part of K straight into
+// the first product's operand.  V goes through LDS, where the transposing reads
+// turn rows of channels into columns of keys; only the wave itself reads what
+// it wrote, so there is no barrier in the loop.  The next step's rows load
+// while this one is computed: 16 KiB a wave for 128 channels of 16 bits, and
+// eight waves a CU keep twice the bytes in flight that its share of HBM needs.
+#pragma once
+
+#include "acp_dev_attn.hpp"
+
+namespace acp {
+namespace dev {
+
+template <class T, int FMT, int DP>
+struct StepShape {
+  static constexpr int kBytes = FMT == kCacheSame ? 2 : 1;      // of a channel
+  static constexpr int kRow = DP * kBytes;                      // of a row in LDS
+  static constexpr int kPieces = kRow / 16;                     // 16-byte pieces of a row
+  static constexpr int kSteps = DP / 32;                        // of the first product
+  static constexpr int kKRegs = DP * kBytes / 64;               // pieces of K a lane has of one of its two keys
+  static constexpr int kVRows = 64 / kPieces;                   // rows that one load of the wave covers
+  static constexpr int kVRegs = kStepKeys / kVRows;
+  static constexpr int kWaveBytes = kStepKeys * kRow;
+  // the waves' sums meet there afterwards, 128 channels at a time
+  static constexpr int kJoinPitch = 132;
+  static constexpr int kJoinBytes = 4 * kStepRows * kJoinPitch * 4;
+  static constexpr int kLds = 4 * kWaveBytes > kJoinBytes ? 4 * kWaveBytes : kJoinBytes;
+};
+
+// Where piece c of row r lies in a wave's rows of V.  A transposing read takes
+// 32 bytes (16 channels) of eight rows, or 16 bytes of sixteen (8-bit codes), in
+// one of its turns: units of that size are permuted by the row, so that these
+// fill the 64 banks.
+template <class S, int FMT>
+__device__ __forceinline__ uint32_t v_at(uint32_t row, uint32_t piece) {
+  constexpr uint32_t kRows = S::kRow >= 256 ? 1u : 256u / S::kRow;  // rows side by side in the banks
+  uint32_t p;
+  if constexpr (FMT == kCacheSame) {
+    constexpr uint32_t kUnits = S::kPieces / 2;
+    p = ((piece >> 1) ^ ((row / kRows) & 7u & (kUnits - 1u))) << 1 | (piece & 1u);
+  } else {
+    p = piece ^ ((row / kRows) & (S::kPieces - 1u));
+  }
+  return row * S::kRow + p * 16u;
+}
+
+template <class T, int FMT, int DP>
+__global__ __launch_bounds__(kAttendThreads, DP == 256 ? 1 : 2) void attend_step_kernel(const AttendArgs A) {
+  using S = StepShape<T, FMT, DP>;
+  __shared__ __attribute__((aligned(16))) char lds[S::kLds];
+  __shared__ float join_stat[4][kStepRows][2];
+  __shared__ uint32_t odd_rows;
+  const AttendPlace at(A);
+  Tile t;
+  if (!t.find<kStepRows>(A, at.slot)) return;
+  const uint32_t splits = t.splits(A);
+  if (at.split >= splits) return;
+  const uint32_t lane = threadIdx.x & 63u, wave = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
+  const uint32_t col = lane & 15u, quarter = lane >> 4;
+  const uint32_t keys = static_cast<uint32_t>(t.keys);
+  const bool exact = A.dim == DP;
+  char* mine = lds + wave * S::kWaveBytes;
+
+  // the lane's row, and its part of Q: channel order as K's pieces have it
+  const uint32_t row = t.first + col;
+  const bool real = row < static_cast<uint32_t>(t.rows);
+  const int32_t sees = real ? t.position(A, row) : -1;
+  rw4 q[S::kSteps];
+  {
+    uint32_t token, head;
+    t.place(A, real ? row : t.first, at.kv, &token, &head);
+    const char* qr = head_row(A, A.q, token, head);
+#pragma unroll
+    for (int s = 0; s < S::kSteps; ++s) {
+      const uint32_t c = FMT == kCacheSame ? 32u * s + 8u * quarter : 64u * (s / 2) + 16u * quarter + 8u * (s & 1);
+      q[s] = rw4{0u, 0u, 0u, 0u};
+      if (real && c < A.dim) q[s] = *reinterpret_cast<const rw4_any*>(qr + c * 2);
+    }
+  }
+
+  af4 o[DP / 16];
+#pragma unroll
+  for (int d = 0; d < DP / 16; ++d) o[d] = af4{0.0f, 0.0f, 0.0f, 0.0f};
+  float m = -__builtin_inff(), l = 0.0f;
+  int v_exp = -200;  // float16 with 8-bit values: o holds sums in units of 2^v_exp
+
+  // The wave's steps: first keys, in ascending order
+  const uint32_t per = A.chunk / (4u * kStepKeys);
+  struct Cursor {
+    uint32_t key, n;
+  };
+  auto advance = [&](Cursor* c) {
+    c->key += 4u * kStepKeys;
+    if (++c->n == per) {
+      c->n = 0;
+      c->key += (A.splits - 1u) * A.chunk;
+    }
+  };
+  // Lanes 0..31 (and again 32..63) have a key each: its page, or -1
+  auto page_at = [&](uint32_t key0) -> int32_t {
+    const uint32_t key = key0 + (lane & 31u);
+    uint32_t index;
+    return key < keys ? key_page(A, t.seq, key, &index) : -1;
+  };
+  struct Rows {  // of the lane's key
+    int64_t k, v;
+    uint32_t here;  // keys that have a page, by bits: uniform
+    float ks, vs;
+  };
+  auto rows_at = [&](uint32_t key0, int32_t page) {
+    Rows r;
+    const uint32_t key = key0 + (lane & 31u);
+    const uint32_t index = key - divide(key, A.batch.page) * A.batch.page.d;
+    const int64_t g = page < 0 ? 0 : page;
+    r.k = g * A.k.s[0] + index * A.k.s[1];
+    r.v = g * A.v.s[0] + index * A.v.s[1];
+    r.here = static_cast<uint32_t>(__builtin_amdgcn_ballot_w64(page >= 0));
+    r.ks = r.vs = 0.0f;
+    if constexpr (FMT != kCacheSame) {
+      if (page >= 0) {
+        const uint64_t s = (static_cast<uint64_t>(page) * A.batch.page.d + index) * A.kv_heads.d + at.kv;
+        r.ks = A.k.scales[s];
+        r.vs = A.v.scales[s];
+      }
+    }
+    return r;
+  };
+  auto from_lane = [](int64_t v, uint32_t src) {
+    const int lo = __builtin_amdgcn_ds_bpermute(static_cast<int>(src * 4u), static_cast<int>(v));
+    const int hi = __builtin_amdgcn_ds_bpermute(static_cast<int>(src * 4u), static_cast<int>(v >> 32));
+    return static_cast<int64_t>(static_cast<uint32_t>(lo)) | static_cast<int64_t>(hi) << 32;
+  };
+  const char* kbase = A.k.p + at.kv * A.k.s[2];
+  const char* vbase = A.v.p + at.kv * A.v.s[2];
+  rw4 kr[2][S::kKRegs], vr[S::kVRegs];
+  // where a piece of 16 bytes at byte c of a row holds channels: all of it, or (codes) its first 8
+  const uint32_t row_bytes = A.dim * S::kBytes;
+  auto piece_of = [&](const char* p, uint32_t c, bool there) {
+    rw4 w{0u, 0u, 0u, 0u};
+    if (there && c + 16u <= row_bytes) {
+      w = *reinterpret_cast<const rw4_any*>(p);
+    } else if (FMT != kCacheSame && there && c < row_bytes) {
+      const rw2 u = *reinterpret_cast<const rw2_any*>(p);
+      w = rw4{u[0], u[1], 0u, 0u};
+    }
+    return w;
+  };
+  auto load_k = [&](const Rows& r) {
+    const char* p[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) p[h] = kbase + from_lane(r.k, 16u * h + col) + 16u * quarter;
+    if (exact && r.here == 0xFFFFFFFFu) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < S::kKRegs; ++i) kr[h][i] = *reinterpret_cast<const rw4_any*>(p[h] + 64 * i);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < S::kKRegs; ++i)
+          kr[h][i] = piece_of(p[h] + 64 * i, 64u * i + 16u * quarter, r.here >> (16u * h + col) & 1u);
+    }
+  };
+  auto load_v = [&](const Rows& r) {
+    const uint32_t piece = lane % S::kPieces, first = lane / S::kPieces;
+    const char* p[S::kVRegs];
+#pragma unroll
+    for (int i = 0; i < S::kVRegs; ++i) p[i] = vbase + from_lane(r.v, first + i * S::kVRows) + piece * 16u;
+    if (exact && r.here == 0xFFFFFFFFu) {
+#pragma unroll
+      for (int i = 0; i < S::kVRegs; ++i) vr[i] = *reinterpret_cast<const rw4_any*>(p[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < S::kVRegs; ++i)
+        vr[i] = piece_of(p[i], piece * 16u, r.here >> (first + i * S::kVRows) & 1u);
+    }
+  };
+
+  Cursor now{at.split * A.chunk + wave * kStepKeys, 0}, next = now;
+  advance(&next);
+  int32_t next_page = -1;
+  Rows r{};
+  if (now.key < keys) {
+    const int32_t page = page_at(now.key);
+    next_page = page_at(next.key);
+    r = rows_at(now.key, page);
+    load_k(r);
+    load_v(r);
+  }
+  while (now.key < keys) {
+    Cursor after = next;
+    advance(&after);
+    const int32_t after_page = page_at(after.key);
+    const Rows rn = rows_at(next.key, next_page);
+
+    af4 s[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      s[h] = af4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < S::kSteps; ++i) {
+        if constexpr (FMT == kCacheSame) s[h] = mfma16<T>(kr[h][i], q[i], s[h]);
+        else
+          s[h] = mfma16<T>(codes_to<T, FMT>(kr[h][i / 2][2 * (i & 1)], kr[h][i / 2][2 * (i & 1) + 1]), q[i], s[h]);
+      }
+    }
+    if (next.key < keys) load_k(rn);
+
+    // scores in powers of two, and what is hidden
+    float x[8], ws[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[4 * h + i] = s[h][i] * A.scale;
+        if constexpr (FMT != kCacheSame) {
+          const int src = static_cast<int>((16u * h + 4u * quarter + i) * 4u);
+          x[4 * h + i] *= as_float(static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(src, static_cast<int>(as_bits(r.ks)))));
+          ws[4 * h + i] = as_float(static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(src, static_cast<int>(as_bits(r.vs)))));
+        }
+      }
+    if (r.here != 0xFFFFFFFFu || static_cast<int32_t>(now.key + kStepKeys - 1u) > t.low) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t j = 16u * (k / 4) + 4u * quarter + (k & 3);
+        if (static_cast<int32_t>(now.key + j) > sees || !(r.here >> j & 1u)) x[k] = -__builtin_inff();
+      }
+    }
+    // The running maximum is taken up only when it grows by 2^8 or more: weights
+    // of up to 256 lose nothing, and most steps need no rescaling.
+    float top = x[0];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) top = __builtin_fmaxf(top, x[k]);
+    top = max_step<5>(max_step<4>(top));
+    if (__builtin_amdgcn_ballot_w64(top > m + 8.0f)) {
+      const float to = __builtin_fmaxf(m, top);
+      const float shrink = exp2_of(m - (to == -__builtin_inff() ? 0.0f : to));
+      m = to;
+      l *= shrink;
+#pragma unroll
+      for (int d = 0; d < DP / 16; ++d) o[d] *= shrink;
+    }
+    const float base = m == -__builtin_inff() ? 0.0f : m;
+    float p[8], sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      p[k] = exp2_of(x[k] - base);
+      sum += p[k];
+    }
+    l += sum;
+    if constexpr (FMT != kCacheSame) {
+      // the values' scales go into the weights; float16 holds them in units of a
+      // power of two that is at least the largest scale so far
+      float unit = 1.0f;
+      if constexpr (std::is_same_v<T, _Float16>) {
+        float big = ws[0];
+#pragma unroll
+        for (int k = 1; k < 8; ++k) big = __builtin_fmaxf(big, ws[k]);
+        big = max_step<5>(max_step<4>(big));
+        const int e = static_cast<int>(as_bits(big) >> 23) - 126;  // big < 2^e
+        const int up = __builtin_amdgcn_readfirstlane(e > v_exp ? e : v_exp);
+        if (up > v_exp) {
+          const float down = v_exp - up < -126 ? 0.0f : as_float(static_cast<uint32_t>(127 + v_exp - up) << 23);
+#pragma unroll
+          for (int d = 0; d < DP / 16; ++d) o[d] *= down;
+          v_exp = up;
+        }
+        unit = __builtin_amdgcn_ldexpf(1.0f, -v_exp);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) p[k] = p[k] > 0.0f ? p[k] * (ws[k] * unit) : 0.0f;
+    }
+    const rw4 weights = narrow(p, static_cast<const T*>(nullptr));
+
+    // V: rows of channels to columns of keys
+    {
+      const uint32_t piece = lane % S::kPieces, first = lane / S::kPieces;
+#pragma unroll
+      for (int i = 0; i < S::kVRegs; ++i)
+        *reinterpret_cast<rw4*>(mine + v_at<S, FMT>(first + i * S::kVRows, piece)) = vr[i];
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (next.key < keys) load_v(rn);
+#pragma unroll
+    for (int d = 0; d < DP / 16; ++d) {
+      rw4 a;
+      if constexpr (FMT == kCacheSame) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t k = 16u * h + 4u * quarter + col / 4u;
+          const uint32_t piece = 2u * d + (col & 3u) / 2u;
+          const as4 w = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (ACP_LDS as4*)(mine + v_at<S, FMT>(k, piece) + (col & 1u) * 8u));
+          const rw2 u = __builtin_bit_cast(rw2, w);
+          a[2 * h] = u[0];
+          a[2 * h + 1] = u[1];
+        }
+      } else {
+        const uint32_t j = col / 2u;
+        const uint32_t k = 16u * (j / 4u) + 4u * quarter + (j & 3u);
+        const ai2 w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((ACP_LDS ai2*)(mine + v_at<S, FMT>(k, d) + (col & 1u) * 8u));
+        a = codes_to<T, FMT>(static_cast<uint32_t>(w[0]), static_cast<uint32_t>(w[1]));
+      }
+      o[d] = mfma16<T>(a, weights, o[d]);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    now = next;
+    next = after;
+    next_page = after_page;
+    r = rn;
+  }
+  if constexpr (FMT != kCacheSame && std::is_same_v<T, _Float16>) {
+    const float unit = __builtin_amdgcn_ldexpf(1.0f, v_exp);
+#pragma unroll
+    for (int d = 0; d < DP / 16; ++d) o[d] *= unit;
+  }
+  l = sum_step<5>(sum_step<4>(l));
+
+  // The waves' sums: row col, channel 16 d + 4 quarter + i in o[d][i]
+  if (quarter == 0) {
+    join_stat[wave][col][0] = m;
+    join_stat[wave][col][1] = l;
+  }
+  if (threadIdx.x == 0) odd_rows = 0;
+  const uint32_t jr = threadIdx.x / 16u, jc = threadIdx.x % 16u * 8u;  // row and channels that a lane joins
+  constexpr int kParts = (DP + 127) / 128, kWide = DP < 128 ? DP : 128;
+  float sums[kParts][8], total = 0.0f, best = -__builtin_inff(), w[4];
+  float* stage = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int h = 0; h < kParts; ++h) {
+    __syncthreads();
+#pragma unroll
+    for (int d = 0; d < kWide / 16; ++d)
+      *reinterpret_cast<af4*>(stage + (wave * kStepRows + col) * S::kJoinPitch + 16 * d + 4 * quarter) = o[8 * h + d];
+    __syncthreads();
+    if (h == 0) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) best = __builtin_fmaxf(best, join_stat[k][jr][0]);
+      const float base = best == -__builtin_inff() ? 0.0f : best;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        w[k] = exp2_of(join_stat[k][jr][0] - base);
+        total = __builtin_fmaf(w[k], join_stat[k][jr][1], total);
+      }
+    }
+    if (jc < kWide) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sums[h][i] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          sums[h][i] = __builtin_fmaf(w[k], stage[(k * kStepRows + jr) * S::kJoinPitch + jc + i], sums[h][i]);
+      }
+    }
+  }
+  const uint32_t my_row = t.first + jr;
+  const bool row_real = my_row < static_cast<uint32_t>(t.rows);
+  if (row_real && t.low + 1 < t.keys) {  // rows that see less than others
+    bool fine = is_finite(total);
+    if (jc < kWide) {
+#pragma unroll
+      for (int h = 0; h < kParts; ++h)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) fine = fine && is_finite(sums[h][i]);
+    }
+    if (!fine && t.position(A, my_row) + 1 < t.keys) atomicOr(&odd_rows, 1u << jr);
+  }
+  __syncthreads();
+  const uint32_t odd = odd_rows;
+  if (row_real && jc < kWide && !(odd >> jr & 1u)) {
+    uint32_t token, head;
+    t.place(A, my_row, at.kv, &token, &head);
+    if (splits == 1u) {
+      char* y = head_row(A, A.out, token, head);
+      const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+#pragma unroll
+      for (int h = 0; h < kParts; ++h) {
+        const uint32_t c = 128u * h + jc;
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = total == 0.0f ? 0.0f : sums[h][i] * inv;
+        if (c < A.dim) *reinterpret_cast<rw4_any*>(y + c * 2) = narrow(f, static_cast<const T*>(nullptr));
+      }
+    } else {
+      const uint64_t r0 = (static_cast<uint64_t>(at.split) * A.tokens + token) * A.heads.d + head;
+#pragma unroll
+      for (int h = 0; h < kParts; ++h) {
+        const uint32_t c = 128u * h + jc;
+        if (c < A.dim) {
+          float* y = A.part + r0 * A.dim + c;
+          *reinterpret_cast<af4*>(y) = af4{sums[h][0], sums[h][1], sums[h][2], sums[h][3]};
+          *reinterpret_cast<af4*>(y + 4) = af4{sums[h][4], sums[h][5], sums[h][6], sums[h][7]};
+        }
+      }
+      if (jc == 0) {
+        A.stat[2 * r0] = best;
+        A.stat[2 * r0 + 1] = total;
+      }
+    }
+  }
+  for (uint32_t k = wave; k < kStepRows; k += 4u)
+    if (odd >> k & 1u) row_by_keys<T, FMT, DP>(A, t, t.first + k, at.kv, at.split, splits);
+}
+
+template <class T>
+hipError_t attend_step_for(int cache, int padded, const AttendArgs& a, hipStream_t s) {
+  const void* f = nullptr;
+#define ACP_STEP(FMT, DP) \
+  if (cache == FMT && padded == DP) f = reinterpret_cast<const void*>(attend_step_kernel<T, FMT, DP>)
+  ACP_STEP(kCacheSame, 64);
+  ACP_STEP(kCacheSame, 128);
+  ACP_STEP(kCacheSame, 256);
+  ACP_STEP(kCacheI8, 64);
+  ACP_STEP(kCacheI8, 128);
+  ACP_STEP(kCacheI8, 256);
+  ACP_STEP(kCacheE4M3, 64);
+  ACP_STEP(kCacheE4M3, 128);
+  ACP_STEP(kCacheE4M3, 256);
+#undef ACP_STEP
+  if (f == nullptr) return hipErrorInvalidValue;
+  AttendArgs copy = a;
+  void* args[] = {&copy};
+  return hipLaunchKernel(f, dim3(a.kv_heads.d * a.slots.d * a.splits), dim3(kAttendThreads), args, 0, s);
+}
+
+}  // namespace dev
+}  // namespace acp

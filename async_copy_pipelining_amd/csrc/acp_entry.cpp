@@ -4,3 +4,4 @@
 #include "acp_api.cpp"
 #include "acp_rows_api.hpp"
 #include "acp_heads_api.hpp"
+#include "acp_attn_api.hpp"

@@ -1,0 +1,10 @@
+// Attention of few rows over caches that are read as bf16.
+#include "acp_dev_attn_step.hpp"
+
+namespace acp {
+
+hipError_t attend_step_bf16(int cache, int padded, const AttendArgs& a, hipStream_t s) {
+  return dev::attend_step_for<dev::bf16_t>(cache, padded, a, s);
+}
+
+}  // namespace acp

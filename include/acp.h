@@ -21,6 +21,7 @@
  *   acp_rotate                               rotary positions, and their backward pass
  *   acp_head_norm, acp_head_norm_backward    norms of queries and keys, with the rotation
  *   acp_cache_append                         new keys and values into a paged cache
+ *   acp_cache_attention                      attention of new tokens over a paged cache
  *
  * plus the host-side descriptor encoder / planner they share.  The method
  * follows four pages:
@@ -577,6 +578,31 @@ typedef struct {
 acp_status acp_cache_append(const acp_paged_cache* cache, const acp_tile_desc* k, const acp_tile_desc* v,
                             const acp_sequences* sequences, const acp_rotary* rotary, const acp_tile_desc* yq,
                             const acp_tile_desc* q, void* hip_stream);
+
+/* Attention of new tokens over a paged cache that holds them already:
+ *   out = sum_j P_j v_j,  P = softmax over j of scale * (q . k_j)
+ * over the positions j up to the token's own that have a page; query head h
+ * reads the cache's head h / (heads / kv heads).  One call takes single tokens,
+ * chunks behind a cached context and whole prompts, of sequences that differ.
+ *   out, q     [tokens, heads, channels] of f16 or bf16, up to 256 channels in
+ *              multiples of 8 (ACP_ERR_UNSUPPORTED else)
+ *   cache      of q's type, or in 8 bits; kv heads divide q's
+ *   scale      finite, of the scores: 1 / sqrt(channels) mostly
+ * Scores and sums are held in float32; the weights are rounded to the tensors'
+ * type before they meet the values, which changes an output by half a step of
+ * that type as its own rounding does.  A token that sees no position gives
+ * zero, scores of -infinity weigh nothing, and what no token may see (positions
+ * behind it, pages past the length) changes nothing, whatever it holds.  Tokens
+ * of no sequence leave out as it was.
+ * acp_cache_attention_workspace gives the bytes of workspace that the call
+ * needs at most (may be 0): partial results where few rows are split over a
+ * long context.  It depends on the shapes, on sequences, max_pages and
+ * max_length, and on no device memory. */
+acp_status acp_cache_attention_workspace(const acp_tile_desc* q, const acp_paged_cache* cache,
+                                         const acp_sequences* sequences, int64_t* bytes);
+acp_status acp_cache_attention(const acp_tile_desc* out, const acp_tile_desc* q, const acp_paged_cache* cache,
+                               const acp_sequences* sequences, float scale, void* workspace, int64_t workspace_bytes,
+                               void* hip_stream);
 
 /* Test export: the raw LDS bytes of tile `tile_index` of `src` after its
  * direct-to-LDS load, written to `out_bytes` (device, tile_bytes long). */
