@@ -8,9 +8,10 @@
 // the tiles of sequence s begin at floor(starts[s] * group / M) + s, which leaves
 // room for ceil(n * group / M) of them before the next sequence's.
 //
-// Keys are cut into chunks of `chunk`; workgroup `split` of a tile takes the
-// chunks split, split + splits, ...  A tile whose keys fill one chunk writes its
-// output, others leave partial results, which a second kernel joins.
+// A launch has a workgroup for each tile and head, or (`shares` > 0) deals the
+// work out evenly: the keys of all tiles of a head, one after another, are cut
+// into equal shares, whatever the lengths are, and a tile that a cut goes through
+// leaves partial results, which a second kernel joins.
 #pragma once
 
 #include "acp_heads.hpp"
@@ -23,20 +24,33 @@ struct AttendArgs {
   BatchArgs batch;
   Div n2;               // token dims, as HeadsCore has them
   Div group;            // query heads of a cache's head
-  Div kv_heads;
+  Div kv_heads;         // heads of the cache, in groups of 2^side_log2 of them
+  int side_log2;        // heads of a workgroup: 0 for many rows
   Div slots;            // tile slots
-  Div heads;            // query heads
   uint32_t tokens, dim;
-  uint32_t chunk, splits;
-  float scale;          // of a score, times log2 e: exponentials are powers of two
-  float* part;          // [splits][token][head][dim] sums of weighted values
-  float* stat;          // [splits][token][head][2] largest score and sum of weights
+  uint32_t shares;      // of a head's work, at most; 0: a workgroup a tile
+  uint32_t least;       // keys of a share, at least
+  uint32_t once;        // few rows: no two tiles read the same keys, but for some sequences
+  uint32_t direct;      // many rows: the cache's rows are 16-byte aligned 16-bit values
+  float scale;          // of a score, times log2 e: exponentials are powers of two; > 0
+  uint32_t flip;        // the queries' sign bits, where it was below zero
+  // partial results: a workgroup leaves up to two, of its first and its last tile.
+  // [workgroup][2][2^side_log2 * M rows]
+  float* part;          // [...][dim] sums of weighted values
+  float* stat;          // [...][2] largest score and sum of weights
+  uint32_t* joins;      // [slots][kv_heads][2] first share and number of shares of a tile
 };
 
 // dt: kRowF16 or kRowBF16; cache: kCacheSame, kCacheI8 or kCacheE4M3; dim padded to 64, 128 or 256
 hipError_t attend_step_launch(int dt, int cache, int padded, const AttendArgs& a, hipStream_t s);
 hipError_t attend_prompt_launch(int dt, int cache, int padded, const AttendArgs& a, hipStream_t s);
-hipError_t attend_join_launch(int dt, int tile_rows, const AttendArgs& a, hipStream_t s);
+// How a workgroup of the join is laid out: lanes of a row, groups of them that
+// share its splits, workgroups for the rows of a tile.
+struct JoinShape {
+  int lanes_log2, shares_log2;
+  Div blocks;
+};
+hipError_t attend_join_launch(int dt, int tile_rows, const AttendArgs& a, const JoinShape& k, hipStream_t s);
 
 hipError_t attend_step_f16(int cache, int padded, const AttendArgs& a, hipStream_t s);
 hipError_t attend_step_bf16(int cache, int padded, const AttendArgs& a, hipStream_t s);
@@ -47,6 +61,6 @@ constexpr int kAttendThreads = 256;
 constexpr int kStepRows = 16;      // rows of a tile of few rows
 constexpr int kPromptRows = 128;   // rows of a tile of many
 constexpr int kStepKeys = 32;      // keys that a wave takes at a time
-constexpr uint32_t kChunkUnit = 128;  // chunks are whole multiples: the keys of a step's four waves, tiles of a prompt
+constexpr uint32_t kCutStep = 4 * kStepKeys, kCutPrompt = 64;  // cuts lie at multiples
 
 }  // namespace acp

@@ -1,22 +1,33 @@
 // Entry points of attention over a paged cache.  Included by acp_entry.cpp
 // after acp_heads_api.hpp, whose helpers it uses.
+#include <limits>
+
 #include "acp_attn.hpp"
 
 namespace {
 
-// Workgroups that a launch aims at where its keys can be split: four for each
-// of 256 CUs.
-constexpr int64_t kAttendGroups = 1024;
-// Keys of a chunk are worth a workgroup of their own from here on.
+// Workgroups that the device has room for at a time, by the padded channels: two
+// a CU, one of 256 channels.
+constexpr int64_t kAttendGroups = 512;
+constexpr int64_t kAttendGroupsWide = 256;
+// From so many times as many tiles on each is a workgroup's; fewer are dealt out
+// evenly.
+constexpr int64_t kAttendTiles = 1;
+// Keys of a share, at least.
 constexpr int64_t kAttendLeast = 256;
+// Sequences of at most so many positions are a workgroup's each, however few.
+constexpr int64_t kAttendAlone = 1024;
+// Neighbouring heads in a workgroup, at most 2^k of them.
+constexpr int64_t kAttendSide = 2;
 // Rows of a sequence, on average, from which on tiles of 128 rows are taken.
-constexpr int64_t kAttendPrompt = 64;
+constexpr int64_t kAttendPrompt = 32;
 
 struct AttendPlan {
   acp::AttendArgs A{};
+  acp::JoinShape join{};
   int tile_rows = 0, padded = 0, cache = 0, dt = 0;
   int64_t workspace = 0, tokens = 0;
-  int64_t stat_at = 0;
+  int64_t stat_at = 0, joins_at = 0;
 };
 
 // Everything but addresses: shapes, the form, the split of the keys.
@@ -42,8 +53,6 @@ acp_status attend_plan(const acp::DescData& q, const CacheSide& k, const acp_seq
   A.dim = static_cast<uint32_t>(dim);
   const int64_t group = std::max<int64_t>(1, heads / kv), sequences = b->sequences;
   A.group = div_by(static_cast<uint64_t>(group));
-  A.kv_heads = div_by(static_cast<uint64_t>(kv));
-  A.heads = div_by(static_cast<uint64_t>(std::max<int64_t>(1, heads)));
   if (P->tokens == 0 || heads == 0 || sequences == 0) return ACP_OK;
   // rows of a sequence: its tokens' query heads of one of the cache's
   const int64_t rows = b->starts ? P->tokens * group : sequences * group;
@@ -55,20 +64,39 @@ acp_status attend_plan(const acp::DescData& q, const CacheSide& k, const acp_seq
   // the longest that a sequence can be
   int64_t longest = std::min<int64_t>(int64_t(b->max_pages) * k.d.shape[1], (int64_t(1) << 31) - 1);
   if (b->max_length) longest = std::min<int64_t>(longest, b->max_length);
-  longest = std::max<int64_t>(1, longest);
+  const int64_t groups = P->padded == 256 ? kAttendGroupsWide : kAttendGroups;
   // sequences mostly fill fewer tiles than their slots
-  const int64_t tiles = kv * std::max<int64_t>(sequences, b->starts ? P->tokens * group / M : slots);
-  const int64_t wanted = std::max<int64_t>(1, kAttendGroups / tiles);
-  int64_t chunk = std::max(ceil_div(longest, wanted), std::min(longest, kAttendLeast));
-  chunk = ceil_div(chunk, acp::kChunkUnit) * acp::kChunkUnit;
-  const int64_t splits = ceil_div(longest, chunk);
-  A.chunk = static_cast<uint32_t>(chunk);
-  A.splits = static_cast<uint32_t>(splits);
-  // a launch has fewer than 2^32 lanes
-  if (kv * slots >= int64_t(1) << 24 || kv * slots * splits >= int64_t(1) << 24 || P->tokens * heads >= int64_t(1) << 26)
-    return ret(ACP_ERR_UNSUPPORTED, "a launch of 2^32 lanes");
-  P->stat_at = align_up(splits * P->tokens * heads * dim * 4, 16);
-  if (splits > 1) P->workspace = P->stat_at + splits * P->tokens * heads * 8;
+  const int64_t tiles = std::max<int64_t>(sequences, b->starts ? P->tokens * group / M : slots);
+  // few rows: neighbouring heads, whose rows lie side by side, in the waves of a
+  // workgroup, as long as all workgroups have work
+  while (M == acp::kStepRows && A.side_log2 < kAttendSide && kv % (int64_t(2) << A.side_log2) == 0 &&
+         (kv >> (A.side_log2 + 1)) * tiles * ceil_div(longest, kAttendLeast) >= groups)
+    ++A.side_log2;
+  const int64_t heads_each = kv >> A.side_log2;
+  A.once = rows <= M * sequences;
+  A.kv_heads = div_by(static_cast<uint64_t>(heads_each));
+  int64_t grid = heads_each * slots;
+  if (heads_each * tiles < kAttendTiles * groups && longest > kAttendAlone) {
+    const int64_t most = std::max<int64_t>(1, groups / heads_each);
+    A.shares = static_cast<uint32_t>(std::min(most, slots * ceil_div(longest + 1, kAttendLeast)));
+    A.least = static_cast<uint32_t>(kAttendLeast);
+    grid = heads_each * A.shares;
+    const int64_t rows = grid * 2 * (M << A.side_log2);
+    P->stat_at = rows * dim * 4;
+    P->joins_at = P->stat_at + rows * 8;
+    P->workspace = P->joins_at + heads_each * slots * 8;
+    // the join: at most four partial results in a row for a lane, as long as lanes last
+    const int64_t used = A.side_log2 || b->starts ? M << A.side_log2 : std::min(M, group);
+    int lanes = 4, shares = 0;
+    while ((int64_t(4) << lanes) < dim) ++lanes;
+    while (lanes + shares < 8 && (int64_t(4) << shares) < ceil_div(A.shares, tiles) + 1) ++shares;
+    P->join.lanes_log2 = lanes;
+    P->join.shares_log2 = shares;
+    const int64_t blocks = ceil_div(used, acp::kAttendThreads >> (lanes + shares));
+    P->join.blocks = div_by(static_cast<uint64_t>(blocks));
+    grid = std::max(grid, heads_each * slots * blocks);
+  }
+  if (grid >= int64_t(1) << 24) return ret(ACP_ERR_UNSUPPORTED, "a launch of 2^32 lanes");
   return ACP_OK;
 }
 
@@ -127,18 +155,28 @@ acp_status cache_attention(const acp_tile_desc* out, const acp_tile_desc* q, con
   if ((st = check_stream(stream)) != ACP_OK) return st;
   set_cache(k, &A.k);
   set_cache(v, &A.v);
-  A.scale = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  // a scale of zero becomes the least: a weight of what is hidden stays zero
+  auto aligned16 = [](const CacheSide& c) {
+    bool all = c.d.gbase % 16 == 0;
+    for (int d = 0; d < 3; ++d) all = all && (c.d.shape[d] == 1 || c.d.strides[d] * c.d.esize % 16 == 0);
+    return all;
+  };
+  A.direct = k.kind == acp::kCacheSame && aligned16(k) && aligned16(v);
+  A.scale = std::max(static_cast<float>(std::fabs(static_cast<double>(scale)) * 1.4426950408889634),
+                     std::numeric_limits<float>::min());
+  A.flip = scale < 0.0f ? 0x80008000u : 0u;
   A.part = static_cast<float*>(workspace);
   A.stat = reinterpret_cast<float*>(static_cast<char*>(workspace) + P.stat_at);
+  A.joins = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + P.joins_at);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const bool few = P.tile_rows == acp::kStepRows;
   hipError_t e = few ? acp::attend_step_launch(P.dt, P.cache, P.padded, A, s)
                      : acp::attend_prompt_launch(P.dt, P.cache, P.padded, A, s);
-  if (e == hipSuccess && A.splits > 1) e = acp::attend_join_launch(P.dt, P.tile_rows, A, s);
+  if (e == hipSuccess && A.shares > 0) e = acp::attend_join_launch(P.dt, P.tile_rows, A, P.join, s);
   return launched(e, std::string("cache attention ") + (few ? "few rows" : "many rows") +
                          (k.kind == acp::kCacheSame ? "" : " 8 bits") + " channels " + std::to_string(P.padded) + " slots " +
-                         std::to_string(A.slots.d) + " splits " + std::to_string(A.splits) + " chunk " +
-                         std::to_string(A.chunk));
+                         std::to_string(A.slots.d) + " heads " + std::to_string(1 << A.side_log2) + " shares " +
+                         std::to_string(A.shares));
 }
 
 }  // namespace

@@ -17,10 +17,11 @@ namespace dev {
 
 template <int FMT, int DP>
 struct PromptShape {
-  static constexpr int kKeys = DP <= 128 ? 64 : 32;   // of a tile: 64 KiB of LDS, two workgroups a CU
+  static constexpr int kKeys = 64;                    // of a tile, in two blocks of 32
   static constexpr int kRow = DP * 2;
   static constexpr int kPieces = kRow / 16;
   static constexpr int kTile = kKeys * kRow;          // bytes of K or V
+  using Piece = std::conditional_t<FMT == kCacheSame, rw4, rw2>;  // 8 channels
   static constexpr int kRegs = kTile / 16 / kAttendThreads;
   static constexpr int kStride = kAttendThreads / kPieces;  // rows between a lane's pieces
 };
@@ -39,286 +40,29 @@ __device__ __forceinline__ uint32_t v_at(uint32_t row, uint32_t piece) {
   return row * (DP * 2u) + (piece ^ (((row / kRows) & 3u & (kUnits - 1u)) << 2)) * 16u;
 }
 
+// The wave's rows: row col, channel 32 d + 8 (i / 4) + 4 half + i % 4 in o[d][i].
 template <class T, int FMT, int DP>
-__global__ __launch_bounds__(kAttendThreads, DP == 256 ? 1 : 2) void attend_prompt_kernel(const AttendArgs A) {
-  using S = PromptShape<FMT, DP>;
-  constexpr int NB = S::kKeys / 32;  // blocks of 32 keys
-  __shared__ __attribute__((aligned(16))) char lds[2][2][S::kTile];
-  __shared__ __attribute__((aligned(16))) float scales[2][2][S::kKeys];
-  const AttendPlace at(A);
-  Tile t;
-  if (!t.find<kPromptRows>(A, at.slot)) return;
-  const uint32_t splits = t.splits(A);
-  if (at.split >= splits) return;
-  const uint32_t lane = threadIdx.x & 63u, wave = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
+__device__ __forceinline__ void prompt_rows(const AttendArgs& A, const Tile& t, const Partial& to, uint32_t begin,
+                                            uint32_t keys, uint32_t kv, const af16 (&o)[DP / 32], float m, float l) {
+  const uint32_t thread = thread_again();
+  const uint32_t lane = thread & 63u, wave = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(thread >> 6));
   const uint32_t col = lane & 31u, half = lane >> 5;
-  const uint32_t keys = static_cast<uint32_t>(t.keys);
-
-  const uint32_t row = t.first + wave * 32u + col;
+  const uint32_t row0 = t.first + wave * 32u, row = row0 + col;
   const bool real = row < static_cast<uint32_t>(t.rows);
-  const int32_t sees = real ? t.position(A, row) : -1;
   uint32_t token, head;
-  t.place(A, real ? row : t.first, at.kv, &token, &head);
-  // positions of the wave's first and last rows
-  const uint32_t row0 = t.first + wave * 32u;
-  const bool any = row0 < static_cast<uint32_t>(t.rows);
-  const int32_t low = any ? t.position(A, row0) : -1;
-  const uint32_t row9 = row0 + 31u < static_cast<uint32_t>(t.rows) ? row0 + 31u : static_cast<uint32_t>(t.rows) - 1u;
-  const int32_t high = any ? t.position(A, row9) : -1;
-
-  rw4 q[DP / 16];
-  {
-    const char* qr = head_row(A, A.q, token, head);
-#pragma unroll
-    for (int s = 0; s < DP / 16; ++s) {
-      const uint32_t c = 16u * s + 8u * half;
-      q[s] = rw4{0u, 0u, 0u, 0u};
-      if (real && c < A.dim) q[s] = *reinterpret_cast<const rw4_any*>(qr + c * 2);
-    }
-  }
-  af16 o[DP / 32];
-#pragma unroll
-  for (int d = 0; d < DP / 32; ++d)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
-  float m = -__builtin_inff(), l = 0.0f;
-  int v_exp = -200;  // as in the form for few rows
-
-  // The lane's pieces of a tile: piece `piece` of rows first, first + kStride, ...
-  const uint32_t piece = threadIdx.x % S::kPieces, first = threadIdx.x / S::kPieces;
-  const char* kbase = A.k.p + at.kv * A.k.s[2] + piece * (FMT == kCacheSame ? 16u : 8u);
-  const char* vbase = A.v.p + at.kv * A.v.s[2] + piece * (FMT == kCacheSame ? 16u : 8u);
-  const bool holds = piece * 8u < A.dim;
-  rw4 kr[S::kRegs], vr[S::kRegs];
-  // Each wave finds the pages of all the tile's keys: lane j has key j
-  auto page_at = [&](uint32_t key0) -> int32_t {
-    const uint32_t key = key0 + (lane & (S::kKeys - 1u));
-    uint32_t index;
-    return key < keys ? key_page(A, t.seq, key, &index) : -1;
-  };
-  float ks = 0.0f, vs = 0.0f;  // of the lane's key in the tile that is loading
-  auto load = [&](uint32_t key0, int32_t page) {
-    const uint64_t here = __builtin_amdgcn_ballot_w64(page >= 0);
-    if constexpr (FMT != kCacheSame) {
-      ks = vs = 0.0f;
-      const uint32_t key = key0 + (lane & (S::kKeys - 1u));
-      if (page >= 0) {
-        const uint32_t index = key - divide(key, A.batch.page) * A.batch.page.d;
-        const uint64_t s = (static_cast<uint64_t>(page) * A.batch.page.d + index) * A.kv_heads.d + at.kv;
-        ks = A.k.scales[s];
-        vs = A.v.scales[s];
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < S::kRegs; ++i) {
-      const uint32_t j = first + i * S::kStride;
-      const uint32_t key = key0 + j;
-      const int64_t g = __builtin_amdgcn_ds_bpermute(static_cast<int>(j * 4u), page);
-      const uint32_t index = key - divide(key, A.batch.page) * A.batch.page.d;
-      const char* kp = kbase + g * A.k.s[0] + index * A.k.s[1];
-      const char* vp = vbase + g * A.v.s[0] + index * A.v.s[1];
-      kr[i] = vr[i] = rw4{0u, 0u, 0u, 0u};
-      if (holds && (here >> j & 1u)) {
-        if constexpr (FMT == kCacheSame) {
-          kr[i] = *reinterpret_cast<const rw4_any*>(kp);
-          vr[i] = *reinterpret_cast<const rw4_any*>(vp);
-        } else {
-          const rw2 a = *reinterpret_cast<const rw2_any*>(kp), b = *reinterpret_cast<const rw2_any*>(vp);
-          kr[i] = rw4{a[0], a[1], 0u, 0u};
-          vr[i] = rw4{b[0], b[1], 0u, 0u};
-        }
-      }
-    }
-    return here;
-  };
-  auto put = [&](int b) {
-#pragma unroll
-    for (int i = 0; i < S::kRegs; ++i) {
-      const uint32_t j = first + i * S::kStride;
-      if constexpr (FMT == kCacheSame) {
-        *reinterpret_cast<rw4*>(lds[b][0] + k_at<DP>(j, piece)) = kr[i];
-        *reinterpret_cast<rw4*>(lds[b][1] + v_at<DP>(j, piece)) = vr[i];
-      } else {
-        *reinterpret_cast<rw4*>(lds[b][0] + k_at<DP>(j, piece)) = codes_to<T, FMT>(kr[i][0], kr[i][1]);
-        *reinterpret_cast<rw4*>(lds[b][1] + v_at<DP>(j, piece)) = codes_to<T, FMT>(vr[i][0], vr[i][1]);
-      }
-    }
-    if constexpr (FMT != kCacheSame) {
-      if (threadIdx.x < S::kKeys) {
-        scales[b][0][threadIdx.x] = ks;
-        scales[b][1][threadIdx.x] = vs;
-      }
-    }
-  };
-
-  const uint32_t per = A.chunk / S::kKeys;
-  uint32_t now = at.split * A.chunk, n = 0;
-  auto after = [&](uint32_t key, uint32_t* k) {
-    key += S::kKeys;
-    if (++*k == per) {
-      *k = 0;
-      key += (A.splits - 1u) * A.chunk;
-    }
-    return key;
-  };
-  uint64_t here = 0;
-  uint32_t next = after(now, &n);
-  int32_t next_page = -1;
-  if (now < keys) {
-    const int32_t page = page_at(now);
-    next_page = page_at(next);
-    here = load(now, page);
-    put(0);
-  }
-  __syncthreads();
-  int b = 0;
-  while (now < keys) {
-    uint32_t n2 = n;
-    const uint32_t then = after(next, &n2);
-    uint64_t next_here = 0;
-    const bool more = next < keys;
-    if (more) next_here = load(next, next_page);
-    next_page = page_at(then);
-
-    if (static_cast<int32_t>(now) <= high) {
-      const char* kt = lds[b][0];
-      const char* vt = lds[b][1];
-      af16 s[NB];
-#pragma unroll
-      for (int h = 0; h < NB; ++h) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[h][i] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < DP / 16; ++i) {
-          const rw4 a = *reinterpret_cast<const rw4*>(kt + k_at<DP>(32u * h + col, 2u * i + half));
-          s[h] = mfma32<T>(a, q[i], s[h]);
-        }
-      }
-      // key of s[h][i]: 32 h + 8 (i / 4) + 4 half + i % 4
-      float top = -__builtin_inff();
-#pragma unroll
-      for (int h = 0; h < NB; ++h)
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[h][i + e] *= A.scale;
-          if constexpr (FMT != kCacheSame) {
-            const af4 w = *reinterpret_cast<const af4*>(&scales[b][0][32 * h + 2 * i + 4 * half]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[h][i + e] *= w[e];
-          }
-        }
-      constexpr uint64_t kAll = S::kKeys == 64 ? ~uint64_t(0) : (uint64_t(1) << (S::kKeys & 63)) - 1;
-      if ((here & kAll) != kAll || static_cast<int32_t>(now + S::kKeys - 1u) > low) {
-#pragma unroll
-        for (int h = 0; h < NB; ++h)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint32_t j = 32u * h + 8u * (i / 4) + 4u * half + (i & 3);
-            if (static_cast<int32_t>(now + j) > sees || !(here >> j & 1u)) s[h][i] = -__builtin_inff();
-          }
-      }
-#pragma unroll
-      for (int h = 0; h < NB; ++h)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, s[h][i]);
-      top = max_step<5>(top);
-      // taken up only when it grows by 2^8 or more, as in the form for few rows
-      if (__builtin_amdgcn_ballot_w64(top > m + 8.0f)) {
-        const float to = __builtin_fmaxf(m, top);
-        const float shrink = exp2_of(m - (to == -__builtin_inff() ? 0.0f : to));
-        m = to;
-        l *= shrink;
-#pragma unroll
-        for (int d = 0; d < DP / 32; ++d) o[d] *= shrink;
-      }
-      const float base = m == -__builtin_inff() ? 0.0f : m;
-      float unit = 1.0f;
-      if constexpr (FMT != kCacheSame && std::is_same_v<T, _Float16>) {
-        float big = scales[b][1][lane & (S::kKeys - 1)];
-        const uint32_t most = static_cast<uint32_t>(
-            over_lanes(static_cast<int>(as_bits(__builtin_fmaxf(big, 0.0f))), 6, [](int x, int y) { return x > y ? x : y; }));
-        const int e = static_cast<int>(most >> 23) - 126;  // big < 2^e
-        const int up = __builtin_amdgcn_readfirstlane(e > v_exp ? e : v_exp);
-        if (up > v_exp) {
-          const float down = v_exp - up < -126 ? 0.0f : as_float(static_cast<uint32_t>(127 + v_exp - up) << 23);
-#pragma unroll
-          for (int d = 0; d < DP / 32; ++d) o[d] *= down;
-          v_exp = up;
-        }
-        unit = __builtin_amdgcn_ldexpf(1.0f, -v_exp);
-      }
-      float sum = 0.0f;
-#pragma unroll
-      for (int h = 0; h < NB; ++h) {
-        rw4 weights[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float p[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            p[i] = exp2_of(s[h][8 * k + i] - base);
-            sum += p[i];
-          }
-          if constexpr (FMT != kCacheSame) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const af4 w = *reinterpret_cast<const af4*>(&scales[b][1][32 * h + 16 * k + 8 * e + 4 * half]);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) p[4 * e + i] = p[4 * e + i] > 0.0f ? p[4 * e + i] * (w[i] * unit) : 0.0f;
-            }
-          }
-          weights[k] = narrow(p, static_cast<const T*>(nullptr));
-        }
-        // group g of 16 lanes reads rows 4 (g / 2) .. and channels 16 (g % 2) ..
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int d = 0; d < DP / 32; ++d) {
-            rw4 a;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t r = 32u * h + 16u * k + 8u * e + 4u * half + (lane & 15u) / 4u;
-              const uint32_t c = 4u * d + 2u * (lane >> 4 & 1u) + (lane & 3u) / 2u;
-              const as4 w = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ACP_LDS as4*)(vt + v_at<DP>(r, c) + (lane & 1u) * 8u));
-              const rw2 u = __builtin_bit_cast(rw2, w);
-              a[2 * e] = u[0];
-              a[2 * e + 1] = u[1];
-            }
-            o[d] = mfma32<T>(a, weights[k], o[d]);
-          }
-      }
-      l += sum;
-    }
-    if (more) put(b ^ 1);
-    __syncthreads();
-    b ^= 1;
-    here = next_here;
-    now = next;
-    next = then;
-    n = n2;
-  }
-  if constexpr (FMT != kCacheSame && std::is_same_v<T, _Float16>) {
-    const float unit = __builtin_amdgcn_ldexpf(1.0f, v_exp);
-#pragma unroll
-    for (int d = 0; d < DP / 32; ++d) o[d] *= unit;
-  }
-  l = sum_step<5>(l);
-  if (!any) return;
-
-  // row col, channel 32 d + 8 (i / 4) + 4 half + i % 4 in o[d][i]
+  t.place(A, real ? row : t.first, kv, &token, &head);
   uint64_t odd = 0;
-  if (low + 1 < t.keys) {
+  if (t.low + 1 < t.keys) {
     bool fine = is_finite(l);
 #pragma unroll
     for (int d = 0; d < DP / 32; ++d)
 #pragma unroll
       for (int i = 0; i < 16; ++i) fine = fine && is_finite(o[d][i]);
-    odd = __builtin_amdgcn_ballot_w64(!fine && real && sees + 1 < t.keys);
+    odd = __builtin_amdgcn_ballot_w64(!fine && real && t.position(A, row) + 1 < t.keys);
     odd = (odd | odd >> 32) & 0xFFFFFFFFu;
   }
   if (real && !(odd >> col & 1u)) {
-    if (splits == 1u) {
+    if (!to.wanted) {
       char* y = head_row(A, A.out, token, head);
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
@@ -334,30 +78,371 @@ __global__ __launch_bounds__(kAttendThreads, DP == 256 ? 1 : 2) void attend_prom
           if (c + 8u < A.dim) *reinterpret_cast<rw2_any*>(y + (c + 8u) * 2) = rw2{w[2], w[3]};
         }
     } else {
-      const uint64_t r0 = (static_cast<uint64_t>(at.split) * A.tokens + token) * A.heads.d + head;
+      float* y = to.part(A, wave * 32u + col);
 #pragma unroll
       for (int d = 0; d < DP / 32; ++d)
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
           const uint32_t c = 32u * d + 2u * i + 4u * half;
-          if (c < A.dim)
-            *reinterpret_cast<af4*>(A.part + r0 * A.dim + c) = af4{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
+          if (c < A.dim) *reinterpret_cast<af4*>(y + c) = af4{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
         }
       if (half == 0) {
-        A.stat[2 * r0] = m;
-        A.stat[2 * r0 + 1] = l;
+        float* z = to.stat(A, wave * 32u + col);
+        z[0] = m;
+        z[1] = l;
       }
     }
   }
   for (uint32_t k = 0; k < 32u; ++k)
-    if (odd >> k & 1u) row_by_keys<T, FMT, DP>(A, t, row0 + k, at.kv, at.split, splits);
+    if (odd >> k & 1u)
+      row_by_keys<T, FMT, DP>(A, t, row0 + k, kv, begin, keys, to.part(A, wave * 32u + k), to.stat(A, wave * 32u + k));
+}
+
+// A tile's keys [begin, keys) for one of the cache's heads.
+//
+// DIRECT: 16-bit rows at 16-byte aligned addresses go straight to LDS, in
+// instructions of 64 pieces of 16 bytes that lie one after another there, the
+// pieces' places permuted on the global side.  They take no registers, so that a
+// whole tile is on its way while another is computed.  Pieces past the channels
+// are never written: they were cleared once.  Else (8-bit codes, other
+// alignments) pieces wait in registers.
+template <class T, int FMT, int DP, bool DIRECT>
+__device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, const Partial& to, uint32_t begin,
+                                            uint32_t keys, uint32_t kv, char (*lds)[2][PromptShape<FMT, DP>::kTile],
+                                            float (*scales)[2][PromptShape<FMT, DP>::kKeys]) {
+  using S = PromptShape<FMT, DP>;
+  constexpr uint32_t kBlock = 32u * DP * 2u;  // bytes of a block of 32 keys in LDS
+  const uint32_t thread = thread_again();
+  const uint32_t lane = thread & 63u, wave = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(thread >> 6));
+  const uint32_t col = lane & 31u, half = lane >> 5;
+
+  const uint32_t row = t.first + wave * 32u + col;
+  const bool real = row < static_cast<uint32_t>(t.rows);
+  const int32_t sees = real ? t.position(A, row) : -1;
+  // positions of the wave's first and last rows
+  const uint32_t row0 = t.first + wave * 32u;
+  const bool any = row0 < static_cast<uint32_t>(t.rows);
+  const int32_t low = any ? t.position(A, row0) : -1;
+  const uint32_t row9 = row0 + 31u < static_cast<uint32_t>(t.rows) ? row0 + 31u : static_cast<uint32_t>(t.rows) - 1u;
+  const int32_t high = any ? t.position(A, row9) : -1;
+
+  rw4 q[DP / 16];
+  {
+    uint32_t token, head;
+    t.place(A, real ? row : t.first, kv, &token, &head);
+    const char* qr = head_row(A, A.q, token, head);
+#pragma unroll
+    for (int s = 0; s < DP / 16; ++s) {
+      const uint32_t c = 16u * s + 8u * half;
+      q[s] = rw4{0u, 0u, 0u, 0u};
+      if (real && c < A.dim) q[s] = *reinterpret_cast<const rw4_any*>(qr + c * 2) ^ A.flip;
+    }
+  }
+  af16 o[DP / 32];
+#pragma unroll
+  for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
+  float m = -__builtin_inff(), l = 0.0f;
+  int v_exp = -200;  // as in the form for few rows
+
+  // Each wave finds the pages of all the tile's keys: lane j has key j
+  auto page_at = [&](uint32_t key0) -> int32_t {
+    const uint32_t key = key0 + lane;
+    uint32_t index;
+    return key < keys ? key_page(A, t.seq, key, &index) : -1;
+  };
+  auto row_of = [&](const CacheTensor& c, uint32_t key0, uint32_t j, int32_t page) {
+    const int64_t g = __builtin_amdgcn_ds_bpermute(static_cast<int>(j * 4u), page);
+    const uint32_t key = key0 + j;
+    return c.p + kv * c.s[2] + g * c.s[0] + (key - divide(key, A.batch.page) * A.batch.page.d) * c.s[1];
+  };
+  // DIRECT: piece `slot` of row j in LDS is piece k_slot (v_slot) of the row
+  constexpr uint32_t kRowsEach = 1024u / S::kRow, kEach = S::kTile / 1024u / 4u;  // rows of an instruction; a wave's
+  const uint32_t slot = lane % S::kPieces;
+  auto fetch = [&](uint32_t b, uint32_t key0, int32_t page, uint64_t here) {
+#pragma unroll
+    for (uint32_t i = 0; i < kEach; ++i) {
+      const uint32_t n = i * 4u + wave, j = n * kRowsEach + lane / S::kPieces;
+      const uint32_t kp = (k_at<DP>(j, slot) - j * S::kRow) / 16u, vp = (v_at<DP>(j, slot) - j * S::kRow) / 16u;
+      const char* kr = row_of(A.k, key0, j, page) + kp * 16u;
+      const char* vr = row_of(A.v, key0, j, page) + vp * 16u;
+      const uint32_t kt = lds_offset(lds[b][0]) + n * 1024u, vt = lds_offset(lds[b][1]) + n * 1024u;
+      if (here == ~uint64_t(0) && A.dim == DP) {
+        to_lds(kr, kt);
+        to_lds(vr, vt);
+      } else {
+        if (!(here >> j & 1u)) {
+          *reinterpret_cast<rw4*>(lds[b][0] + n * 1024u + lane * 16u) = rw4{0u, 0u, 0u, 0u};
+          *reinterpret_cast<rw4*>(lds[b][1] + n * 1024u + lane * 16u) = rw4{0u, 0u, 0u, 0u};
+        } else {
+          if (kp * 8u < A.dim) to_lds(kr, kt);
+          if (vp * 8u < A.dim) to_lds(vr, vt);
+        }
+      }
+    }
+  };
+  // else: the lane's pieces of a tile: piece `piece` of rows first, first + kStride, ...
+  const uint32_t piece = thread % S::kPieces, first = thread / S::kPieces;
+  typename S::Piece kw[DIRECT ? 1 : S::kRegs], vw[DIRECT ? 1 : S::kRegs];
+  auto load = [&](uint32_t key0, int32_t page, uint64_t here) {
+    using P = typename S::Piece;
+    typedef P P_any __attribute__((aligned(1)));
+#pragma unroll
+    for (int i = 0; i < S::kRegs; ++i) {
+      const uint32_t j = first + i * S::kStride;
+      const char* kr = row_of(A.k, key0, j, page) + piece * sizeof(P);
+      const char* vr = row_of(A.v, key0, j, page) + piece * sizeof(P);
+      kw[i] = vw[i] = P{};
+      if (piece * 8u < A.dim && (here >> j & 1u)) {
+        kw[i] = *reinterpret_cast<const P_any*>(kr);
+        vw[i] = *reinterpret_cast<const P_any*>(vr);
+      }
+    }
+  };
+  auto value = [](const typename S::Piece& w) {
+    if constexpr (FMT == kCacheSame) return w;
+    else return codes_to<T, FMT>(w[0], w[1]);
+  };
+  auto put = [&](uint32_t b) {
+#pragma unroll
+    for (int i = 0; i < S::kRegs; ++i) {
+      const uint32_t j = first + i * S::kStride;
+      *reinterpret_cast<rw4*>(lds[b][0] + k_at<DP>(j, piece)) = value(kw[i]);
+      *reinterpret_cast<rw4*>(lds[b][1] + v_at<DP>(j, piece)) = value(vw[i]);
+    }
+  };
+  // 8-bit rows: the scales of the tile's keys
+  float ks = 0.0f, vs = 0.0f;
+  auto load_scales = [&](uint32_t key0, int32_t page) {
+    if constexpr (FMT != kCacheSame) {
+      ks = vs = 0.0f;
+      const uint32_t key = key0 + lane;
+      if (page >= 0) {
+        const uint32_t index = key - divide(key, A.batch.page) * A.batch.page.d;
+        const uint64_t s = (static_cast<uint64_t>(page) * A.batch.page.d + index) * A.kv_heads.d + kv;
+        ks = A.k.scales[s];
+        vs = A.v.scales[s];
+      }
+    }
+  };
+  auto put_scales = [&](uint32_t b) {
+    if constexpr (FMT != kCacheSame) {
+      if (thread < S::kKeys) {
+        scales[b][0][thread] = ks;
+        scales[b][1][thread] = vs;
+      }
+    }
+  };
+
+  // Reads: K's piece 2 i + half of row 32 h + col; V's channels 32 d .. of rows
+  // 32 h + 16 k + 8 e + 4 half .., group g of 16 lanes channels 16 (g % 2) of them
+  const uint32_t ka = k_at<DP>(col, half);
+  const uint32_t va = v_at<DP>(4u * half + (lane & 15u) / 4u, 2u * (lane >> 4 & 1u) + (lane & 3u) / 2u) + (lane & 1u) * 8u;
+
+  uint32_t now = begin, b = 0;
+  int32_t page = page_at(now), next_page = page_at(now + S::kKeys);
+  uint64_t here = __builtin_amdgcn_ballot_w64(page >= 0);
+  if constexpr (DIRECT) {
+    if (A.dim != DP) {  // channels that no row has
+#pragma unroll 1
+      for (uint32_t i = thread * 16u; i < 4u * S::kTile; i += kAttendThreads * 16u)
+        *reinterpret_cast<rw4*>(lds[0][0] + i) = rw4{0u, 0u, 0u, 0u};
+      __syncthreads();
+    }
+    if (now < keys) fetch(0, now, page, here);
+  } else {
+    load(now, page, here);
+    load_scales(now, page);
+    put(0);
+    put_scales(0);
+  }
+  while (now < keys) {
+    const uint32_t next = now + S::kKeys;
+    const bool more = next < keys;
+    // this tile has arrived, and all waves are done with the other one
+    if constexpr (DIRECT) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    page = next_page;
+    const uint64_t next_here = __builtin_amdgcn_ballot_w64(page >= 0);
+    if (more) {
+      if constexpr (DIRECT) {
+        fetch(b ^ 1u, next, page, next_here);
+      } else {
+        load(next, page, next_here);
+        load_scales(next, page);
+      }
+    }
+    next_page = page_at(next + S::kKeys);
+
+    if (static_cast<int32_t>(now) <= high) {
+      const char* kt = lds[b][0];
+      const char* vt = lds[b][1];
+      af16 s[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[h][i] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < DP / 16; ++i)
+          s[h] = mfma32<T>(*reinterpret_cast<const rw4*>(kt + h * kBlock + (ka ^ (32u * i))), q[i], s[h]);
+      }
+      // key of s[h][i]: 32 h + 8 (i / 4) + 4 half + i % 4
+      if constexpr (FMT != kCacheSame) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const af4 x = *reinterpret_cast<const af4*>(&scales[b][0][32 * h + 2 * i + 4 * half]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[h][i + e] *= x[e];
+          }
+      }
+      if (here != ~uint64_t(0) || static_cast<int32_t>(now + S::kKeys - 1u) > low) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t j = 32u * h + 8u * (i / 4) + 4u * half + (i & 3);
+            if (static_cast<int32_t>(now + j) > sees || !(here >> j & 1u)) s[h][i] = -__builtin_inff();
+          }
+      }
+      float top = -__builtin_inff();
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, s[h][i]);
+      top = max_step<5>(top) * A.scale;
+      // taken up only when it grows by 2^8 or more, as in the form for few rows
+      if (__builtin_amdgcn_ballot_w64(top > m + 8.0f)) {
+        const float up = __builtin_fmaxf(m, top);
+        const float shrink = exp2_of(m - (up == -__builtin_inff() ? 0.0f : up));
+        m = up;
+        l *= shrink;
+#pragma unroll
+        for (int d = 0; d < DP / 32; ++d) o[d] *= shrink;
+      }
+      const float base = m == -__builtin_inff() ? 0.0f : m;
+      float unit = 1.0f;
+      if constexpr (FMT != kCacheSame && std::is_same_v<T, _Float16>) {
+        const float big = __builtin_fmaxf(scales[b][1][lane], 0.0f);
+        const uint32_t most = static_cast<uint32_t>(
+            over_lanes(static_cast<int>(as_bits(big)), 6, [](int x, int y) { return x > y ? x : y; }));
+        const int e = static_cast<int>(most >> 23) - 126;  // big < 2^e
+        const int up = __builtin_amdgcn_readfirstlane(e > v_exp ? e : v_exp);
+        if (up > v_exp) {
+          const float down = v_exp - up < -126 ? 0.0f : as_float(static_cast<uint32_t>(127 + v_exp - up) << 23);
+#pragma unroll
+          for (int d = 0; d < DP / 32; ++d) o[d] *= down;
+          v_exp = up;
+        }
+        unit = __builtin_amdgcn_ldexpf(1.0f, -v_exp);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        rw4 weights[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float p[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) p[i] = exp2_of(__builtin_fmaf(s[h][8 * k + i], A.scale, -base));
+          if constexpr (FMT != kCacheSame) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) l += p[i];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const af4 x = *reinterpret_cast<const af4*>(&scales[b][1][32 * h + 16 * k + 8 * e + 4 * half]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) p[4 * e + i] = p[4 * e + i] > 0.0f ? p[4 * e + i] * (x[i] * unit) : 0.0f;
+            }
+          }
+          weights[k] = narrow(p, static_cast<const T*>(nullptr));
+          if constexpr (FMT == kCacheSame) {
+            // the sum of the weights as they were rounded
+#pragma unroll
+            for (int i = 0; i < 4; ++i) l = add_pair<T>(weights[k][i], l);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int d = 0; d < DP / 32; ++d) {
+            rw4 a;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const as4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                  (ACP_LDS as4*)(vt + h * kBlock + (va ^ (64u * d)) + (16u * k + 8u * e) * S::kRow));
+              const rw2 x = __builtin_bit_cast(rw2, u);
+              a[2 * e] = x[0];
+              a[2 * e + 1] = x[1];
+            }
+            o[d] = mfma32<T>(a, weights[k], o[d]);
+          }
+      }
+    }
+    if constexpr (!DIRECT) {
+      if (more) {
+        put(b ^ 1u);
+        put_scales(b ^ 1u);
+      }
+    }
+    now = next;
+    here = next_here;
+    b ^= 1u;
+  }
+  if constexpr (FMT != kCacheSame && std::is_same_v<T, _Float16>) {
+    const float unit = __builtin_amdgcn_ldexpf(1.0f, v_exp);
+#pragma unroll
+    for (int d = 0; d < DP / 32; ++d) o[d] *= unit;
+  }
+  l = sum_step<5>(l);
+  if (!any) return;
+  prompt_rows<T, FMT, DP>(attend_args(), t, to, begin, keys, kv, o, m, l);
+}
+
+template <class T, int FMT, int DP, bool SHARES, bool DIRECT>
+__global__ __launch_bounds__(kAttendThreads, DP == 256 ? 1 : 2) void attend_prompt_kernel(const AttendArgs A) {
+  using S = PromptShape<FMT, DP>;
+  __shared__ __attribute__((aligned(16))) char lds[2][2][S::kTile];
+  __shared__ __attribute__((aligned(16))) float scales[2][2][S::kKeys];
+  const AttendPlace at(A);
+  Walk<kPromptRows, kCutPrompt, SHARES> walk;
+  if constexpr (!SHARES) {
+    Tile t;
+    if (!t.find<kPromptRows>(A, at.index)) return;
+    walk.cut(A, static_cast<uint32_t>(t.keys));
+    const Partial to(A, walk, t, at.kv);
+    prompt_tile<T, FMT, DP, DIRECT>(A, t, to, walk.begin, walk.end, at.kv, lds, scales);
+  } else {
+    __shared__ uint64_t walk_space[kWalkWords];
+    if (!walk.begin_at(A, at.index, walk_space)) return;
+    bool more;
+    do {
+      Tile t;
+      if (t.set<kPromptRows>(A, walk.seq, walk.tile)) {
+        walk.cut(A, static_cast<uint32_t>(t.keys));
+        const Partial to(A, walk, t, at.kv);
+        walk.put(walk_space);
+        prompt_tile<T, FMT, DP, DIRECT>(attend_args(), t, to, walk.begin, walk.end, at.kv, lds, scales);
+      }
+      __syncthreads();  // the next tile's keys and sums go where this one's were
+      walk.take(walk_space);
+      more = walk.next(A);
+      __syncthreads();
+    } while (more);
+  }
 }
 
 template <class T>
 hipError_t attend_prompt_for(int cache, int padded, const AttendArgs& a, hipStream_t s) {
   const void* f = nullptr;
-#define ACP_PROMPT(FMT, DP) \
-  if (cache == FMT && padded == DP) f = reinterpret_cast<const void*>(attend_prompt_kernel<T, FMT, DP>)
+#define ACP_PROMPT(FMT, DP)                                                                                    \
+  if (cache == FMT && padded == DP)                                                                            \
+    f = FMT == kCacheSame && a.direct                                                                          \
+            ? (a.shares ? reinterpret_cast<const void*>(attend_prompt_kernel<T, kCacheSame, DP, true, true>)   \
+                        : reinterpret_cast<const void*>(attend_prompt_kernel<T, kCacheSame, DP, false, true>)) \
+            : (a.shares ? reinterpret_cast<const void*>(attend_prompt_kernel<T, FMT, DP, true, false>)         \
+                        : reinterpret_cast<const void*>(attend_prompt_kernel<T, FMT, DP, false, false>))
   ACP_PROMPT(kCacheSame, 64);
   ACP_PROMPT(kCacheSame, 128);
   ACP_PROMPT(kCacheSame, 256);
@@ -371,7 +456,7 @@ hipError_t attend_prompt_for(int cache, int padded, const AttendArgs& a, hipStre
   if (f == nullptr) return hipErrorInvalidValue;
   AttendArgs copy = a;
   void* args[] = {&copy};
-  return hipLaunchKernel(f, dim3(a.kv_heads.d * a.slots.d * a.splits), dim3(kAttendThreads), args, 0, s);
+  return hipLaunchKernel(f, dim3(attend_grid(a)), dim3(kAttendThreads), args, 0, s);
 }
 
 }  // namespace dev

@@ -54,20 +54,129 @@ __device__ __forceinline__ uint32_t v_at(uint32_t row, uint32_t piece) {
   return row * S::kRow + p * 16u;
 }
 
+// Channels 128 h + jc .. + 8 of row jr of each of the workgroup's heads, from the
+// sums of the waves that shared the head's keys; rows that are odd are left out.
+template <class T, class S, int WIDE>
+__device__ __forceinline__ void join_out(const AttendArgs& A, const Tile& t, const Partial& to, uint32_t kv0, int h,
+                                         const float* stage, const float (*stat)[kStepRows][2], const uint32_t* odd,
+                                         uint32_t jr, uint32_t jc, bool real) {
+  const uint32_t c = 128u * h + jc, side = 1u << A.side_log2, turns = 4u >> A.side_log2;
+  if (!real || jc >= WIDE || c >= A.dim) return;
+  for (uint32_t g = 0; g < side; ++g) {
+    if (odd[g] >> jr & 1u) continue;
+    float best = -__builtin_inff(), total = 0.0f, sum[8];
+    for (uint32_t k = 0; k < turns; ++k) best = __builtin_fmaxf(best, stat[k * side + g][jr][0]);
+    const float base = best == -__builtin_inff() ? 0.0f : best;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
+    for (uint32_t k = 0; k < turns; ++k) {
+      const uint32_t w = k * side + g;
+      const float f = exp2_of(stat[w][jr][0] - base);
+      total = __builtin_fmaf(f, stat[w][jr][1], total);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] = __builtin_fmaf(f, stage[(w * kStepRows + jr) * S::kJoinPitch + jc + i], sum[i]);
+    }
+    if (!to.wanted) {
+      uint32_t token, head;
+      t.place(A, t.first + jr, kv0 + g, &token, &head);
+      char* y = head_row(A, A.out, token, head);
+      const float inv = 1.0f / total;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] = total == 0.0f ? 0.0f : sum[i] * inv;
+      *reinterpret_cast<rw4_any*>(y + c * 2) = narrow(sum, static_cast<const T*>(nullptr));
+    } else {
+      const uint32_t index = g * kStepRows + jr;
+      float* y = to.part(A, index) + c;
+      *reinterpret_cast<af4*>(y) = af4{sum[0], sum[1], sum[2], sum[3]};
+      *reinterpret_cast<af4*>(y + 4) = af4{sum[4], sum[5], sum[6], sum[7]};
+      if (c == 0) {
+        float* z = to.stat(A, index);
+        z[0] = best;
+        z[1] = total;
+      }
+    }
+  }
+}
+
+// The waves' sums: row col, channel 16 d + 4 quarter + i in o[d][i].  A lane
+// joins eight channels of a row, head after head.
 template <class T, int FMT, int DP>
-__global__ __launch_bounds__(kAttendThreads, DP == 256 ? 1 : 2) void attend_step_kernel(const AttendArgs A) {
+__device__ __forceinline__ void step_rows(const AttendArgs& A, const Tile& t, const Partial& to, uint32_t begin,
+                                          uint32_t keys, uint32_t kv0, const af4 (&o)[DP / 16], float m, float l, char* lds,
+                                          float (*join_stat)[kStepRows][2], uint32_t* odd_rows) {
   using S = StepShape<T, FMT, DP>;
-  __shared__ __attribute__((aligned(16))) char lds[S::kLds];
-  __shared__ float join_stat[4][kStepRows][2];
-  __shared__ uint32_t odd_rows;
-  const AttendPlace at(A);
-  Tile t;
-  if (!t.find<kStepRows>(A, at.slot)) return;
-  const uint32_t splits = t.splits(A);
-  if (at.split >= splits) return;
-  const uint32_t lane = threadIdx.x & 63u, wave = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
+  const uint32_t thread = thread_again();
+  const uint32_t lane = thread & 63u, wave = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(thread >> 6));
+  const uint32_t col = lane & 15u, quarter = lane >> 4, side = 1u << A.side_log2;
+  if (quarter == 0) {
+    join_stat[wave][col][0] = m;
+    join_stat[wave][col][1] = l;
+  }
+  if (thread < 4) odd_rows[thread] = 0;
+  const uint32_t jr = thread / 16u, jc = thread % 16u * 8u;
+  constexpr int kParts = (DP + 127) / 128, kWide = DP < 128 ? DP : 128;
+  float* stage = reinterpret_cast<float*>(lds);
+  const uint32_t my_row = t.first + jr;
+  const bool row_real = my_row < static_cast<uint32_t>(t.rows);
+  const bool mixed = t.low + 1 < t.keys;  // rows that see less than others
+#pragma unroll
+  for (int h = 0; h < kParts; ++h) {
+    __syncthreads();
+#pragma unroll
+    for (int d = 0; d < kWide / 16; ++d)
+      *reinterpret_cast<af4*>(stage + (wave * kStepRows + col) * S::kJoinPitch + 16 * d + 4 * quarter) = o[8 * h + d];
+    __syncthreads();
+    if (mixed) {
+      // a row is odd by its sum or any of its channels, which other lanes have
+      if (row_real && t.position(A, my_row) + 1 < t.keys) {
+        for (uint32_t w = 0; w < 4u; ++w) {
+          bool fine = is_finite(join_stat[w][jr][1]);
+          if (jc < kWide) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) fine = fine && is_finite(stage[(w * kStepRows + jr) * S::kJoinPitch + jc + i]);
+          }
+          if (!fine) atomicOr(&odd_rows[w & (side - 1u)], 1u << jr);
+        }
+      }
+    }
+    if (kParts > 1 && mixed) continue;  // written below, once all channels were looked at
+    if (mixed) __syncthreads();
+    join_out<T, S, kWide>(A, t, to, kv0, h, stage, join_stat, odd_rows, jr, jc, row_real);
+  }
+  if (kParts > 1 && mixed) {
+#pragma unroll
+    for (int h = 0; h < kParts; ++h) {
+      __syncthreads();
+#pragma unroll
+      for (int d = 0; d < kWide / 16; ++d)
+        *reinterpret_cast<af4*>(stage + (wave * kStepRows + col) * S::kJoinPitch + 16 * d + 4 * quarter) = o[8 * h + d];
+      __syncthreads();
+      join_out<T, S, kWide>(A, t, to, kv0, h, stage, join_stat, odd_rows, jr, jc, row_real);
+    }
+  }
+  if (mixed) {
+    for (uint32_t g = 0; g < side; ++g)
+      for (uint32_t k = wave; k < kStepRows; k += 4u)
+        if (odd_rows[g] >> k & 1u) {
+          const uint32_t index = g * kStepRows + k;
+          row_by_keys<T, FMT, DP>(A, t, t.first + k, kv0 + g, begin, keys, to.part(A, index), to.stat(A, index));
+        }
+  }
+}
+
+// A tile's keys [begin, keys) for the workgroup's heads.
+template <class T, int FMT, int DP>
+__device__ __forceinline__ void step_tile(const AttendArgs& A, const Tile& t, const Partial& to, uint32_t begin,
+                                          uint32_t keys, uint32_t kv0, char* lds, float (*join_stat)[kStepRows][2],
+                                          uint32_t* odd_rows) {
+  using S = StepShape<T, FMT, DP>;
+  const uint32_t thread = thread_again();
+  const uint32_t lane = thread & 63u, wave = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(thread >> 6));
   const uint32_t col = lane & 15u, quarter = lane >> 4;
-  const uint32_t keys = static_cast<uint32_t>(t.keys);
+  // Waves side by side have `side` heads of the same keys, and 4 / side of them
+  // take a head's steps in turn.
+  const uint32_t side = 1u << A.side_log2, turn = wave >> A.side_log2, stride = (4u >> A.side_log2) * kStepKeys;
+  const uint32_t kv = kv0 + (wave & (side - 1u));
   const bool exact = A.dim == DP;
   char* mine = lds + wave * S::kWaveBytes;
 
@@ -78,13 +187,13 @@ __global__ __launch_bounds__(kAttendThreads, DP == 256 ? 1 : 2) void attend_step
   rw4 q[S::kSteps];
   {
     uint32_t token, head;
-    t.place(A, real ? row : t.first, at.kv, &token, &head);
+    t.place(A, real ? row : t.first, kv, &token, &head);
     const char* qr = head_row(A, A.q, token, head);
 #pragma unroll
     for (int s = 0; s < S::kSteps; ++s) {
       const uint32_t c = FMT == kCacheSame ? 32u * s + 8u * quarter : 64u * (s / 2) + 16u * quarter + 8u * (s & 1);
       q[s] = rw4{0u, 0u, 0u, 0u};
-      if (real && c < A.dim) q[s] = *reinterpret_cast<const rw4_any*>(qr + c * 2);
+      if (real && c < A.dim) q[s] = *reinterpret_cast<const rw4_any*>(qr + c * 2) ^ A.flip;
     }
   }
 
@@ -94,18 +203,6 @@ __global__ __launch_bounds__(kAttendThreads, DP == 256 ? 1 : 2) void attend_step
   float m = -__builtin_inff(), l = 0.0f;
   int v_exp = -200;  // float16 with 8-bit values: o holds sums in units of 2^v_exp
 
-  // The wave's steps: first keys, in ascending order
-  const uint32_t per = A.chunk / (4u * kStepKeys);
-  struct Cursor {
-    uint32_t key, n;
-  };
-  auto advance = [&](Cursor* c) {
-    c->key += 4u * kStepKeys;
-    if (++c->n == per) {
-      c->n = 0;
-      c->key += (A.splits - 1u) * A.chunk;
-    }
-  };
   // Lanes 0..31 (and again 32..63) have a key each: its page, or -1
   auto page_at = [&](uint32_t key0) -> int32_t {
     const uint32_t key = key0 + (lane & 31u);
@@ -128,7 +225,7 @@ __global__ __launch_bounds__(kAttendThreads, DP == 256 ? 1 : 2) void attend_step
     r.ks = r.vs = 0.0f;
     if constexpr (FMT != kCacheSame) {
       if (page >= 0) {
-        const uint64_t s = (static_cast<uint64_t>(page) * A.batch.page.d + index) * A.kv_heads.d + at.kv;
+        const uint64_t s = (static_cast<uint64_t>(page) * A.batch.page.d + index) * (A.kv_heads.d << A.side_log2) + kv;
         r.ks = A.k.scales[s];
         r.vs = A.v.scales[s];
       }
@@ -140,8 +237,8 @@ __global__ __launch_bounds__(kAttendThreads, DP == 256 ? 1 : 2) void attend_step
     const int hi = __builtin_amdgcn_ds_bpermute(static_cast<int>(src * 4u), static_cast<int>(v >> 32));
     return static_cast<int64_t>(static_cast<uint32_t>(lo)) | static_cast<int64_t>(hi) << 32;
   };
-  const char* kbase = A.k.p + at.kv * A.k.s[2];
-  const char* vbase = A.v.p + at.kv * A.v.s[2];
+  const char* kbase = A.k.p + kv * A.k.s[2];
+  const char* vbase = A.v.p + kv * A.v.s[2];
   rw4 kr[2][S::kKRegs], vr[S::kVRegs];
   // where a piece of 16 bytes at byte c of a row holds channels: all of it, or (codes) its first 8
   const uint32_t row_bytes = A.dim * S::kBytes;
@@ -159,7 +256,15 @@ __global__ __launch_bounds__(kAttendThreads, DP == 256 ? 1 : 2) void attend_step
     const char* p[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) p[h] = kbase + from_lane(r.k, 16u * h + col) + 16u * quarter;
-    if (exact && r.here == 0xFFFFFFFFu) {
+    if (exact && r.here == 0xFFFFFFFFu && A.once) {
+      asm volatile("");  // keeps the branches apart: joined, the loads would lose their policy
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < S::kKRegs; ++i)
+          kr[h][i] = __builtin_nontemporal_load(reinterpret_cast<const rw4_any*>(p[h] + 64 * i));
+      asm volatile("");
+    } else if (exact && r.here == 0xFFFFFFFFu) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -177,7 +282,12 @@ __global__ __launch_bounds__(kAttendThreads, DP == 256 ? 1 : 2) void attend_step
     const char* p[S::kVRegs];
 #pragma unroll
     for (int i = 0; i < S::kVRegs; ++i) p[i] = vbase + from_lane(r.v, first + i * S::kVRows) + piece * 16u;
-    if (exact && r.here == 0xFFFFFFFFu) {
+    if (exact && r.here == 0xFFFFFFFFu && A.once) {
+      asm volatile("");
+#pragma unroll
+      for (int i = 0; i < S::kVRegs; ++i) vr[i] = __builtin_nontemporal_load(reinterpret_cast<const rw4_any*>(p[i]));
+      asm volatile("");
+    } else if (exact && r.here == 0xFFFFFFFFu) {
 #pragma unroll
       for (int i = 0; i < S::kVRegs; ++i) vr[i] = *reinterpret_cast<const rw4_any*>(p[i]);
     } else {
@@ -187,22 +297,22 @@ __global__ __launch_bounds__(kAttendThreads, DP == 256 ? 1 : 2) void attend_step
     }
   };
 
-  Cursor now{at.split * A.chunk + wave * kStepKeys, 0}, next = now;
-  advance(&next);
+  // The wave's steps: this one and the next, whose rows load meanwhile; the page
+  // numbers of the one after are on their way too.
+  uint32_t now = begin + turn * kStepKeys, next = now + stride;
   int32_t next_page = -1;
   Rows r{};
-  if (now.key < keys) {
-    const int32_t page = page_at(now.key);
-    next_page = page_at(next.key);
-    r = rows_at(now.key, page);
+  if (now < keys) {
+    const int32_t page = page_at(now);
+    next_page = page_at(next);
+    r = rows_at(now, page);
     load_k(r);
     load_v(r);
   }
-  while (now.key < keys) {
-    Cursor after = next;
-    advance(&after);
-    const int32_t after_page = page_at(after.key);
-    const Rows rn = rows_at(next.key, next_page);
+  while (now < keys) {
+    const int32_t after_page = page_at(next + stride);
+    const Rows rn = rows_at(next, next_page);
+    const bool more = next < keys;
 
     af4 s[2];
 #pragma unroll
@@ -215,7 +325,7 @@ __global__ __launch_bounds__(kAttendThreads, DP == 256 ? 1 : 2) void attend_step
           s[h] = mfma16<T>(codes_to<T, FMT>(kr[h][i / 2][2 * (i & 1)], kr[h][i / 2][2 * (i & 1) + 1]), q[i], s[h]);
       }
     }
-    if (next.key < keys) load_k(rn);
+    if (more) load_k(rn);
 
     // scores in powers of two, and what is hidden
     float x[8], ws[8];
@@ -230,11 +340,11 @@ __global__ __launch_bounds__(kAttendThreads, DP == 256 ? 1 : 2) void attend_step
           ws[4 * h + i] = as_float(static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(src, static_cast<int>(as_bits(r.vs)))));
         }
       }
-    if (r.here != 0xFFFFFFFFu || static_cast<int32_t>(now.key + kStepKeys - 1u) > t.low) {
+    if (r.here != 0xFFFFFFFFu || static_cast<int32_t>(now + kStepKeys - 1u) > t.low) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const uint32_t j = 16u * (k / 4) + 4u * quarter + (k & 3);
-        if (static_cast<int32_t>(now.key + j) > sees || !(r.here >> j & 1u)) x[k] = -__builtin_inff();
+        if (static_cast<int32_t>(now + j) > sees || !(r.here >> j & 1u)) x[k] = -__builtin_inff();
       }
     }
     // The running maximum is taken up only when it grows by 2^8 or more: weights
@@ -292,7 +402,7 @@ __global__ __launch_bounds__(kAttendThreads, DP == 256 ? 1 : 2) void attend_step
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    if (next.key < keys) load_v(rn);
+    if (more) load_v(rn);
 #pragma unroll
     for (int d = 0; d < DP / 16; ++d) {
       rw4 a;
@@ -318,7 +428,7 @@ __global__ __launch_bounds__(kAttendThreads, DP == 256 ? 1 : 2) void attend_step
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     now = next;
-    next = after;
+    next += stride;
     next_page = after_page;
     r = rn;
   }
@@ -329,97 +439,49 @@ __global__ __launch_bounds__(kAttendThreads, DP == 256 ? 1 : 2) void attend_step
   }
   l = sum_step<5>(sum_step<4>(l));
 
-  // The waves' sums: row col, channel 16 d + 4 quarter + i in o[d][i]
-  if (quarter == 0) {
-    join_stat[wave][col][0] = m;
-    join_stat[wave][col][1] = l;
+  step_rows<T, FMT, DP>(attend_args(), t, to, begin, keys, kv0, o, m, l, lds, join_stat, odd_rows);
+}
+
+template <class T, int FMT, int DP, bool SHARES>
+__global__ __launch_bounds__(kAttendThreads, DP == 256 ? 1 : 2) void attend_step_kernel(const AttendArgs A) {
+  __shared__ __attribute__((aligned(16))) char lds[StepShape<T, FMT, DP>::kLds];
+  __shared__ float join_stat[4][kStepRows][2];
+  __shared__ uint32_t odd_rows[4];
+  const AttendPlace at(A);
+  Walk<kStepRows, kCutStep, SHARES> walk;
+  if constexpr (!SHARES) {
+    Tile t;
+    if (!t.find<kStepRows>(A, at.index)) return;
+    walk.cut(A, static_cast<uint32_t>(t.keys));
+    const Partial to(A, walk, t, at.kv);
+    step_tile<T, FMT, DP>(A, t, to, walk.begin, walk.end, at.kv << A.side_log2, lds, join_stat, odd_rows);
+  } else {
+    __shared__ uint64_t walk_space[kWalkWords];
+    if (!walk.begin_at(A, at.index, walk_space)) return;
+    bool more;
+    do {
+      Tile t;
+      if (t.set<kStepRows>(A, walk.seq, walk.tile)) {
+        walk.cut(A, static_cast<uint32_t>(t.keys));
+        const Partial to(A, walk, t, at.kv);
+        walk.put(walk_space);
+        step_tile<T, FMT, DP>(attend_args(), t, to, walk.begin, walk.end, at.kv << A.side_log2, lds, join_stat, odd_rows);
+      }
+      __syncthreads();  // the next tile's keys and sums go where this one's were
+      walk.take(walk_space);
+      more = walk.next(A);
+      __syncthreads();
+    } while (more);
   }
-  if (threadIdx.x == 0) odd_rows = 0;
-  const uint32_t jr = threadIdx.x / 16u, jc = threadIdx.x % 16u * 8u;  // row and channels that a lane joins
-  constexpr int kParts = (DP + 127) / 128, kWide = DP < 128 ? DP : 128;
-  float sums[kParts][8], total = 0.0f, best = -__builtin_inff(), w[4];
-  float* stage = reinterpret_cast<float*>(lds);
-#pragma unroll
-  for (int h = 0; h < kParts; ++h) {
-    __syncthreads();
-#pragma unroll
-    for (int d = 0; d < kWide / 16; ++d)
-      *reinterpret_cast<af4*>(stage + (wave * kStepRows + col) * S::kJoinPitch + 16 * d + 4 * quarter) = o[8 * h + d];
-    __syncthreads();
-    if (h == 0) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) best = __builtin_fmaxf(best, join_stat[k][jr][0]);
-      const float base = best == -__builtin_inff() ? 0.0f : best;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        w[k] = exp2_of(join_stat[k][jr][0] - base);
-        total = __builtin_fmaf(w[k], join_stat[k][jr][1], total);
-      }
-    }
-    if (jc < kWide) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        sums[h][i] = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          sums[h][i] = __builtin_fmaf(w[k], stage[(k * kStepRows + jr) * S::kJoinPitch + jc + i], sums[h][i]);
-      }
-    }
-  }
-  const uint32_t my_row = t.first + jr;
-  const bool row_real = my_row < static_cast<uint32_t>(t.rows);
-  if (row_real && t.low + 1 < t.keys) {  // rows that see less than others
-    bool fine = is_finite(total);
-    if (jc < kWide) {
-#pragma unroll
-      for (int h = 0; h < kParts; ++h)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) fine = fine && is_finite(sums[h][i]);
-    }
-    if (!fine && t.position(A, my_row) + 1 < t.keys) atomicOr(&odd_rows, 1u << jr);
-  }
-  __syncthreads();
-  const uint32_t odd = odd_rows;
-  if (row_real && jc < kWide && !(odd >> jr & 1u)) {
-    uint32_t token, head;
-    t.place(A, my_row, at.kv, &token, &head);
-    if (splits == 1u) {
-      char* y = head_row(A, A.out, token, head);
-      const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-#pragma unroll
-      for (int h = 0; h < kParts; ++h) {
-        const uint32_t c = 128u * h + jc;
-        float f[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = total == 0.0f ? 0.0f : sums[h][i] * inv;
-        if (c < A.dim) *reinterpret_cast<rw4_any*>(y + c * 2) = narrow(f, static_cast<const T*>(nullptr));
-      }
-    } else {
-      const uint64_t r0 = (static_cast<uint64_t>(at.split) * A.tokens + token) * A.heads.d + head;
-#pragma unroll
-      for (int h = 0; h < kParts; ++h) {
-        const uint32_t c = 128u * h + jc;
-        if (c < A.dim) {
-          float* y = A.part + r0 * A.dim + c;
-          *reinterpret_cast<af4*>(y) = af4{sums[h][0], sums[h][1], sums[h][2], sums[h][3]};
-          *reinterpret_cast<af4*>(y + 4) = af4{sums[h][4], sums[h][5], sums[h][6], sums[h][7]};
-        }
-      }
-      if (jc == 0) {
-        A.stat[2 * r0] = best;
-        A.stat[2 * r0 + 1] = total;
-      }
-    }
-  }
-  for (uint32_t k = wave; k < kStepRows; k += 4u)
-    if (odd >> k & 1u) row_by_keys<T, FMT, DP>(A, t, t.first + k, at.kv, at.split, splits);
 }
 
 template <class T>
 hipError_t attend_step_for(int cache, int padded, const AttendArgs& a, hipStream_t s) {
   const void* f = nullptr;
-#define ACP_STEP(FMT, DP) \
-  if (cache == FMT && padded == DP) f = reinterpret_cast<const void*>(attend_step_kernel<T, FMT, DP>)
+#define ACP_STEP(FMT, DP)                                                                       \
+  if (cache == FMT && padded == DP)                                                            \
+    f = a.shares ? reinterpret_cast<const void*>(attend_step_kernel<T, FMT, DP, true>)          \
+                 : reinterpret_cast<const void*>(attend_step_kernel<T, FMT, DP, false>)
   ACP_STEP(kCacheSame, 64);
   ACP_STEP(kCacheSame, 128);
   ACP_STEP(kCacheSame, 256);
@@ -433,7 +495,7 @@ hipError_t attend_step_for(int cache, int padded, const AttendArgs& a, hipStream
   if (f == nullptr) return hipErrorInvalidValue;
   AttendArgs copy = a;
   void* args[] = {&copy};
-  return hipLaunchKernel(f, dim3(a.kv_heads.d * a.slots.d * a.splits), dim3(kAttendThreads), args, 0, s);
+  return hipLaunchKernel(f, dim3(attend_grid(a)), dim3(kAttendThreads), args, 0, s);
 }
 
 }  // namespace dev
