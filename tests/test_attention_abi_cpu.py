@@ -71,7 +71,7 @@ def test_workspace():
     # what the caller knows of the lengths makes it smaller; they are never read
     assert size(4, 4, 4096, max_length=200) == 0
     assert 0 < size(4, 4, 4096, max_length=3000) <= long
-    assert size(4, 4, 4096, starts=0) == long
+    assert 0 < size(4, 4, 4096, starts=0) <= long
     # many tiles fill the device without a split
     assert size(1 << 16, 4, 4096) == 0
     refused(lambda: acp.acp_cache_attention_workspace(desc(1, Q), None, pages_of()), INVALID, "no cache")
