@@ -299,13 +299,17 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
           }
       }
       if (here != ~uint64_t(0) || static_cast<int32_t>(now + S::kKeys - 1u) > low) {
+        // both in the lane's own terms, so that the bit and the bound are constants
+        const int32_t left = sees - static_cast<int32_t>(now + 4u * half);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t mine = static_cast<uint32_t>(here >> (32 * h)) >> (4u * half);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const uint32_t j = 32u * h + 8u * (i / 4) + 4u * half + (i & 3);
-            if (static_cast<int32_t>(now + j) > sees || !(here >> j & 1u)) s[h][i] = -__builtin_inff();
+            const int j = 8 * (i / 4) + (i & 3);
+            if (32 * h + j > left || !(mine & (1u << j))) s[h][i] = -__builtin_inff();
           }
+        }
       }
       float top = -__builtin_inff();
 #pragma unroll

@@ -341,10 +341,13 @@ __device__ __forceinline__ void step_tile(const AttendArgs& A, const Tile& t, co
         }
       }
     if (r.here != 0xFFFFFFFFu || static_cast<int32_t>(now + kStepKeys - 1u) > t.low) {
+      // both in the lane's own terms, so that the bit and the bound are constants
+      const int32_t left = sees - static_cast<int32_t>(now + 4u * quarter);
+      const uint32_t mine = r.here >> (4u * quarter);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const uint32_t j = 16u * (k / 4) + 4u * quarter + (k & 3);
-        if (static_cast<int32_t>(now + j) > sees || !(r.here >> j & 1u)) x[k] = -__builtin_inff();
+        const int j = 16 * (k / 4) + (k & 3);
+        if (j > left || !(mine & (1u << j))) x[k] = -__builtin_inff();
       }
     }
     // The running maximum is taken up only when it grows by 2^8 or more: weights
