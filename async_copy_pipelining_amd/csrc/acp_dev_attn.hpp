@@ -325,6 +325,17 @@ __device__ __forceinline__ int32_t key_page(const AttendArgs& A, uint32_t seq, u
   return page_of(A.batch, seq, n);
 }
 
+// The same in two parts, for loops over keys: the load, at an address that is
+// right for any key (keys > 0), and what it says, once it is needed.  A test in
+// between would wait for all that was loaded before.
+__device__ __forceinline__ int32_t page_entry(const AttendArgs& A, uint32_t seq, uint32_t key, uint32_t keys) {
+  const uint32_t n = divide(key < keys ? key : keys - 1u, A.batch.page);
+  return A.batch.pages[static_cast<uint64_t>(seq) * A.batch.max_pages + n];
+}
+__device__ __forceinline__ int32_t entry_page(const AttendArgs& A, int32_t entry, uint32_t key, uint32_t keys) {
+  return key < keys && static_cast<uint32_t>(entry) < A.batch.page_count ? entry : -1;
+}
+
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // The two halves of lanes that hold one row's values 16 or 32 lanes apart.

@@ -147,26 +147,36 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
   int v_exp = -200;  // as in the form for few rows
 
   // Each wave finds the pages of all the tile's keys: lane j has key j
-  auto page_at = [&](uint32_t key0) -> int32_t {
-    const uint32_t key = key0 + lane;
-    uint32_t index;
-    return key < keys ? key_page(A, t.seq, key, &index) : -1;
-  };
-  auto row_of = [&](const CacheTensor& c, uint32_t key0, uint32_t j, int32_t page) {
+  auto entry_at = [&](uint32_t key0) { return page_entry(A, t.seq, key0 + lane, keys); };
+  auto page_at = [&](uint32_t key0, int32_t entry) { return entry_page(A, entry, key0 + lane, keys); };
+  // An instruction of a wave has 64 pieces: rows of kRowsEach keys, one after
+  // another, instruction i of wave w those from (4 i + w) kRowsEach on.  Where all
+  // of them lie in one page, which pages of a multiple of kRowsEach make sure of,
+  // their address is the wave's and takes no vector instructions; else each lane
+  // works out its own.
+  constexpr uint32_t kRowsEach = 64u / S::kPieces, kEach = S::kRegs;
+  static_assert(S::kKeys % (4u * kRowsEach) == 0 && kEach * 4u * kRowsEach == S::kKeys);
+  const uint32_t slot = lane % S::kPieces, line = lane / S::kPieces;
+  const bool runs = A.batch.page.d % kRowsEach == 0;  // begin is a multiple of kCutPrompt
+  auto row_of = [&](const CacheTensor& c, uint32_t key0, uint32_t i, int32_t page) {
+    const char* p = c.p + kv * c.s[2];
+    if (runs) {
+      const uint32_t j = (i * 4u + wave) * kRowsEach, key = key0 + j;
+      const int64_t g = __builtin_amdgcn_readlane(page, static_cast<int>(j));
+      return p + (g * c.s[0] + (key - divide(key, A.batch.page) * A.batch.page.d) * c.s[1]) + line * c.s[1];
+    }
+    const uint32_t j = (i * 4u + wave) * kRowsEach + line, key = key0 + j;
     const int64_t g = __builtin_amdgcn_ds_bpermute(static_cast<int>(j * 4u), page);
-    const uint32_t key = key0 + j;
-    return c.p + kv * c.s[2] + g * c.s[0] + (key - divide(key, A.batch.page) * A.batch.page.d) * c.s[1];
+    return p + g * c.s[0] + (key - divide(key, A.batch.page) * A.batch.page.d) * c.s[1];
   };
-  // DIRECT: piece `slot` of row j in LDS is piece k_slot (v_slot) of the row
-  constexpr uint32_t kRowsEach = 1024u / S::kRow, kEach = S::kTile / 1024u / 4u;  // rows of an instruction; a wave's
-  const uint32_t slot = lane % S::kPieces;
+  // DIRECT: piece `slot` of row j in LDS is piece kp (vp) of the row
   auto fetch = [&](uint32_t b, uint32_t key0, int32_t page, uint64_t here) {
 #pragma unroll
     for (uint32_t i = 0; i < kEach; ++i) {
-      const uint32_t n = i * 4u + wave, j = n * kRowsEach + lane / S::kPieces;
+      const uint32_t n = i * 4u + wave, j = n * kRowsEach + line;
       const uint32_t kp = (k_at<DP>(j, slot) - j * S::kRow) / 16u, vp = (v_at<DP>(j, slot) - j * S::kRow) / 16u;
-      const char* kr = row_of(A.k, key0, j, page) + kp * 16u;
-      const char* vr = row_of(A.v, key0, j, page) + vp * 16u;
+      const char* kr = row_of(A.k, key0, i, page) + kp * 16u;
+      const char* vr = row_of(A.v, key0, i, page) + vp * 16u;
       const uint32_t kt = lds_offset(lds[b][0]) + n * 1024u, vt = lds_offset(lds[b][1]) + n * 1024u;
       if (here == ~uint64_t(0) && A.dim == DP) {
         to_lds(kr, kt);
@@ -182,19 +192,18 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
       }
     }
   };
-  // else: the lane's pieces of a tile: piece `piece` of rows first, first + kStride, ...
-  const uint32_t piece = thread % S::kPieces, first = thread / S::kPieces;
+  // else: the lane's pieces of a tile
   typename S::Piece kw[DIRECT ? 1 : S::kRegs], vw[DIRECT ? 1 : S::kRegs];
   auto load = [&](uint32_t key0, int32_t page, uint64_t here) {
     using P = typename S::Piece;
     typedef P P_any __attribute__((aligned(1)));
 #pragma unroll
-    for (int i = 0; i < S::kRegs; ++i) {
-      const uint32_t j = first + i * S::kStride;
-      const char* kr = row_of(A.k, key0, j, page) + piece * sizeof(P);
-      const char* vr = row_of(A.v, key0, j, page) + piece * sizeof(P);
+    for (uint32_t i = 0; i < kEach; ++i) {
+      const uint32_t j = (i * 4u + wave) * kRowsEach + line;
+      const char* kr = row_of(A.k, key0, i, page) + slot * sizeof(P);
+      const char* vr = row_of(A.v, key0, i, page) + slot * sizeof(P);
       kw[i] = vw[i] = P{};
-      if (piece * 8u < A.dim && (here >> j & 1u)) {
+      if (slot * 8u < A.dim && (here >> j & 1u)) {
         kw[i] = *reinterpret_cast<const P_any*>(kr);
         vw[i] = *reinterpret_cast<const P_any*>(vr);
       }
@@ -206,10 +215,10 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
   };
   auto put = [&](uint32_t b) {
 #pragma unroll
-    for (int i = 0; i < S::kRegs; ++i) {
-      const uint32_t j = first + i * S::kStride;
-      *reinterpret_cast<rw4*>(lds[b][0] + k_at<DP>(j, piece)) = value(kw[i]);
-      *reinterpret_cast<rw4*>(lds[b][1] + v_at<DP>(j, piece)) = value(vw[i]);
+    for (uint32_t i = 0; i < kEach; ++i) {
+      const uint32_t j = (i * 4u + wave) * kRowsEach + line;
+      *reinterpret_cast<rw4*>(lds[b][0] + k_at<DP>(j, slot)) = value(kw[i]);
+      *reinterpret_cast<rw4*>(lds[b][1] + v_at<DP>(j, slot)) = value(vw[i]);
     }
   };
   // 8-bit rows: the scales of the tile's keys
@@ -241,7 +250,12 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
   const uint32_t va = v_at<DP>(4u * half + (lane & 15u) / 4u, 2u * (lane >> 4 & 1u) + (lane & 3u) / 2u) + (lane & 1u) * 8u;
 
   uint32_t now = begin, b = 0;
-  int32_t page = page_at(now), next_page = page_at(now + S::kKeys);
+  int32_t page = -1, entry = -1;  // of this tile; of the next, not looked at yet
+  if (now < keys) {
+    page = entry_at(now);
+    entry = entry_at(now + S::kKeys);
+  }
+  page = page_at(now, page);
   uint64_t here = __builtin_amdgcn_ballot_w64(page >= 0);
   if constexpr (DIRECT) {
     if (A.dim != DP) {  // channels that no row has
@@ -263,7 +277,8 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
     // this tile has arrived, and all waves are done with the other one
     if constexpr (DIRECT) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    page = next_page;
+    page = page_at(next, entry);
+    entry = entry_at(next + S::kKeys);
     const uint64_t next_here = __builtin_amdgcn_ballot_w64(page >= 0);
     if (more) {
       if constexpr (DIRECT) {
@@ -273,7 +288,6 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
         load_scales(next, page);
       }
     }
-    next_page = page_at(next + S::kKeys);
 
     if (static_cast<int32_t>(now) <= high) {
       const char* kt = lds[b][0];

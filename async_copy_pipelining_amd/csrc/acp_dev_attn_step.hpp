@@ -204,19 +204,16 @@ __device__ __forceinline__ void step_tile(const AttendArgs& A, const Tile& t, co
   int v_exp = -200;  // float16 with 8-bit values: o holds sums in units of 2^v_exp
 
   // Lanes 0..31 (and again 32..63) have a key each: its page, or -1
-  auto page_at = [&](uint32_t key0) -> int32_t {
-    const uint32_t key = key0 + (lane & 31u);
-    uint32_t index;
-    return key < keys ? key_page(A, t.seq, key, &index) : -1;
-  };
+  auto entry_at = [&](uint32_t key0) { return page_entry(A, t.seq, key0 + (lane & 31u), keys); };
   struct Rows {  // of the lane's key
     int64_t k, v;
     uint32_t here;  // keys that have a page, by bits: uniform
     float ks, vs;
   };
-  auto rows_at = [&](uint32_t key0, int32_t page) {
+  auto rows_at = [&](uint32_t key0, int32_t entry) {
     Rows r;
     const uint32_t key = key0 + (lane & 31u);
+    const int32_t page = entry_page(A, entry, key, keys);
     const uint32_t index = key - divide(key, A.batch.page) * A.batch.page.d;
     const int64_t g = page < 0 ? 0 : page;
     r.k = g * A.k.s[0] + index * A.k.s[1];
@@ -300,18 +297,18 @@ __device__ __forceinline__ void step_tile(const AttendArgs& A, const Tile& t, co
   // The wave's steps: this one and the next, whose rows load meanwhile; the page
   // numbers of the one after are on their way too.
   uint32_t now = begin + turn * kStepKeys, next = now + stride;
-  int32_t next_page = -1;
+  int32_t entry = -1;
   Rows r{};
   if (now < keys) {
-    const int32_t page = page_at(now);
-    next_page = page_at(next);
-    r = rows_at(now, page);
+    const int32_t first = entry_at(now);
+    entry = entry_at(next);
+    r = rows_at(now, first);
     load_k(r);
     load_v(r);
   }
   while (now < keys) {
-    const int32_t after_page = page_at(next + stride);
-    const Rows rn = rows_at(next, next_page);
+    const Rows rn = rows_at(next, entry);
+    entry = entry_at(next + stride);
     const bool more = next < keys;
 
     af4 s[2];
@@ -432,7 +429,6 @@ __device__ __forceinline__ void step_tile(const AttendArgs& A, const Tile& t, co
     __builtin_amdgcn_wave_barrier();
     now = next;
     next += stride;
-    next_page = after_page;
     r = rn;
   }
   if constexpr (FMT != kCacheSame && std::is_same_v<T, _Float16>) {
