@@ -336,6 +336,13 @@ __device__ __forceinline__ int32_t entry_page(const AttendArgs& A, int32_t entry
   return key < keys && static_cast<uint32_t>(entry) < A.batch.page_count ? entry : -1;
 }
 
+// Lane `src`'s value.
+__device__ __forceinline__ int64_t from_lane(int64_t v, uint32_t src) {
+  const int lo = __builtin_amdgcn_ds_bpermute(static_cast<int>(src * 4u), static_cast<int>(v));
+  const int hi = __builtin_amdgcn_ds_bpermute(static_cast<int>(src * 4u), static_cast<int>(v >> 32));
+  return static_cast<int64_t>(static_cast<uint32_t>(lo)) | static_cast<int64_t>(hi) << 32;
+}
+
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // The two halves of lanes that hold one row's values 16 or 32 lanes apart.

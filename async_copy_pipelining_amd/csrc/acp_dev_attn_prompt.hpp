@@ -22,20 +22,28 @@ struct PromptShape {
   static constexpr int kPieces = kRow / 16;
   static constexpr int kTile = kKeys * kRow;          // bytes of K or V
   using Piece = std::conditional_t<FMT == kCacheSame, rw4, rw2>;  // 8 channels
-  static constexpr int kRegs = kTile / 16 / kAttendThreads;
-  static constexpr int kStride = kAttendThreads / kPieces;  // rows between a lane's pieces
+  static constexpr int kRegs = kTile / 16 / kAttendThreads;  // pieces of K or V that a lane brings
 };
+
+// f(integral_constant i) for i = I .. N - 1
+template <uint32_t N, uint32_t I = 0, class F>
+__device__ __forceinline__ void unroll(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<uint32_t, I>{});
+    unroll<N, I + 1>(f);
+  }
+}
 
 // Where piece c of row r lies.  K is read as 16 bytes of 32 rows: pieces are
 // permuted by the row.  V's transposing reads take 64 bytes of four rows at a
 // time: units of that size are.
 template <int DP>
-__device__ __forceinline__ uint32_t k_at(uint32_t row, uint32_t piece) {
+__device__ __forceinline__ constexpr uint32_t k_at(uint32_t row, uint32_t piece) {
   constexpr uint32_t kPieces = DP / 8, kRows = kPieces >= 16 ? 1u : 16u / kPieces;
   return row * (DP * 2u) + (piece ^ ((row / kRows) & (kPieces - 1u) & 15u)) * 16u;
 }
 template <int DP>
-__device__ __forceinline__ uint32_t v_at(uint32_t row, uint32_t piece) {
+__device__ __forceinline__ constexpr uint32_t v_at(uint32_t row, uint32_t piece) {
   constexpr uint32_t kRows = DP >= 128 ? 1u : 128u / DP, kUnits = DP / 32;
   return row * (DP * 2u) + (piece ^ (((row / kRows) & 3u & (kUnits - 1u)) << 2)) * 16u;
 }
@@ -146,68 +154,82 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
   float m = -__builtin_inff(), l = 0.0f;
   int v_exp = -200;  // as in the form for few rows
 
-  // Each wave finds the pages of all the tile's keys: lane j has key j
+  // Each wave finds the rows of all the tile's keys: lane j has key j.
   auto entry_at = [&](uint32_t key0) { return page_entry(A, t.seq, key0 + lane, keys); };
   auto page_at = [&](uint32_t key0, int32_t entry) { return entry_page(A, entry, key0 + lane, keys); };
-  // An instruction of a wave has 64 pieces: rows of kRowsEach keys, one after
-  // another, instruction i of wave w those from (4 i + w) kRowsEach on.  Where all
-  // of them lie in one page, which pages of a multiple of kRowsEach make sure of,
-  // their address is the wave's and takes no vector instructions; else each lane
-  // works out its own.
+  // An instruction of a wave has 64 pieces: rows of kRowsEach keys, instruction i
+  // of wave w those from (4 i + w) kRowsEach on.  Piece `slot` of a row in LDS is
+  // piece kp (vp) of the row in memory: V's is the same for all i.
   constexpr uint32_t kRowsEach = 64u / S::kPieces, kEach = S::kRegs;
-  static_assert(S::kKeys % (4u * kRowsEach) == 0 && kEach * 4u * kRowsEach == S::kKeys);
-  const uint32_t slot = lane % S::kPieces, line = lane / S::kPieces;
-  const bool runs = A.batch.page.d % kRowsEach == 0;  // begin is a multiple of kCutPrompt
-  auto row_of = [&](const CacheTensor& c, uint32_t key0, uint32_t i, int32_t page) {
-    const char* p = c.p + kv * c.s[2];
-    if (runs) {
-      const uint32_t j = (i * 4u + wave) * kRowsEach, key = key0 + j;
-      const int64_t g = __builtin_amdgcn_readlane(page, static_cast<int>(j));
-      return p + (g * c.s[0] + (key - divide(key, A.batch.page) * A.batch.page.d) * c.s[1]) + line * c.s[1];
-    }
-    const uint32_t j = (i * 4u + wave) * kRowsEach + line, key = key0 + j;
-    const int64_t g = __builtin_amdgcn_ds_bpermute(static_cast<int>(j * 4u), page);
-    return p + g * c.s[0] + (key - divide(key, A.batch.page) * A.batch.page.d) * c.s[1];
-  };
-  // DIRECT: piece `slot` of row j in LDS is piece kp (vp) of the row
-  auto fetch = [&](uint32_t b, uint32_t key0, int32_t page, uint64_t here) {
+  static_assert(kEach * 4u * kRowsEach == S::kKeys);
+  const uint32_t slot = lane % S::kPieces, line = lane / S::kPieces, row_in = wave * kRowsEach + line;
+  static_assert(v_at<DP>(4u * kRowsEach, 0) == 4u * kRowsEach * S::kRow);
+  const uint32_t kp0 = (k_at<DP>(row_in, slot) - row_in * S::kRow) / 16u;
+  const uint32_t vp = (v_at<DP>(row_in, slot) - row_in * S::kRow) / 16u;
+  auto kp = [&](uint32_t i) { return kp0 ^ (k_at<DP>(i * 4u * kRowsEach, 0) - i * 4u * kRowsEach * S::kRow) / 16u; };
+  // Where the rows of the tile after this one lie.  The lanes of a row's pieces
+  // need kEach rows each, the same ones: the lanes of a quad work out one row each
+  // (two, where there are eight) and pass it on.
+  constexpr uint32_t kOwn = kEach < 4u ? kEach : 4u, kSets = kEach / kOwn;
+  const char* k_head = A.k.p + kv * A.k.s[2];
+  const char* v_head = A.v.p + kv * A.v.s[2];
+  const char *k_row[kSets], *v_row[kSets];
+  auto rows_at = [&](uint32_t key0, int32_t page) {
 #pragma unroll
-    for (uint32_t i = 0; i < kEach; ++i) {
-      const uint32_t n = i * 4u + wave, j = n * kRowsEach + line;
-      const uint32_t kp = (k_at<DP>(j, slot) - j * S::kRow) / 16u, vp = (v_at<DP>(j, slot) - j * S::kRow) / 16u;
-      const char* kr = row_of(A.k, key0, i, page) + kp * 16u;
-      const char* vr = row_of(A.v, key0, i, page) + vp * 16u;
-      const uint32_t kt = lds_offset(lds[b][0]) + n * 1024u, vt = lds_offset(lds[b][1]) + n * 1024u;
-      if (here == ~uint64_t(0) && A.dim == DP) {
-        to_lds(kr, kt);
-        to_lds(vr, vt);
-      } else {
-        if (!(here >> j & 1u)) {
-          *reinterpret_cast<rw4*>(lds[b][0] + n * 1024u + lane * 16u) = rw4{0u, 0u, 0u, 0u};
-          *reinterpret_cast<rw4*>(lds[b][1] + n * 1024u + lane * 16u) = rw4{0u, 0u, 0u, 0u};
-        } else {
-          if (kp * 8u < A.dim) to_lds(kr, kt);
-          if (vp * 8u < A.dim) to_lds(vr, vt);
-        }
-      }
+    for (uint32_t n = 0; n < kSets; ++n) {
+      const uint32_t j = (n * 4u + (lane & (kOwn - 1u))) * 4u * kRowsEach + row_in, key = key0 + j;
+      const uint32_t index = key - divide(key, A.batch.page) * A.batch.page.d;
+      const int p = __builtin_amdgcn_ds_bpermute(static_cast<int>(j * 4u), page);
+      const uint32_t g = p < 0 ? 0u : static_cast<uint32_t>(p);
+      k_row[n] = k_head + (g * A.k.s[0] + index * A.k.s[1]);
+      v_row[n] = v_head + (g * A.v.s[0] + index * A.v.s[1]);
     }
   };
-  // else: the lane's pieces of a tile
+  auto row_of = [&](const char* const (&own)[kSets], auto I) {
+    constexpr int i = decltype(I)::value;
+    const uint64_t p = reinterpret_cast<uint64_t>(own[i / 4]);
+    const uint32_t lo = static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(p), i % 4 * 0x55, 0xF, 0xF, true));
+    const uint32_t hi = static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(p >> 32), i % 4 * 0x55, 0xF, 0xF, true));
+    return reinterpret_cast<const char*>(static_cast<uint64_t>(hi) << 32 | lo);
+  };
+  auto fetch = [&](uint32_t b, uint64_t here) {
+    const uint32_t kt = lds_offset(lds[b][0]) + wave * 1024u, vt = lds_offset(lds[b][1]) + wave * 1024u;
+    if (here == ~uint64_t(0) && A.dim == DP) {
+      unroll<kEach>([&](auto I) {
+        constexpr uint32_t i = decltype(I)::value;
+        to_lds(row_of(k_row, I) + kp(i) * 16u, kt + i * 4096u);
+        to_lds(row_of(v_row, I) + vp * 16u, vt + i * 4096u);
+      });
+    } else {
+      unroll<kEach>([&](auto I) {
+        constexpr uint32_t i = decltype(I)::value;
+        const char* kr = row_of(k_row, I) + kp(i) * 16u;
+        const char* vr = row_of(v_row, I) + vp * 16u;
+        if (!(here >> (i * 4u * kRowsEach) >> row_in & 1u)) {
+          *reinterpret_cast<rw4*>(lds[b][0] + (i * 4u + wave) * 1024u + lane * 16u) = rw4{0u, 0u, 0u, 0u};
+          *reinterpret_cast<rw4*>(lds[b][1] + (i * 4u + wave) * 1024u + lane * 16u) = rw4{0u, 0u, 0u, 0u};
+        } else {
+          if (kp(i) * 8u < A.dim) to_lds(kr, kt + i * 4096u);
+          if (vp * 8u < A.dim) to_lds(vr, vt + i * 4096u);
+        }
+      });
+    }
+  };
+  // not DIRECT: the lane's pieces of a tile
   typename S::Piece kw[DIRECT ? 1 : S::kRegs], vw[DIRECT ? 1 : S::kRegs];
-  auto load = [&](uint32_t key0, int32_t page, uint64_t here) {
+  auto load = [&](uint64_t here) {
     using P = typename S::Piece;
     typedef P P_any __attribute__((aligned(1)));
-#pragma unroll
-    for (uint32_t i = 0; i < kEach; ++i) {
-      const uint32_t j = (i * 4u + wave) * kRowsEach + line;
-      const char* kr = row_of(A.k, key0, i, page) + slot * sizeof(P);
-      const char* vr = row_of(A.v, key0, i, page) + slot * sizeof(P);
+    unroll<kEach>([&](auto I) {
+      constexpr uint32_t i = decltype(I)::value;
+      const char* kr = row_of(k_row, I) + slot * sizeof(P);
+      const char* vr = row_of(v_row, I) + slot * sizeof(P);
       kw[i] = vw[i] = P{};
-      if (slot * 8u < A.dim && (here >> j & 1u)) {
+      if (slot * 8u < A.dim && (here >> (i * 4u * kRowsEach) >> row_in & 1u)) {
         kw[i] = *reinterpret_cast<const P_any*>(kr);
         vw[i] = *reinterpret_cast<const P_any*>(vr);
       }
-    }
+    });
   };
   auto value = [](const typename S::Piece& w) {
     if constexpr (FMT == kCacheSame) return w;
@@ -216,7 +238,7 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
   auto put = [&](uint32_t b) {
 #pragma unroll
     for (uint32_t i = 0; i < kEach; ++i) {
-      const uint32_t j = (i * 4u + wave) * kRowsEach + line;
+      const uint32_t j = i * 4u * kRowsEach + row_in;
       *reinterpret_cast<rw4*>(lds[b][0] + k_at<DP>(j, slot)) = value(kw[i]);
       *reinterpret_cast<rw4*>(lds[b][1] + v_at<DP>(j, slot)) = value(vw[i]);
     }
@@ -249,14 +271,11 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
   const uint32_t ka = k_at<DP>(col, half);
   const uint32_t va = v_at<DP>(4u * half + (lane & 15u) / 4u, 2u * (lane >> 4 & 1u) + (lane & 3u) / 2u) + (lane & 1u) * 8u;
 
+  // Three tiles at once: one is computed, the next one's rows load, the pages of
+  // the one after are known (`page`), and of the fourth they load (`entry`).
   uint32_t now = begin, b = 0;
-  int32_t page = -1, entry = -1;  // of this tile; of the next, not looked at yet
-  if (now < keys) {
-    page = entry_at(now);
-    entry = entry_at(now + S::kKeys);
-  }
-  page = page_at(now, page);
-  uint64_t here = __builtin_amdgcn_ballot_w64(page >= 0);
+  int32_t page = -1, entry = -1;
+  uint64_t here = 0, next_here = 0;
   if constexpr (DIRECT) {
     if (A.dim != DP) {  // channels that no row has
 #pragma unroll 1
@@ -264,12 +283,25 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
         *reinterpret_cast<rw4*>(lds[0][0] + i) = rw4{0u, 0u, 0u, 0u};
       __syncthreads();
     }
-    if (now < keys) fetch(0, now, page, here);
-  } else {
-    load(now, page, here);
-    load_scales(now, page);
-    put(0);
-    put_scales(0);
+  }
+  if (now < keys) {
+    const int32_t first = entry_at(now), second = entry_at(now + S::kKeys);
+    entry = entry_at(now + 2u * S::kKeys);
+    page = page_at(now, first);
+    here = __builtin_amdgcn_ballot_w64(page >= 0);
+    rows_at(now, page);
+    if constexpr (DIRECT) {
+      page = page_at(now + S::kKeys, second);
+      fetch(0, here);
+    } else {
+      load(here);
+      load_scales(now, page);
+      page = page_at(now + S::kKeys, second);
+      put(0);
+      put_scales(0);
+    }
+    next_here = __builtin_amdgcn_ballot_w64(page >= 0);
+    rows_at(now + S::kKeys, page);
   }
   while (now < keys) {
     const uint32_t next = now + S::kKeys;
@@ -277,17 +309,17 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
     // this tile has arrived, and all waves are done with the other one
     if constexpr (DIRECT) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    page = page_at(next, entry);
-    entry = entry_at(next + S::kKeys);
-    const uint64_t next_here = __builtin_amdgcn_ballot_w64(page >= 0);
-    if (more) {
-      if constexpr (DIRECT) {
-        fetch(b ^ 1u, next, page, next_here);
-      } else {
-        load(next, page, next_here);
-        load_scales(next, page);
-      }
+    if constexpr (!DIRECT) {
+      if (more) load_scales(next, page);
     }
+    page = page_at(next + S::kKeys, entry);
+    entry = entry_at(next + 2u * S::kKeys);
+    if (more) {
+      if constexpr (DIRECT) fetch(b ^ 1u, next_here);
+      else load(next_here);
+    }
+    const uint64_t after_here = __builtin_amdgcn_ballot_w64(page >= 0);
+    rows_at(next + S::kKeys, page);
 
     if (static_cast<int32_t>(now) <= high) {
       const char* kt = lds[b][0];
@@ -406,6 +438,7 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
     }
     now = next;
     here = next_here;
+    next_here = after_here;
     b ^= 1u;
   }
   if constexpr (FMT != kCacheSame && std::is_same_v<T, _Float16>) {

@@ -229,11 +229,6 @@ __device__ __forceinline__ void step_tile(const AttendArgs& A, const Tile& t, co
     }
     return r;
   };
-  auto from_lane = [](int64_t v, uint32_t src) {
-    const int lo = __builtin_amdgcn_ds_bpermute(static_cast<int>(src * 4u), static_cast<int>(v));
-    const int hi = __builtin_amdgcn_ds_bpermute(static_cast<int>(src * 4u), static_cast<int>(v >> 32));
-    return static_cast<int64_t>(static_cast<uint32_t>(lo)) | static_cast<int64_t>(hi) << 32;
-  };
   const char* kbase = A.k.p + kv * A.k.s[2];
   const char* vbase = A.v.p + kv * A.v.s[2];
   rw4 kr[2][S::kKRegs], vr[S::kVRegs];
