@@ -192,7 +192,7 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
     const uint32_t hi = static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(p >> 32), i % 4 * 0x55, 0xF, 0xF, true));
     return reinterpret_cast<const char*>(static_cast<uint64_t>(hi) << 32 | lo);
   };
-  auto fetch = [&](uint32_t b, uint64_t here) {
+  auto bring = [&](uint32_t b, uint64_t here) {
     const uint32_t kt = lds_offset(lds[b][0]) + wave * 1024u, vt = lds_offset(lds[b][1]) + wave * 1024u;
     if (here == ~uint64_t(0) && A.dim == DP) {
       unroll<kEach>([&](auto I) {
@@ -292,7 +292,7 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
     rows_at(now, page);
     if constexpr (DIRECT) {
       page = page_at(now + S::kKeys, second);
-      fetch(0, here);
+      bring(0, here);
     } else {
       load(here);
       load_scales(now, page);
@@ -315,23 +315,49 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
     page = page_at(next + S::kKeys, entry);
     entry = entry_at(next + 2u * S::kKeys);
     if (more) {
-      if constexpr (DIRECT) fetch(b ^ 1u, next_here);
+      if constexpr (DIRECT) bring(b ^ 1u, next_here);
       else load(next_here);
     }
-    const uint64_t after_here = __builtin_amdgcn_ballot_w64(page >= 0);
-    rows_at(next + S::kKeys, page);
-
     if (static_cast<int32_t>(now) <= high) {
       const char* kt = lds[b][0];
       const char* vt = lds[b][1];
       af16 s[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[h][i] = 0.0f;
+      // 16 keys' values, read while the scores are computed
+      auto values_of = [&](uint32_t n, rw4 (&a)[DP / 32]) {
 #pragma unroll
-        for (int i = 0; i < DP / 16; ++i)
-          s[h] = mfma32<T>(*reinterpret_cast<const rw4*>(kt + h * kBlock + (ka ^ (32u * i))), q[i], s[h]);
+        for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const as4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (ACP_LDS as4*)(vt + (va ^ (64u * d)) + (16u * n + 8u * e) * S::kRow));
+            const rw2 x = __builtin_bit_cast(rw2, u);
+            a[d][2 * e] = x[0];
+            a[d][2 * e + 1] = x[1];
+          }
+      };
+      rw4 a[2][DP / 32];
+      {
+        constexpr uint32_t kSteps = DP / 8, kAhead = DP == 256 ? 8 : kSteps;
+        rw4 w[kSteps];
+        auto read = [&](uint32_t n) {
+          return *reinterpret_cast<const rw4*>(kt + n % 2u * kBlock + (ka ^ (32u * (n / 2u))));
+        };
+#pragma unroll
+        for (uint32_t n = 0; n < kAhead; ++n) w[n] = read(n);
+        unroll<kSteps>([&](auto N) {
+          constexpr uint32_t n = decltype(N)::value;
+          if constexpr (n + kAhead < kSteps) w[n + kAhead] = read(n + kAhead);
+          s[n % 2u] = mfma32<T>(w[n], q[n / 2u], s[n % 2u]);
+          if constexpr (n == kSteps / 2u) {
+            values_of(0, a[0]);
+            values_of(1, a[1]);
+          }
+        });
+        asm volatile("" ::: "memory");
       }
       // key of s[h][i]: 32 h + 8 (i / 4) + 4 half + i % 4
       if constexpr (FMT != kCacheSame) {
@@ -388,48 +414,34 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
         }
         unit = __builtin_amdgcn_ldexpf(1.0f, -v_exp);
       }
+      unroll<4>([&](auto N) {
+        constexpr uint32_t n = decltype(N)::value;
+        float p[8];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        rw4 weights[2];
+        for (int i = 0; i < 8; ++i) p[i] = exp2_of(__builtin_fmaf(s[n / 2u][8 * (n & 1u) + i], A.scale, -base));
+        if constexpr (FMT != kCacheSame) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float p[8];
+          for (int i = 0; i < 8; ++i) l += p[i];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) p[i] = exp2_of(__builtin_fmaf(s[h][8 * k + i], A.scale, -base));
-          if constexpr (FMT != kCacheSame) {
+          for (int e = 0; e < 2; ++e) {
+            const af4 x = *reinterpret_cast<const af4*>(&scales[b][1][16u * n + 8 * e + 4 * half]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) l += p[i];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const af4 x = *reinterpret_cast<const af4*>(&scales[b][1][32 * h + 16 * k + 8 * e + 4 * half]);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) p[4 * e + i] = p[4 * e + i] > 0.0f ? p[4 * e + i] * (x[i] * unit) : 0.0f;
-            }
-          }
-          weights[k] = narrow(p, static_cast<const T*>(nullptr));
-          if constexpr (FMT == kCacheSame) {
-            // the sum of the weights as they were rounded
-#pragma unroll
-            for (int i = 0; i < 4; ++i) l = add_pair<T>(weights[k][i], l);
+            for (int i = 0; i < 4; ++i) p[4 * e + i] = p[4 * e + i] > 0.0f ? p[4 * e + i] * (x[i] * unit) : 0.0f;
           }
         }
+        const rw4 weights = narrow(p, static_cast<const T*>(nullptr));
+        if constexpr (FMT == kCacheSame) {
+          // the sum of the weights as they were rounded
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+          for (int i = 0; i < 4; ++i) l = add_pair<T>(weights[i], l);
+        }
 #pragma unroll
-          for (int d = 0; d < DP / 32; ++d) {
-            rw4 a;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const as4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                  (ACP_LDS as4*)(vt + h * kBlock + (va ^ (64u * d)) + (16u * k + 8u * e) * S::kRow));
-              const rw2 x = __builtin_bit_cast(rw2, u);
-              a[2 * e] = x[0];
-              a[2 * e + 1] = x[1];
-            }
-            o[d] = mfma32<T>(a, weights[k], o[d]);
-          }
-      }
+        for (int d = 0; d < DP / 32; ++d) o[d] = mfma32<T>(a[n & 1u][d], weights, o[d]);
+        if constexpr (n < 2u) values_of(n + 2u, a[n & 1u]);
+      });
     }
+    const uint64_t after_here = __builtin_amdgcn_ballot_w64(page >= 0);
+    rows_at(next + S::kKeys, page);
     if constexpr (!DIRECT) {
       if (more) {
         put(b ^ 1u);
