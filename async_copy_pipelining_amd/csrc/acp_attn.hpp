@@ -59,7 +59,11 @@ hipError_t attend_prompt_bf16(int cache, int padded, const AttendArgs& a, hipStr
 
 constexpr int kAttendThreads = 256;
 constexpr int kStepRows = 16;      // rows of a tile of few rows
-constexpr int kPromptRows = 128;   // rows of a tile of many
+// Waves of a tile of many rows, which has 32 rows a wave: eight for 128 channels,
+// which halves what a tile's keys cost in loads (prompts of [2 x 8192 tokens, 32 /
+// 8 heads, 128] 751 us, four waves 767); four for 64, of which a CU holds more than
+// one workgroup (87 us against 96), and for 256, whose registers leave no room.
+constexpr int prompt_waves(int padded) { return padded == 128 ? 8 : 4; }
 constexpr int kStepKeys = 32;      // keys that a wave takes at a time
 constexpr uint32_t kCutStep = 4 * kStepKeys, kCutPrompt = 64;  // cuts lie at multiples
 

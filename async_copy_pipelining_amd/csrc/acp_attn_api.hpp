@@ -6,8 +6,8 @@
 
 namespace {
 
-// Workgroups that the device has room for at a time, by the padded channels: two
-// a CU, one of 256 channels.
+// Workgroups that the device has room for at a time: two a CU; one of 256 channels
+// or of eight waves.
 constexpr int64_t kAttendGroups = 512;
 constexpr int64_t kAttendGroupsWide = 256;
 // From so many times as many tiles on each is a workgroup's; fewer are dealt out
@@ -19,7 +19,7 @@ constexpr int64_t kAttendLeast = 256;
 constexpr int64_t kAttendAlone = 1024;
 // Neighbouring heads in a workgroup, at most 2^k of them.
 constexpr int64_t kAttendSide = 2;
-// Rows of a sequence, on average, from which on tiles of 128 rows are taken.
+// Rows of a sequence, on average, from which on the form for many is taken.
 constexpr int64_t kAttendPrompt = 32;
 
 struct AttendPlan {
@@ -56,7 +56,7 @@ acp_status attend_plan(const acp::DescData& q, const CacheSide& k, const acp_seq
   if (P->tokens == 0 || heads == 0 || sequences == 0) return ACP_OK;
   // rows of a sequence: its tokens' query heads of one of the cache's
   const int64_t rows = b->starts ? P->tokens * group : sequences * group;
-  P->tile_rows = rows >= kAttendPrompt * sequences ? acp::kPromptRows : acp::kStepRows;
+  P->tile_rows = rows >= kAttendPrompt * sequences ? 32 * acp::prompt_waves(P->padded) : acp::kStepRows;
   const int64_t M = P->tile_rows;
   const int64_t slots = b->starts ? P->tokens * group / M + sequences : sequences * ceil_div(group, M);
   if (slots >= kRowLimit) return ret(ACP_ERR_UNSUPPORTED, "2^31 tiles of rows");
@@ -64,7 +64,7 @@ acp_status attend_plan(const acp::DescData& q, const CacheSide& k, const acp_seq
   // the longest that a sequence can be
   int64_t longest = std::min<int64_t>(int64_t(b->max_pages) * k.d.shape[1], (int64_t(1) << 31) - 1);
   if (b->max_length) longest = std::min<int64_t>(longest, b->max_length);
-  const int64_t groups = P->padded == 256 ? kAttendGroupsWide : kAttendGroups;
+  const int64_t groups = P->padded == 256 || M == 256 ? kAttendGroupsWide : kAttendGroups;
   // sequences mostly fill fewer tiles than their slots
   const int64_t tiles = std::max<int64_t>(sequences, b->starts ? P->tokens * group / M : slots);
   // few rows: neighbouring heads, whose rows lie side by side, in the waves of a

@@ -1,13 +1,13 @@
 // Attention of many rows for each of the cache's heads: chunks and prompts.
 // Bound by the matrix instructions and the exponentials.
 //
-// 128 rows a workgroup, 32 a wave, as columns of S^T = K Q^T and O^T = V^T P^T
-// (32x32x16 matrix instructions): a row's scores lie in two lanes, its maximum
-// and its sum need one exchange, and the weights are the second product's
-// operand as they are.  The waves share tiles of keys in LDS, two of them, so
-// that the next one is written while this one is read and there is one barrier
-// a tile.  A tile's rows are loaded a tile ahead into registers, at any
-// alignment, and 8-bit codes become 16-bit values on the way.
+// 32 rows a wave, 128 or 256 a workgroup, as columns of S^T = K Q^T and
+// O^T = V^T P^T (32x32x16 matrix instructions): a row's scores lie in two lanes,
+// its maximum and its sum need one exchange, and the weights are the second
+// product's operand as they are.  The waves share tiles of 64 keys in LDS, two of
+// them, so that the next one comes while this one is read and there is one
+// barrier a tile.  16-bit rows go there straight from memory; 8-bit codes become
+// 16-bit values in registers on the way, as do rows of odd alignment.
 #pragma once
 
 #include "acp_dev_attn.hpp"
@@ -15,14 +15,18 @@
 namespace acp {
 namespace dev {
 
-template <int FMT, int DP>
+template <int FMT, int DP, bool DIRECT, int W>
 struct PromptShape {
+  static constexpr uint32_t kWaves = W;
   static constexpr int kKeys = 64;                    // of a tile, in two blocks of 32
   static constexpr int kRow = DP * 2;
   static constexpr int kPieces = kRow / 16;
   static constexpr int kTile = kKeys * kRow;          // bytes of K or V
   using Piece = std::conditional_t<FMT == kCacheSame, rw4, rw2>;  // 8 channels
-  static constexpr int kRegs = kTile / 16 / kAttendThreads;  // pieces of K or V that a lane brings
+  static constexpr int kRegs = kTile / 16 / (64 * W);  // pieces of K or V that a lane brings
+  // Operands of K, and groups of 16 keys of V, that are read ahead: as many as
+  // registers last for.  More take nothing off the time.
+  static constexpr uint32_t kKAhead = 4, kVAhead = DP == 256 && !DIRECT ? 0 : 1;
 };
 
 // f(integral_constant i) for i = I .. N - 1
@@ -114,11 +118,11 @@ __device__ __forceinline__ void prompt_rows(const AttendArgs& A, const Tile& t, 
 // whole tile is on its way while another is computed.  Pieces past the channels
 // are never written: they were cleared once.  Else (8-bit codes, other
 // alignments) pieces wait in registers.
-template <class T, int FMT, int DP, bool DIRECT>
+template <class T, int FMT, int DP, bool DIRECT, int W>
 __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, const Partial& to, uint32_t begin,
-                                            uint32_t keys, uint32_t kv, char (*lds)[2][PromptShape<FMT, DP>::kTile],
-                                            float (*scales)[2][PromptShape<FMT, DP>::kKeys]) {
-  using S = PromptShape<FMT, DP>;
+                                            uint32_t keys, uint32_t kv, char (*lds)[2][PromptShape<FMT, DP, DIRECT, W>::kTile],
+                                            float (*scales)[2][PromptShape<FMT, DP, DIRECT, W>::kKeys]) {
+  using S = PromptShape<FMT, DP, DIRECT, W>;
   constexpr uint32_t kBlock = 32u * DP * 2u;  // bytes of a block of 32 keys in LDS
   const uint32_t thread = thread_again();
   const uint32_t lane = thread & 63u, wave = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(thread >> 6));
@@ -161,12 +165,12 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
   // of wave w those from (4 i + w) kRowsEach on.  Piece `slot` of a row in LDS is
   // piece kp (vp) of the row in memory: V's is the same for all i.
   constexpr uint32_t kRowsEach = 64u / S::kPieces, kEach = S::kRegs;
-  static_assert(kEach * 4u * kRowsEach == S::kKeys);
+  static_assert(kEach * S::kWaves * kRowsEach == S::kKeys);
   const uint32_t slot = lane % S::kPieces, line = lane / S::kPieces, row_in = wave * kRowsEach + line;
-  static_assert(v_at<DP>(4u * kRowsEach, 0) == 4u * kRowsEach * S::kRow);
+  static_assert(v_at<DP>(S::kWaves * kRowsEach, 0) == S::kWaves * kRowsEach * S::kRow);
   const uint32_t kp0 = (k_at<DP>(row_in, slot) - row_in * S::kRow) / 16u;
   const uint32_t vp = (v_at<DP>(row_in, slot) - row_in * S::kRow) / 16u;
-  auto kp = [&](uint32_t i) { return kp0 ^ (k_at<DP>(i * 4u * kRowsEach, 0) - i * 4u * kRowsEach * S::kRow) / 16u; };
+  auto kp = [&](uint32_t i) { return kp0 ^ (k_at<DP>(i * S::kWaves * kRowsEach, 0) - i * S::kWaves * kRowsEach * S::kRow) / 16u; };
   // Where the rows of the tile after this one lie.  The lanes of a row's pieces
   // need kEach rows each, the same ones: the lanes of a quad work out one row each
   // (two, where there are eight) and pass it on.
@@ -177,7 +181,7 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
   auto rows_at = [&](uint32_t key0, int32_t page) {
 #pragma unroll
     for (uint32_t n = 0; n < kSets; ++n) {
-      const uint32_t j = (n * 4u + (lane & (kOwn - 1u))) * 4u * kRowsEach + row_in, key = key0 + j;
+      const uint32_t j = (n * 4u + (lane & (kOwn - 1u))) * S::kWaves * kRowsEach + row_in, key = key0 + j;
       const uint32_t index = key - divide(key, A.batch.page) * A.batch.page.d;
       const int p = __builtin_amdgcn_ds_bpermute(static_cast<int>(j * 4u), page);
       const uint32_t g = p < 0 ? 0u : static_cast<uint32_t>(p);
@@ -197,20 +201,20 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
     if (here == ~uint64_t(0) && A.dim == DP) {
       unroll<kEach>([&](auto I) {
         constexpr uint32_t i = decltype(I)::value;
-        to_lds(row_of(k_row, I) + kp(i) * 16u, kt + i * 4096u);
-        to_lds(row_of(v_row, I) + vp * 16u, vt + i * 4096u);
+        to_lds(row_of(k_row, I) + kp(i) * 16u, kt + i * S::kWaves * 1024u);
+        to_lds(row_of(v_row, I) + vp * 16u, vt + i * S::kWaves * 1024u);
       });
     } else {
       unroll<kEach>([&](auto I) {
         constexpr uint32_t i = decltype(I)::value;
         const char* kr = row_of(k_row, I) + kp(i) * 16u;
         const char* vr = row_of(v_row, I) + vp * 16u;
-        if (!(here >> (i * 4u * kRowsEach) >> row_in & 1u)) {
-          *reinterpret_cast<rw4*>(lds[b][0] + (i * 4u + wave) * 1024u + lane * 16u) = rw4{0u, 0u, 0u, 0u};
-          *reinterpret_cast<rw4*>(lds[b][1] + (i * 4u + wave) * 1024u + lane * 16u) = rw4{0u, 0u, 0u, 0u};
+        if (!(here >> (i * S::kWaves * kRowsEach) >> row_in & 1u)) {
+          *reinterpret_cast<rw4*>(lds[b][0] + (i * S::kWaves + wave) * 1024u + lane * 16u) = rw4{0u, 0u, 0u, 0u};
+          *reinterpret_cast<rw4*>(lds[b][1] + (i * S::kWaves + wave) * 1024u + lane * 16u) = rw4{0u, 0u, 0u, 0u};
         } else {
-          if (kp(i) * 8u < A.dim) to_lds(kr, kt + i * 4096u);
-          if (vp * 8u < A.dim) to_lds(vr, vt + i * 4096u);
+          if (kp(i) * 8u < A.dim) to_lds(kr, kt + i * S::kWaves * 1024u);
+          if (vp * 8u < A.dim) to_lds(vr, vt + i * S::kWaves * 1024u);
         }
       });
     }
@@ -225,7 +229,7 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
       const char* kr = row_of(k_row, I) + slot * sizeof(P);
       const char* vr = row_of(v_row, I) + slot * sizeof(P);
       kw[i] = vw[i] = P{};
-      if (slot * 8u < A.dim && (here >> (i * 4u * kRowsEach) >> row_in & 1u)) {
+      if (slot * 8u < A.dim && (here >> (i * S::kWaves * kRowsEach) >> row_in & 1u)) {
         kw[i] = *reinterpret_cast<const P_any*>(kr);
         vw[i] = *reinterpret_cast<const P_any*>(vr);
       }
@@ -238,7 +242,7 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
   auto put = [&](uint32_t b) {
 #pragma unroll
     for (uint32_t i = 0; i < kEach; ++i) {
-      const uint32_t j = i * 4u * kRowsEach + row_in;
+      const uint32_t j = i * S::kWaves * kRowsEach + row_in;
       *reinterpret_cast<rw4*>(lds[b][0] + k_at<DP>(j, slot)) = value(kw[i]);
       *reinterpret_cast<rw4*>(lds[b][1] + v_at<DP>(j, slot)) = value(vw[i]);
     }
@@ -279,7 +283,7 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
   if constexpr (DIRECT) {
     if (A.dim != DP) {  // channels that no row has
 #pragma unroll 1
-      for (uint32_t i = thread * 16u; i < 4u * S::kTile; i += kAttendThreads * 16u)
+      for (uint32_t i = thread * 16u; i < 4u * S::kTile; i += S::kWaves * 1024u)
         *reinterpret_cast<rw4*>(lds[0][0] + i) = rw4{0u, 0u, 0u, 0u};
       __syncthreads();
     }
@@ -326,7 +330,7 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[h][i] = 0.0f;
-      // 16 keys' values, read while the scores are computed
+      // 16 keys' values, the first ones read while the scores are computed
       auto values_of = [&](uint32_t n, rw4 (&a)[DP / 32]) {
 #pragma unroll
         for (int d = 0; d < DP / 32; ++d)
@@ -339,9 +343,9 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
             a[d][2 * e + 1] = x[1];
           }
       };
-      rw4 a[2][DP / 32];
+      rw4 a[DP / 32];
       {
-        constexpr uint32_t kSteps = DP / 8, kAhead = DP == 256 ? 8 : kSteps;
+        constexpr uint32_t kSteps = DP / 8, kAhead = S::kKAhead;
         rw4 w[kSteps];
         auto read = [&](uint32_t n) {
           return *reinterpret_cast<const rw4*>(kt + n % 2u * kBlock + (ka ^ (32u * (n / 2u))));
@@ -352,10 +356,7 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
           constexpr uint32_t n = decltype(N)::value;
           if constexpr (n + kAhead < kSteps) w[n + kAhead] = read(n + kAhead);
           s[n % 2u] = mfma32<T>(w[n], q[n / 2u], s[n % 2u]);
-          if constexpr (n == kSteps / 2u) {
-            values_of(0, a[0]);
-            values_of(1, a[1]);
-          }
+          if constexpr (S::kVAhead && n == kSteps / 2u) values_of(0, a);
         });
         asm volatile("" ::: "memory");
       }
@@ -416,6 +417,7 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
       }
       unroll<4>([&](auto N) {
         constexpr uint32_t n = decltype(N)::value;
+        if constexpr (!S::kVAhead) values_of(n, a);
         float p[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) p[i] = exp2_of(__builtin_fmaf(s[n / 2u][8 * (n & 1u) + i], A.scale, -base));
@@ -436,8 +438,8 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
           for (int i = 0; i < 4; ++i) l = add_pair<T>(weights[i], l);
         }
 #pragma unroll
-        for (int d = 0; d < DP / 32; ++d) o[d] = mfma32<T>(a[n & 1u][d], weights, o[d]);
-        if constexpr (n < 2u) values_of(n + 2u, a[n & 1u]);
+        for (int d = 0; d < DP / 32; ++d) o[d] = mfma32<T>(a[d], weights, o[d]);
+        if constexpr (S::kVAhead && n < 3u) values_of(n + 1u, a);
       });
     }
     const uint64_t after_here = __builtin_amdgcn_ballot_w64(page >= 0);
@@ -463,30 +465,30 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
   prompt_rows<T, FMT, DP>(attend_args(), t, to, begin, keys, kv, o, m, l);
 }
 
-template <class T, int FMT, int DP, bool SHARES, bool DIRECT>
-__global__ __launch_bounds__(kAttendThreads, DP == 256 ? 1 : 2) void attend_prompt_kernel(const AttendArgs A) {
-  using S = PromptShape<FMT, DP>;
+template <class T, int FMT, int DP, bool SHARES, bool DIRECT, int W>
+__global__ __launch_bounds__(64 * W, DP == 256 ? 1 : 2) void attend_prompt_kernel(const AttendArgs A) {
+  using S = PromptShape<FMT, DP, DIRECT, W>;
   __shared__ __attribute__((aligned(16))) char lds[2][2][S::kTile];
   __shared__ __attribute__((aligned(16))) float scales[2][2][S::kKeys];
   const AttendPlace at(A);
-  Walk<kPromptRows, kCutPrompt, SHARES> walk;
+  Walk<32 * W, kCutPrompt, SHARES> walk;
   if constexpr (!SHARES) {
     Tile t;
-    if (!t.find<kPromptRows>(A, at.index)) return;
+    if (!t.find<32 * W>(A, at.index)) return;
     walk.cut(A, static_cast<uint32_t>(t.keys));
     const Partial to(A, walk, t, at.kv);
-    prompt_tile<T, FMT, DP, DIRECT>(A, t, to, walk.begin, walk.end, at.kv, lds, scales);
+    prompt_tile<T, FMT, DP, DIRECT, W>(A, t, to, walk.begin, walk.end, at.kv, lds, scales);
   } else {
     __shared__ uint64_t walk_space[kWalkWords];
     if (!walk.begin_at(A, at.index, walk_space)) return;
     bool more;
     do {
       Tile t;
-      if (t.set<kPromptRows>(A, walk.seq, walk.tile)) {
+      if (t.set<32 * W>(A, walk.seq, walk.tile)) {
         walk.cut(A, static_cast<uint32_t>(t.keys));
         const Partial to(A, walk, t, at.kv);
         walk.put(walk_space);
-        prompt_tile<T, FMT, DP, DIRECT>(attend_args(), t, to, walk.begin, walk.end, at.kv, lds, scales);
+        prompt_tile<T, FMT, DP, DIRECT, W>(attend_args(), t, to, walk.begin, walk.end, at.kv, lds, scales);
       }
       __syncthreads();  // the next tile's keys and sums go where this one's were
       walk.take(walk_space);
@@ -496,16 +498,19 @@ __global__ __launch_bounds__(kAttendThreads, DP == 256 ? 1 : 2) void attend_prom
   }
 }
 
+template <class T, int FMT, int DP, bool DIRECT>
+const void* attend_prompt_of(bool shares) {
+  constexpr int W = prompt_waves(DP);
+  return shares ? reinterpret_cast<const void*>(attend_prompt_kernel<T, FMT, DP, true, DIRECT, W>)
+                : reinterpret_cast<const void*>(attend_prompt_kernel<T, FMT, DP, false, DIRECT, W>);
+}
 template <class T>
 hipError_t attend_prompt_for(int cache, int padded, const AttendArgs& a, hipStream_t s) {
   const void* f = nullptr;
-#define ACP_PROMPT(FMT, DP)                                                                                    \
-  if (cache == FMT && padded == DP)                                                                            \
-    f = FMT == kCacheSame && a.direct                                                                          \
-            ? (a.shares ? reinterpret_cast<const void*>(attend_prompt_kernel<T, kCacheSame, DP, true, true>)   \
-                        : reinterpret_cast<const void*>(attend_prompt_kernel<T, kCacheSame, DP, false, true>)) \
-            : (a.shares ? reinterpret_cast<const void*>(attend_prompt_kernel<T, FMT, DP, true, false>)         \
-                        : reinterpret_cast<const void*>(attend_prompt_kernel<T, FMT, DP, false, false>))
+#define ACP_PROMPT(FMT, DP)                                                        \
+  if (cache == FMT && padded == DP)                                                \
+  f = FMT == kCacheSame && a.direct ? attend_prompt_of<T, kCacheSame, DP, true>(a.shares) \
+                                    : attend_prompt_of<T, FMT, DP, false>(a.shares)
   ACP_PROMPT(kCacheSame, 64);
   ACP_PROMPT(kCacheSame, 128);
   ACP_PROMPT(kCacheSame, 256);
@@ -519,7 +524,7 @@ hipError_t attend_prompt_for(int cache, int padded, const AttendArgs& a, hipStre
   if (f == nullptr) return hipErrorInvalidValue;
   AttendArgs copy = a;
   void* args[] = {&copy};
-  return hipLaunchKernel(f, dim3(attend_grid(a)), dim3(kAttendThreads), args, 0, s);
+  return hipLaunchKernel(f, dim3(attend_grid(a)), dim3(64 * prompt_waves(padded)), args, 0, s);
 }
 
 }  // namespace dev

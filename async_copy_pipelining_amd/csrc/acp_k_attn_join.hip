@@ -112,11 +112,16 @@ hipError_t attend_prompt_launch(int dt, int cache, int padded, const AttendArgs&
 
 hipError_t attend_join_launch(int dt, int tile_rows, const AttendArgs& a, const JoinShape& k, hipStream_t s) {
   using namespace dev;
-  const bool few = tile_rows == kStepRows;
-  const void* f = dt == kRowF16 ? (few ? reinterpret_cast<const void*>(attend_join_kernel<_Float16, kStepRows>)
-                                       : reinterpret_cast<const void*>(attend_join_kernel<_Float16, kPromptRows>))
-                                : (few ? reinterpret_cast<const void*>(attend_join_kernel<bf16_t, kStepRows>)
-                                       : reinterpret_cast<const void*>(attend_join_kernel<bf16_t, kPromptRows>));
+  const void* f = nullptr;
+#define ACP_JOIN(M)                                                                          \
+  if (tile_rows == M)                                                                        \
+  f = dt == kRowF16 ? reinterpret_cast<const void*>(attend_join_kernel<_Float16, M>)         \
+                    : reinterpret_cast<const void*>(attend_join_kernel<bf16_t, M>)
+  ACP_JOIN(kStepRows);
+  ACP_JOIN(128);
+  ACP_JOIN(256);
+#undef ACP_JOIN
+  if (f == nullptr) return hipErrorInvalidValue;
   AttendArgs copy = a;
   JoinShape shape = k;
   void* args[] = {&copy, &shape.lanes_log2, &shape.shares_log2, &shape.blocks};
