@@ -220,7 +220,7 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
     }
   };
   // not DIRECT: the lane's pieces of a tile
-  typename S::Piece kw[DIRECT ? 1 : S::kRegs], vw[DIRECT ? 1 : S::kRegs];
+  typename S::Piece kw[S::kRegs], vw[S::kRegs];
   auto load = [&](uint64_t here) {
     using P = typename S::Piece;
     typedef P P_any __attribute__((aligned(1)));

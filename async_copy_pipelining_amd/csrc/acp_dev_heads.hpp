@@ -14,30 +14,36 @@ typedef hf4 hf4_any __attribute__((aligned(4)));
 
 // A lane's two chunks of every row: first channel and channels of each.
 // Turned units come first.  Halves: V channels of the first half and those
-// they are paired with, half the turned channels further; pairs, and channels
-// that are not turned: 2 V neighbours.
+// they are paired with, half the turned channels further.  Pairs, and channels
+// that are not turned, whose chunks have no need of each other: lanes that are
+// neighbours have chunks that are, so that a load or store of the wave has whole
+// runs of a row (2 V neighbours a lane, every other 16 bytes at a time: [20480 new
+// tokens, 32 + 8 + 8 heads, 128] bfloat16 appended in 145 us, so in 110).
 template <class T, bool PAIRS>
 struct Unit {
   int at[2], n[2];
   bool turned;
-  uint32_t first;  // index of its first frequency
+  uint32_t first[2];  // its frequencies: V / 2 from each of these on
 
   __device__ __forceinline__ Unit(const HeadsCore& A, uint32_t u) {
     constexpr int V = kChunk<T>;
-    const int half = static_cast<int>(A.rotated / 2);
+    const int half = static_cast<int>(A.rotated / 2), k = static_cast<int>(u < A.turn_units ? u : u - A.turn_units);
     turned = u < A.turn_units;
-    first = u * V;
-    const int from = turned ? 0 : static_cast<int>(A.rotated), to = turned ? static_cast<int>(A.rotated) : static_cast<int>(A.dim);
-    const int k = static_cast<int>(turned ? u : u - A.turn_units);
     if (!PAIRS && turned) {
       at[0] = k * V;
       at[1] = half + k * V;
       n[0] = n[1] = within(half - k * V);
+      first[0] = u * V;
+      first[1] = u * V + V / 2;
     } else {
-      at[0] = from + 2 * k * V;
-      at[1] = at[0] + V;
+      const int from = turned ? 0 : static_cast<int>(A.rotated), to = static_cast<int>(turned ? A.rotated : A.dim);
+      const int further = static_cast<int>(turned ? A.turn_units : A.units - A.turn_units) * V;
+      at[0] = from + k * V;
+      at[1] = at[0] + further;
       n[0] = within(to - at[0]);
       n[1] = within(to - at[1]);
+      first[0] = static_cast<uint32_t>(at[0]) / 2;
+      first[1] = static_cast<uint32_t>(at[1]) / 2;
     }
     if (u >= A.units) n[0] = n[1] = 0;
   }
@@ -78,24 +84,25 @@ struct Waves {
     s[i] = (k & 2 ? -scale : scale) * sign * sk;
   }
 
-  template <bool WHOLE>
-  __device__ __forceinline__ void at(const HeadsCore& A, uint32_t first, bool turned, int32_t position) {
+  template <bool WHOLE, class U>
+  __device__ __forceinline__ void at(const HeadsCore& A, const U& u, int32_t position) {
     constexpr double kTurn = 0.15915494309189533577;  // 1 / 2 pi
     double f[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) f[i] = 0.0;
-    if (turned) {
+    auto index = [&](int i) { return u.first[i / (V / 2)] + i % (V / 2); };
+    if (u.turned) {
       if constexpr (WHOLE) {
 #pragma unroll
         for (int i = 0; i < V; i += 2) {
-          const hd2 w = *reinterpret_cast<const hd2_any*>(A.frequencies + first + i);
+          const hd2 w = *reinterpret_cast<const hd2_any*>(A.frequencies + index(i));
           f[i] = w[0];
           f[i + 1] = w[1];
         }
       } else {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          if (first + i < A.rotated / 2) f[i] = A.frequencies[first + i];
+          if (index(i) < A.rotated / 2) f[i] = A.frequencies[index(i)];
       }
     }
 #pragma unroll
@@ -153,6 +160,26 @@ struct Piece {
                            narrow(a, static_cast<const T*>(nullptr)));
     store_chunk<T, !WHOLE>(row + u.at[1] * static_cast<int>(sizeof(T)), there ? u.n[1] : 0,
                            narrow(b, static_cast<const T*>(nullptr)));
+  }
+};
+
+// The lane's units of U passes over the heads.  A kernel loads the first ones of
+// every tensor before it looks for positions and pages and forms angles: neither
+// waits for the other.
+template <class T, bool PAIRS, bool WHOLE, int U>
+struct Passes {
+  Piece<T, PAIRS, WHOLE> piece[U];
+
+  static __device__ __forceinline__ uint32_t head(const HeadsCore& A, uint32_t pass, uint32_t slot) {
+    return (pass << A.heads_log2) + slot;
+  }
+  __device__ __forceinline__ void load(const HeadsCore& A, const char* x, int64_t x_head, const Unit<T, PAIRS>& u,
+                                       uint32_t heads, uint32_t slot, uint32_t from, uint32_t to) {
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const uint32_t h = head(A, from + k, slot);
+      piece[k].load(x + h * x_head, u, from + k < to && h < heads);
+    }
   }
 };
 

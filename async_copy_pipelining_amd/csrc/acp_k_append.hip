@@ -10,40 +10,37 @@
 namespace acp {
 namespace dev {
 
-constexpr int kPassesInFlight = 4;
+// Passes in flight: of the queries, which mostly have several times the heads,
+// and of keys and of values.
+constexpr int kPassesQ = 4, kPassesKV = 2;
 
-// Where a pass's rows go: an output tensor, or a cache's page.
-template <class T, bool PAIRS, bool WHOLE, bool PACK, bool TURN>
-__device__ __forceinline__ void rows_through(const HeadsCore& A, const char* x, int64_t x_head, char* y, int64_t y_head,
-                                             float* scales, int format, uint32_t heads, uint32_t slot,
-                                             const Unit<T, PAIRS>& u, const Waves<kChunk<T>>& w, uint32_t from,
-                                             uint32_t to) {
-  constexpr int V = kChunk<T>, U = kPassesInFlight;
+// Passes [from, to) of a tensor, of which the first U are loaded.  y: an output's
+// row of the token, or a page's.
+template <class T, bool PAIRS, bool WHOLE, bool PACK, bool TURN, int U>
+__device__ __forceinline__ void rows_through(const HeadsCore& A, Passes<T, PAIRS, WHOLE, U>& in, const char* x,
+                                             int64_t x_head, char* y, int64_t y_head, float* scales, int format,
+                                             uint32_t heads, uint32_t slot, const Unit<T, PAIRS>& u,
+                                             const Waves<kChunk<T>>& w, uint32_t from, uint32_t to) {
+  constexpr int V = kChunk<T>;
   for (uint32_t p = from; p < to; p += U) {
-    Piece<T, PAIRS, WHOLE> piece[U];
-    uint32_t head[U];
-    bool there[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      head[k] = ((p + k) << A.heads_log2) + slot;
-      there[k] = p + k < to && head[k] < heads;
-      piece[k].load(x + head[k] * x_head, u, there[k]);
-    }
+    if (p != from) in.load(A, x, x_head, u, heads, slot, p, to);
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       if (p + k >= to) break;
+      const uint32_t head = in.head(A, p + k, slot);
+      const bool there = head < heads;
+      Piece<T, PAIRS, WHOLE>& piece = in.piece[k];
       if constexpr (!TURN && !PACK && WHOLE) {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          store_chunk<T, false>(y + head[k] * y_head + u.at[j] * static_cast<int>(sizeof(T)), there[k] ? u.n[j] : 0,
-                                piece[k].raw[j]);
+          store_chunk<T, false>(y + head * y_head + u.at[j] * static_cast<int>(sizeof(T)), there ? u.n[j] : 0, piece.raw[j]);
         continue;
       }
       float a[V], b[V];
-      piece[k].values(u, there[k], a, b);
+      piece.values(u, there, a, b);
       if constexpr (TURN) turn<PAIRS>(a, b, w, u.turned);
       if constexpr (!PACK) {
-        piece[k].store(y + head[k] * y_head, u, there[k], a, b);
+        piece.store(y + head * y_head, u, there, a, b);
       } else {
         uint32_t m = 0;
 #pragma unroll
@@ -56,10 +53,10 @@ __device__ __forceinline__ void rows_through(const HeadsCore& A, const char* x, 
             over_lanes(static_cast<int>(m), A.lanes_log2, [](int c, int d) { return c > d ? c : d; }));
         const float s = block_scale(format, m);
         const Codes<V> ca = encode<T, V>(format, a, s), cb = encode<T, V>(format, b, s);
-        char* row = y + head[k] * y_head;
-        store_codes<V, !WHOLE>(row + u.at[0], there[k] ? u.n[0] : 0, ca);
-        store_codes<V, !WHOLE>(row + u.at[1], there[k] ? u.n[1] : 0, cb);
-        if (there[k] && u.at[0] == 0 && u.n[0] > 0) scales[head[k]] = s;
+        char* row = y + head * y_head;
+        store_codes<V, !WHOLE>(row + u.at[0], there ? u.n[0] : 0, ca);
+        store_codes<V, !WHOLE>(row + u.at[1], there ? u.n[1] : 0, cb);
+        if (there && u.at[0] == 0 && u.n[0] > 0) scales[head] = s;
       }
     }
   }
@@ -72,6 +69,18 @@ __global__ __launch_bounds__(kHeadThreads) void append_kernel(const AppendArgs A
   const HeadPlace at(A, wave);  // a wave has one token: at.group
   const uint32_t token = at.group;
   const Unit<T, PAIRS> u(A, at.unit);
+  // the wave's passes of q, k and v, which follow one another
+  const uint32_t first = at.pass, last = first + A.per_wave, k0 = A.q.passes, v0 = k0 + A.k.passes;
+  auto within = [](uint32_t p, uint32_t from, uint32_t n) { return p < from ? 0u : p - from < n ? p - from : n; };
+  const uint32_t q_from = within(first, 0, A.q.passes), q_to = within(last, 0, A.q.passes);
+  const uint32_t k_from = within(first, k0, A.k.passes), k_to = within(last, k0, A.k.passes);
+  const uint32_t v_from = within(first, v0, A.v.passes), v_to = within(last, v0, A.v.passes);
+  const char *xq = token_row(A, A.q.x, token), *xk = token_row(A, A.k.x, token), *xv = token_row(A, A.v.x, token);
+  Passes<T, PAIRS, WHOLE, kPassesQ> q;
+  Passes<T, PAIRS, WHOLE, kPassesKV> k, v;
+  q.load(A, xq, A.q.x.s[2], u, A.q.heads, at.slot, q_from, q_to);
+  k.load(A, xk, A.k.x.s[2], u, A.k.heads, at.slot, k_from, k_to);
+  v.load(A, xv, A.v.x.s[2], u, A.v.heads, at.slot, v_from, v_to);
   const uint32_t seq = sequence_of(A.batch, token);
   if (seq >= A.batch.sequences) return;
   int32_t behind = 1;  // tokens of the sequence from this one on
@@ -80,45 +89,40 @@ __global__ __launch_bounds__(kHeadThreads) void append_kernel(const AppendArgs A
     behind = A.batch.starts[seq + 1u] - static_cast<int32_t>(token);
   }
   const int32_t position = A.batch.lengths[seq] - behind;
-  uint32_t from = at.pass, to = from + A.per_wave;
-  Waves<kChunk<T>> w;
-  if (A.rotated && from < A.q.passes + A.k.passes) w.template at<WHOLE>(A, u.first, u.turned, position);
-  const uint32_t q_end = to < A.q.passes ? to : A.q.passes;
-  if (from < q_end) {
-    if (A.rotated)
-      rows_through<T, PAIRS, WHOLE, false, true>(A, token_row(A, A.q.x, token), A.q.x.s[2], token_row(A, A.q.y, token),
-                                                 A.q.y.s[2], nullptr, 0, A.q.heads, at.slot, u, w, from, q_end);
-    else
-      rows_through<T, PAIRS, WHOLE, false, false>(A, token_row(A, A.q.x, token), A.q.x.s[2], token_row(A, A.q.y, token),
-                                                  A.q.y.s[2], nullptr, 0, A.q.heads, at.slot, u, w, from, q_end);
+  int32_t page = -1;
+  uint32_t slot = 0;
+  if (position >= 0) {
+    const uint32_t index = divide(static_cast<uint32_t>(position), A.batch.page);
+    slot = static_cast<uint32_t>(position) - index * A.batch.page.d;
+    page = page_of(A.batch, seq, index);
   }
-  from = from > A.q.passes ? from - A.q.passes : 0u;
-  to = to > A.q.passes ? to - A.q.passes : 0u;
-  if (to == 0 || position < 0) return;
-  const uint32_t index = divide(static_cast<uint32_t>(position), A.batch.page);
-  const int32_t page = page_of(A.batch, seq, index);
+  Waves<kChunk<T>> w;
+  if (A.rotated && first < v0) w.template at<WHOLE>(A, u, position);
+  if (q_from < q_to) {
+    char* y = token_row(A, A.q.y, token);
+    if (A.rotated)
+      rows_through<T, PAIRS, WHOLE, false, true>(A, q, xq, A.q.x.s[2], y, A.q.y.s[2], nullptr, 0, A.q.heads, at.slot, u, w,
+                                                 q_from, q_to);
+    else
+      rows_through<T, PAIRS, WHOLE, false, false>(A, q, xq, A.q.x.s[2], y, A.q.y.s[2], nullptr, 0, A.q.heads, at.slot, u,
+                                                  w, q_from, q_to);
+  }
   if (page < 0) return;
-  const uint32_t slot = static_cast<uint32_t>(position) - index * A.batch.page.d;
   const uint64_t row = static_cast<uint64_t>(page) * A.batch.page.d + slot;
-  const uint32_t k_end = to < A.k.passes ? to : A.k.passes;
-  if (from < k_end) {
+  if (k_from < k_to) {
     char* y = A.ck.p + page * A.ck.s[0] + slot * A.ck.s[1];
     float* scales = PACK ? A.ck.scales + row * A.k.heads : nullptr;
     if (A.rotated)
-      rows_through<T, PAIRS, WHOLE, PACK, true>(A, token_row(A, A.k.x, token), A.k.x.s[2], y, A.ck.s[2], scales,
-                                                A.format, A.k.heads, at.slot, u, w, from, k_end);
+      rows_through<T, PAIRS, WHOLE, PACK, true>(A, k, xk, A.k.x.s[2], y, A.ck.s[2], scales, A.format, A.k.heads, at.slot,
+                                                u, w, k_from, k_to);
     else
-      rows_through<T, PAIRS, WHOLE, PACK, false>(A, token_row(A, A.k.x, token), A.k.x.s[2], y, A.ck.s[2], scales,
-                                                 A.format, A.k.heads, at.slot, u, w, from, k_end);
+      rows_through<T, PAIRS, WHOLE, PACK, false>(A, k, xk, A.k.x.s[2], y, A.ck.s[2], scales, A.format, A.k.heads, at.slot,
+                                                 u, w, k_from, k_to);
   }
-  from = from > A.k.passes ? from - A.k.passes : 0u;
-  to = to > A.k.passes ? to - A.k.passes : 0u;
-  const uint32_t v_end = to < A.v.passes ? to : A.v.passes;
-  if (from < v_end)
-    rows_through<T, PAIRS, WHOLE, PACK, false>(A, token_row(A, A.v.x, token), A.v.x.s[2],
-                                               A.cv.p + page * A.cv.s[0] + slot * A.cv.s[1], A.cv.s[2],
-                                               PACK ? A.cv.scales + row * A.v.heads : nullptr, A.format, A.v.heads,
-                                               at.slot, u, w, from, v_end);
+  if (v_from < v_to)
+    rows_through<T, PAIRS, WHOLE, PACK, false>(A, v, xv, A.v.x.s[2], A.cv.p + page * A.cv.s[0] + slot * A.cv.s[1],
+                                               A.cv.s[2], PACK ? A.cv.scales + row * A.v.heads : nullptr, A.format,
+                                               A.v.heads, at.slot, u, w, v_from, v_to);
 }
 
 }  // namespace dev

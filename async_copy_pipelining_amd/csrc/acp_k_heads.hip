@@ -7,14 +7,16 @@
 namespace acp {
 namespace dev {
 
-constexpr int kPassesInFlight = 4;
+// Passes in flight of queries, which mostly have several times the heads, and of keys.
+constexpr int kPassesQ = 4, kPassesK = 2;
 
-// The passes [from, to) of one side of a wave's tokens.
-template <class T, bool PAIRS, bool WHOLE, bool NORM>
-__device__ __forceinline__ void side_forward(const HeadsCore& A, const HeadSide& S, const HeadPlace& at,
-                                             const Unit<T, PAIRS>& u, const Waves<kChunk<T>>& w, uint32_t from,
-                                             uint32_t to) {
-  constexpr int V = kChunk<T>, U = kPassesInFlight;
+// The passes [from, to) of one side of a wave's tokens, the first U of them loaded.
+template <class T, bool PAIRS, bool WHOLE, bool NORM, int U>
+__device__ __forceinline__ void side_forward(const HeadsCore& A, const HeadSide& S, Passes<T, PAIRS, WHOLE, U>& in,
+                                             const HeadPlace& at, const Unit<T, PAIRS>& u, const Waves<kChunk<T>>& w,
+                                             uint32_t from, uint32_t to) {
+  constexpr int V = kChunk<T>;
+  if (from >= to) return;
   const bool real = at.token < A.tokens;
   const uint32_t token = real ? at.token : 0u;
   const char* x = token_row(A, S.x, token);
@@ -22,20 +24,14 @@ __device__ __forceinline__ void side_forward(const HeadsCore& A, const HeadSide&
   float wa[V], wb[V];
   if constexpr (NORM) load_weight<T, PAIRS, WHOLE>(S.weight, u, wa, wb);
   for (uint32_t p = from; p < to; p += U) {
-    Piece<T, PAIRS, WHOLE> piece[U];
-    uint32_t head[U];
-    bool there[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      head[k] = ((p + k) << A.heads_log2) + at.slot;
-      there[k] = real && p + k < to && head[k] < S.heads;
-      piece[k].load(x + head[k] * S.x.s[2], u, there[k]);
-    }
+    if (p != from) in.load(A, x, S.x.s[2], u, real ? S.heads : 0u, at.slot, p, to);
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       if (p + k >= to) break;
+      const uint32_t head = in.head(A, p + k, at.slot);
+      const bool there = real && head < S.heads;
       float a[V], b[V];
-      piece[k].values(u, there[k], a, b);
+      in.piece[k].values(u, there, a, b);
       if constexpr (NORM) {
         float sum = 0.0f;
 #pragma unroll
@@ -48,7 +44,7 @@ __device__ __forceinline__ void side_forward(const HeadsCore& A, const HeadSide&
         }
       }
       turn<PAIRS>(a, b, w, u.turned);
-      piece[k].store(y + head[k] * S.y.s[2], u, there[k], a, b);
+      in.piece[k].store(y + head * S.y.s[2], u, there, a, b);
     }
   }
 }
@@ -59,23 +55,28 @@ __global__ __launch_bounds__(kHeadThreads) void heads_forward_kernel(const Heads
   if (wave >= A.groups * A.parts.d) return;
   const HeadPlace at(A, wave);
   const Unit<T, PAIRS> u(A, at.unit);
+  const bool real = at.token < A.tokens;
+  const uint32_t token = real ? at.token : 0u;
+  // the wave's passes of queries and keys, which follow one another
+  const HeadSide &Q = A.side[0], &K = A.side[1];
+  const uint32_t first = at.pass, last = first + A.per_wave;
+  const uint32_t q_to = last < Q.passes ? last : Q.passes;
+  const uint32_t k_from = first > Q.passes ? first - Q.passes : 0u, k_last = last > Q.passes ? last - Q.passes : 0u;
+  const uint32_t k_to = k_last < K.passes ? k_last : K.passes;
+  Passes<T, PAIRS, WHOLE, kPassesQ> q;
+  Passes<T, PAIRS, WHOLE, kPassesK> k;
+  q.load(A, token_row(A, Q.x, token), Q.x.s[2], u, real ? Q.heads : 0u, at.slot, first, q_to);
+  k.load(A, token_row(A, K.x, token), K.x.s[2], u, real ? K.heads : 0u, at.slot, k_from, k_to);
   Waves<kChunk<T>> w;
   if (A.rotated) {
     int32_t position = 0;
-    if (at.token < A.tokens)
+    if (real)
       position = A.positions ? A.positions[at.token]
                              : static_cast<int32_t>(at.token - divide(at.token, A.span) * A.span.d);
-    w.template at<WHOLE>(A, u.first, u.turned, position);
+    w.template at<WHOLE>(A, u, position);
   }
-  uint32_t from = at.pass, to = from + A.per_wave;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const HeadSide& S = A.side[k];
-    const uint32_t end = to < S.passes ? to : S.passes;
-    if (from < end) side_forward<T, PAIRS, WHOLE, NORM>(A, S, at, u, w, from, end);
-    from = from > S.passes ? from - S.passes : 0u;
-    to = to > S.passes ? to - S.passes : 0u;
-  }
+  side_forward<T, PAIRS, WHOLE, NORM>(A, Q, q, at, u, w, first, q_to);
+  side_forward<T, PAIRS, WHOLE, NORM>(A, K, k, at, u, w, k_from, k_to);
 }
 
 }  // namespace dev

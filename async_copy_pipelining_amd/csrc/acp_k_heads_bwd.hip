@@ -84,7 +84,7 @@ __global__ __launch_bounds__(kHeadThreads) void heads_backward_kernel(const Head
       if (at.token < A.tokens)
         position = A.positions ? A.positions[at.token]
                                : static_cast<int32_t>(at.token - divide(at.token, A.span) * A.span.d);
-      w.template at<WHOLE>(A, u.first, u.turned, position);
+      w.template at<WHOLE>(A, u, position);
     }
     uint32_t from = at.pass, to = from + A.per_wave;
 #pragma unroll
