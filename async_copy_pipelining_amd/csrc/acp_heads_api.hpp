@@ -8,7 +8,7 @@ namespace {
 
 // Waves that a launch aims at before it gives a wave more than one pass: four
 // for each of 256 CUs.
-constexpr int64_t kHeadWaves = 1024;
+constexpr int64_t kHeadWaves = 4096;
 // Passes of a wave over its tokens' heads, which share one set of angles.
 constexpr int64_t kHeadPasses = 8;
 // Workgroups of a backward pass: each leaves 8 bytes a channel.
