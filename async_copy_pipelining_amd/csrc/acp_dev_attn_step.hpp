@@ -34,7 +34,9 @@ struct StepShape {
   // the waves' sums meet there afterwards, 128 channels at a time
   static constexpr int kJoinPitch = 132;
   static constexpr int kJoinBytes = 4 * kStepRows * kJoinPitch * 4;
-  static constexpr int kLds = 4 * kWaveBytes > kJoinBytes ? 4 * kWaveBytes : kJoinBytes;
+  // 8-bit rows: the scales of a wave's keys, behind all waves' rows
+  static constexpr int kScaleBytes = FMT == kCacheSame ? 0 : 2 * kStepKeys * 4;
+  static constexpr int kLds = 4 * (kWaveBytes + kScaleBytes) > kJoinBytes ? 4 * (kWaveBytes + kScaleBytes) : kJoinBytes;
 };
 
 // Where piece c of row r lies in a wave's rows of V.  A transposing read takes
@@ -179,6 +181,7 @@ __device__ __forceinline__ void step_tile(const AttendArgs& A, const Tile& t, co
   const uint32_t kv = kv0 + (wave & (side - 1u));
   const bool exact = A.dim == DP;
   char* mine = lds + wave * S::kWaveBytes;
+  float* my_scales = reinterpret_cast<float*>(lds + 4 * S::kWaveBytes + wave * S::kScaleBytes);
 
   // the lane's row, and its part of Q: channel order as K's pieces have it
   const uint32_t row = t.first + col;
@@ -306,6 +309,7 @@ __device__ __forceinline__ void step_tile(const AttendArgs& A, const Tile& t, co
     entry = entry_at(next + stride);
     const bool more = next < keys;
 
+    if constexpr (FMT != kCacheSame) my_scales[lane] = lane < 32u ? r.ks : r.vs;
     af4 s[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -321,17 +325,25 @@ __device__ __forceinline__ void step_tile(const AttendArgs& A, const Tile& t, co
 
     // scores in powers of two, and what is hidden
     float x[8], ws[8];
+    if constexpr (FMT != kCacheSame) {
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h) {
+      if constexpr (FMT == kCacheSame) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[4 * h + i] = s[h][i] * A.scale;
-        if constexpr (FMT != kCacheSame) {
-          const int src = static_cast<int>((16u * h + 4u * quarter + i) * 4u);
-          x[4 * h + i] *= as_float(static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(src, static_cast<int>(as_bits(r.ks)))));
-          ws[4 * h + i] = as_float(static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(src, static_cast<int>(as_bits(r.vs)))));
+        for (int i = 0; i < 4; ++i) x[4 * h + i] = s[h][i] * A.scale;
+      } else {
+        const af4 k = *reinterpret_cast<const af4*>(my_scales + 16u * h + 4u * quarter);
+        const af4 v = *reinterpret_cast<const af4*>(my_scales + 32u + 16u * h + 4u * quarter);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[4 * h + i] = s[h][i] * A.scale * k[i];
+          ws[4 * h + i] = v[i];
         }
       }
+    }
     if (r.here != 0xFFFFFFFFu || static_cast<int32_t>(now + kStepKeys - 1u) > t.low) {
       // both in the lane's own terms, so that the bit and the bound are constants
       const int32_t left = sees - static_cast<int32_t>(now + 4u * quarter);
