@@ -96,7 +96,8 @@ acp_status attend_plan(const acp::DescData& q, const CacheSide& k, const acp_seq
     P->join.blocks = div_by(static_cast<uint64_t>(blocks));
     grid = std::max(grid, heads_each * slots * blocks);
   }
-  if (grid >= int64_t(1) << 24) return ret(ACP_ERR_UNSUPPORTED, "a launch of 2^32 lanes");
+  const int64_t threads = M == acp::kStepRows ? acp::kAttendThreads : 64 * acp::prompt_waves(P->padded);
+  if (grid * threads >= int64_t(1) << 32) return ret(ACP_ERR_UNSUPPORTED, "a launch of 2^32 lanes");
   return ACP_OK;
 }
 

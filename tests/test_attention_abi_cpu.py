@@ -76,3 +76,9 @@ def test_workspace():
     assert size(1 << 16, 4, 4096) == 0
     refused(lambda: acp.acp_cache_attention_workspace(desc(1, Q), None, pages_of()), INVALID, "no cache")
     refused(lambda: acp.acp_cache_attention_workspace(desc(1, Q), cache_of(), None), INVALID, "no sequences")
+
+
+def test_launches_of_wide_workgroups():
+    """Tiles of 128 channels have 512 lanes: as many of them are half as many lanes too many."""
+    assert size(1 << 25, 1 << 22, 1, dim=64) == 0
+    refused(lambda: size(1 << 25, 1 << 22, 1), UNSUPPORTED, "2^32 lanes")
