@@ -1,0 +1,39 @@
+"""Attention over paged caches on the GPU where tiles of rows and of keys end:
+counts next to their sizes, pages that end inside a wave's rows, rows of every
+alignment, few heads and many."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+from tests.test_gpu_cache_attention import TYPES, check, say  # noqa: E402
+
+# new tokens, lengths, page, heads, kv heads, channels
+TILES = [
+    ((256,), (256,), 3, 1, 1, 128), ((64,), (64,), 64, 4, 1, 128), ((65, 63), (128, 65), 7, 4, 1, 72),
+    ((300,), (301,), 24, 3, 1, 112), ((257,), (600,), 1, 2, 2, 128), ((40, 1, 0, 90), (700, 700, 3, 90), 2, 8, 1, 104),
+    ((127, 129), (127, 193), 96, 2, 1, 128), ((129,), (129,), 5, 2, 1, 56), ((128, 64), (192, 64), 10, 3, 3, 64),
+    ((70,), (190,), 6, 2, 1, 200), ((128,), (128,), 33, 1, 1, 256),
+]
+
+
+@pytest.mark.parametrize("gap", [0, 8, 3])
+@pytest.mark.parametrize("fmt", [None, "i8", "e4m3"])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_tiles(dtype, fmt, gap):
+    for n, (news, lengths, page, heads, kv, dim) in enumerate(TILES):
+        say(f"tiles {dtype} {fmt} {gap} {news} {lengths} {page} {heads}/{kv} {dim}")
+        check(news, lengths, page, heads, kv, dim, dtype, fmt, ((0, 1, 2, 3), (0, 2, 1, 3), (2, 0, 1, 3))[n % 3], gap, n,
+              form="many rows" if sum(news) * heads // kv >= 64 * len(news) else None, before=n % 2)
+
+
+@pytest.mark.parametrize("fmt", [None, "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_shares_of_many_rows(dtype, dim, fmt):
+    """Long contexts under chunks: shares that begin and end inside tiles, tiles of several shares."""
+    for n, (news, lengths, page) in enumerate((((33,), (4097,), 48), ((100, 40, 64), (3000, 40, 1500), 5), ((64, 64), (64, 2111), 16))):
+        say(f"shares {dtype} {fmt} {dim} {news} {lengths}")
+        ran = check(news, lengths, page, 8, 2, dim, dtype, fmt, seed=n, form="many rows")
+        assert "shares 0" not in ran, ran

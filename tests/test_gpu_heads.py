@@ -309,3 +309,26 @@ def test_the_same_call_gives_the_same_bits():
         torch.cuda.synchronize()
         got.append((dx.t.clone(), dw))
     assert all(torch.equal(a, got[0][0]) and torch.equal(b, got[0][1]) for a, b in got[1:])
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_pairs_and_rests_of_any_number_of_chunks(dtype):
+    """Chunks of 16 bytes of the turned channels and of the others: odd numbers of them, the last one not full."""
+    for n, (dim, rot) in enumerate(((24, 24), (24, 8), (40, 24), (56, 40), (72, 24), (88, 88), (66, 26), (12, 10), (120, 4), (30, 0))):
+        say(f"chunks {dtype} {dim} {rot}")
+        tokens = 50 + n
+        freq, pos = H.frequencies(rot or 2), places(tokens, n)
+        r = rotary(freq, rot, "pairs") if rot else None
+        x = [Field((tokens, h, dim), dtype, None, n % 3, np.random.default_rng(n + h).standard_normal((tokens, h, dim)))
+             for h in (5, 2)]
+        y = [Field(f.t.shape, dtype, None, (n + 1) % 3) for f in x]
+        w = np.random.default_rng(n).uniform(0.5, 1.5, dim).astype(np.float32)
+        acp.acp_head_norm(y[0].desc, x[0].desc, torch.tensor(w, device=DEV), y[1].desc, x[1].desc, None, 1e-5, ints(pos), r,
+                          torch.cuda.current_stream())
+        torch.cuda.synchronize()
+        for f, g, v in zip(x, y, (w, None)):
+            normed = H.head_norm(f.values(), v, 1e-5)
+            want = H.rotate(normed, pos, freq, rot, "pairs") if rot else normed
+            bound = H.pair_sum(normed, rot, "pairs") * (norm_relative(dim) + (WAVE + 4 * U)) + out_step(dtype, want)
+            close(g.values(), want, bound, (dim, rot))
+            assert g.untouched()
