@@ -10,17 +10,26 @@ namespace {
 // or of eight waves.
 constexpr int64_t kAttendGroups = 512;
 constexpr int64_t kAttendGroupsWide = 256;
-// From so many times as many tiles on each is a workgroup's; fewer are dealt out
-// evenly.
-constexpr int64_t kAttendTiles = 1;
-// Keys of a share, at least.
+// Fewer tiles than workgroups are dealt out evenly; others are a workgroup's each:
+// shares begin inside tiles, so that neighbours no longer read the same keys at
+// the same time ([2 x 4096, 16 heads, 64] as 848 tiles: 89 us, in shares 109).
+// Keys of a share, at least ([4 tokens over up to 2000 positions, 32 / 8 heads,
+// 128]: 20 us, of 512 24, of 128 18; one token over 32768: 38, 36 and 45).
 constexpr int64_t kAttendLeast = 256;
-// Sequences of at most so many positions are a workgroup's each, however few.
+// Sequences of at most so many positions are a workgroup's each, however few (4
+// tokens over up to 1000 positions 18 us, dealt out 19; over 2000 36, dealt out 20).
 constexpr int64_t kAttendAlone = 1024;
-// Neighbouring heads in a workgroup, at most 2^k of them.
+// Neighbouring heads in a workgroup, at most 2^k of them (32 tokens over up to
+// 32768 positions 403 us; two heads 418, one 453).
 constexpr int64_t kAttendSide = 2;
-// Rows of a sequence, on average, from which on the form for many is taken.
-constexpr int64_t kAttendPrompt = 32;
+// Rows of a sequence from which on the form for many is taken.  The other has 16
+// of a tile, and reads the keys for each: where all sequences have the same number
+// its limit is one tile ([64 tokens over up to 8192 positions, 32 / 2 heads] 70 us,
+// many rows 86; 48 / 2 heads 111, 88), and on average of sequences that differ less
+// (16 of up to 8192 positions, 32 / 8 heads: 10 rows 82 us, 89; 15 rows 101, 90).
+// 8-bit rows become 16 bits on their way to the form for many: three tiles
+// (30 rows 89 us, 110).
+constexpr int64_t kAttendPrompt = acp::kStepRows + 1, kAttendPromptRagged = 12, kAttendPrompt8 = 44;
 
 struct AttendPlan {
   acp::AttendArgs A{};
@@ -56,7 +65,10 @@ acp_status attend_plan(const acp::DescData& q, const CacheSide& k, const acp_seq
   if (P->tokens == 0 || heads == 0 || sequences == 0) return ACP_OK;
   // rows of a sequence: its tokens' query heads of one of the cache's
   const int64_t rows = b->starts ? P->tokens * group : sequences * group;
-  P->tile_rows = rows >= kAttendPrompt * sequences ? 32 * acp::prompt_waves(P->padded) : acp::kStepRows;
+  const int64_t many = k.kind != acp::kCacheSame                   ? kAttendPrompt8
+                       : b->starts && P->tokens > sequences ? kAttendPromptRagged
+                                                            : kAttendPrompt;
+  P->tile_rows = rows >= many * sequences ? 32 * acp::prompt_waves(P->padded) : acp::kStepRows;
   const int64_t M = P->tile_rows;
   const int64_t slots = b->starts ? P->tokens * group / M + sequences : sequences * ceil_div(group, M);
   if (slots >= kRowLimit) return ret(ACP_ERR_UNSUPPORTED, "2^31 tiles of rows");
@@ -76,7 +88,7 @@ acp_status attend_plan(const acp::DescData& q, const CacheSide& k, const acp_seq
   A.once = rows <= M * sequences;
   A.kv_heads = div_by(static_cast<uint64_t>(heads_each));
   int64_t grid = heads_each * slots;
-  if (heads_each * tiles < kAttendTiles * groups && longest > kAttendAlone) {
+  if (heads_each * tiles < groups && longest > kAttendAlone) {
     const int64_t most = std::max<int64_t>(1, groups / heads_each);
     A.shares = static_cast<uint32_t>(std::min(most, slots * ceil_div(longest + 1, kAttendLeast)));
     A.least = static_cast<uint32_t>(kAttendLeast);

