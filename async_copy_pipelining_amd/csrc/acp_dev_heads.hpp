@@ -134,6 +134,22 @@ __device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const Waves<V
   }
 }
 
+// A chunk to a row.  Runs of lanes that fill whole lines of 128 bytes pass the L2s
+// by ([16384, 32 + 8, 128] bfloat16, halves: 58 us, kept 62); of shorter ones two
+// instructions fill a line, which only then is written (20480 tokens appended in
+// pairs of half the channels: 105 us, not kept 110).  Norms, which have more to do
+// for a row, lose more by the branch (60 us, 63).
+template <class T, bool TAIL>
+__device__ __forceinline__ void store_whole(char* p, int n, const rw4& r, bool keep) {
+  if (!keep || n < kChunk<T>) {
+    asm volatile("");  // keeps the branches apart: joined, the stores would lose their policy
+    store_chunk<T, TAIL>(p, n, r);
+    asm volatile("");
+  } else {
+    *reinterpret_cast<rw4_any*>(p) = r;
+  }
+}
+
 // A unit of a row.
 template <class T, bool PAIRS, bool WHOLE>
 struct Piece {
@@ -154,12 +170,12 @@ struct Piece {
     widen(raw[0], a, static_cast<const T*>(nullptr));
     widen(raw[1], b, static_cast<const T*>(nullptr));
   }
-  static __device__ __forceinline__ void store(char* row, const Unit<T, PAIRS>& u, bool there, const float (&a)[V],
-                                               const float (&b)[V]) {
-    store_chunk<T, !WHOLE>(row + u.at[0] * static_cast<int>(sizeof(T)), there ? u.n[0] : 0,
-                           narrow(a, static_cast<const T*>(nullptr)));
-    store_chunk<T, !WHOLE>(row + u.at[1] * static_cast<int>(sizeof(T)), there ? u.n[1] : 0,
-                           narrow(b, static_cast<const T*>(nullptr)));
+  static __device__ __forceinline__ void store(bool keep, char* row, const Unit<T, PAIRS>& u, bool there,
+                                               const float (&a)[V], const float (&b)[V]) {
+    store_whole<T, !WHOLE>(row + u.at[0] * static_cast<int>(sizeof(T)), there ? u.n[0] : 0,
+                           narrow(a, static_cast<const T*>(nullptr)), keep);
+    store_whole<T, !WHOLE>(row + u.at[1] * static_cast<int>(sizeof(T)), there ? u.n[1] : 0,
+                           narrow(b, static_cast<const T*>(nullptr)), keep);
   }
 };
 

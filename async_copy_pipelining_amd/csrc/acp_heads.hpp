@@ -30,6 +30,7 @@ struct HeadsCore {
   int heads_log2;              // heads that a wave handles side by side
   uint32_t per_wave;           // passes over the heads of a wave's tokens that the wave makes
   Div parts;                   // waves that share the passes of one group of tokens
+  uint32_t keep;               // stores stay in the L2s for a while, as store_whole says
   uint32_t groups;             // groups of tokens: the wave's lanes hold 2^(6 - lanes_log2 - heads_log2)
   float turn_scale, sign;      // of cos and sin; -1: turned back
   float eps;

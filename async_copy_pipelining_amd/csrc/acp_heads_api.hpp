@@ -133,6 +133,8 @@ acp_status head_split(int64_t dim, int esize, int pairs, bool one_token, const i
   // a launch has fewer than 2^32 lanes
   if (g * parts >= (int64_t(1) << 26) - 4) return ret(ACP_ERR_UNSUPPORTED, "a launch of 2^32 lanes");
   for (int k = 0; k < sides; ++k) *passes[k] = static_cast<uint32_t>(ceil_div(heads[k], int64_t(1) << hs));
+  const int64_t rest_units = units - turned;
+  A->keep = (turned > 0 && turned < 8) || (rest_units > 0 && rest_units < 8);
   A->lanes_log2 = lanes;
   A->heads_log2 = hs;
   A->groups = static_cast<uint32_t>(g);

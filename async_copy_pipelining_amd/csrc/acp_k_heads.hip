@@ -47,7 +47,7 @@ __device__ __forceinline__ void side_forward(const HeadsCore& A, const HeadSide&
         }
       }
       turn<PAIRS>(a, b, w, u.turned);
-      in.piece[k].store(y + head * S.y.s[2], u, there, a, b);
+      in.piece[k].store(!NORM && A.keep, y + head * S.y.s[2], u, there, a, b);
     }
   }
 }

@@ -62,7 +62,7 @@ __device__ __forceinline__ void side_backward(const HeadsCore& A, const HeadGrad
         a[i] = r * __builtin_fmaf(-a[i], m, ga[i] * wa[i]);
         b[i] = r * __builtin_fmaf(-b[i], m, gb[i] * wb[i]);
       }
-      Piece<T, PAIRS, WHOLE>::store(dx + head[k] * S.dx.s[2], u, there[k], a, b);
+      Piece<T, PAIRS, WHOLE>::store(false, dx + head[k] * S.dx.s[2], u, there[k], a, b);
     }
   }
 }
