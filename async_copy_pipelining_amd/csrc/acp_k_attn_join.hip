@@ -21,6 +21,8 @@ __global__ __launch_bounds__(kAttendThreads) void attend_join_kernel(const Atten
   const uint32_t* record = A.joins + 2 * static_cast<uint64_t>(item);
   const uint32_t first = record[0], splits = record[1];
   if (splits < 2u) return;  // written already
+  // starts that do not ascend give tiles without a record
+  if (first >= A.shares || splits > A.shares - first) return;
   const uint32_t shares = 1u << shares_log2;
   const uint32_t c = (threadIdx.x & ((1u << lanes_log2) - 1u)) * 4u;
   const uint32_t share = threadIdx.x >> lanes_log2 & (shares - 1u);

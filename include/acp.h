@@ -549,13 +549,16 @@ typedef struct {
 /* The sequences of a batch.  All arrays are device int32.
  *   starts      [sequences + 1], ascending: sequence s has the tokens from
  *               starts[s] up to before starts[s + 1], none where these are
- *               equal.  NULL: token s is the one token of sequence s
+ *               equal.  NULL: token s is the one token of sequence s.  Where
+ *               they do not ascend, or leave the tokens, the outputs' rows are
+ *               undefined, and nothing else is touched
  *   lengths     [sequences]: positions of the sequence, its tokens here, which
  *               are the last of them, included
  *   pages       [sequences, max_pages], packed: position p lies in the page
  *               pages[s][p / positions of a page]
  *   max_length  no sequence is longer, where the caller knows it (0: not
- *               known).  Work is split by it; results do not depend on it
+ *               known).  Work is split by it, and with it the order of sums;
+ *               longer sequences are taken in full all the same
  * Nothing of it is read on the host, so a captured graph may be replayed with
  * other contents.  A page number outside the cache, or a position past
  * max_pages, is a position without a page: what is appended there is left

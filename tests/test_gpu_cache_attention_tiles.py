@@ -1,13 +1,15 @@
 """Attention over paged caches on the GPU where tiles of rows and of keys end:
 counts next to their sizes, pages that end inside a wave's rows, rows of every
 alignment, few heads and many."""
+import numpy as np
 import pytest
 
 pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
-from tests.test_gpu_cache_attention import TYPES, check, say  # noqa: E402
+from tests.heads_util import Cache, Field, batch, shuffled_pages  # noqa: E402
+from tests.test_gpu_cache_attention import TYPES, attend, check, say  # noqa: E402
 
 # new tokens, lengths, page, heads, kv heads, channels
 TILES = [
@@ -49,3 +51,19 @@ def test_shares_of_few_rows(dtype, dim, fmt):
         say(f"shares {dtype} {fmt} {dim} {news} {lengths}")
         ran = check(news, lengths, page, heads, kv, dim, dtype, fmt, seed=n, form="few rows", wide=200)
         assert "shares 0" not in ran, ran
+
+
+def test_starts_that_do_not_ascend_touch_nothing_else():
+    """Sequences that overlap, go backwards or leave the tokens: the kernels keep to the outputs and the workspace."""
+    tokens, lengths = 40, (900, 30, 2000, 64)
+    pages, count = shuffled_pages(lengths, 16, 1)
+    for dim in (64, 128):
+        cache = Cache((count, 16, 2, dim), "bf16", seed=1)
+        q = Field((tokens, 8, dim), "bf16", values=np.random.default_rng(2).standard_normal((tokens, 8, dim)))
+        for starts in ((0, 30, 10, 40, 40), (20, 5, 39, 0, 40), (0, 1000, 3, -7, 40), (-5, 40, 2 ** 31 - 1, 0, 1), (7, 7, 7, 7, 7)):
+            for room in (0, 600):
+                say(f"starts {starts} {dim} {room}")
+                table = np.concatenate([pages, np.full((4, room), -1)], axis=1) if room else pages
+                out = Field((tokens, 8, dim), "bf16")
+                attend(out, q, cache, batch(lengths, table, starts), 0.1)
+                assert out.untouched()
