@@ -56,7 +56,8 @@ struct Tokens {
       start = B.starts[seq];
       news = B.starts[seq + 1u] - start;
     }
-    behind = B.lengths[seq] - news;
+    const int32_t length = B.lengths[seq];  // below zero as zero: nothing is seen
+    behind = (length > 0 ? length : 0) - news;
     const int32_t left = static_cast<int32_t>(A.tokens) - start;  // starts past the tokens
     if (start < 0 || left <= 0 || news < 0) news = 0;
     rows = (news < left ? news : left) * static_cast<int32_t>(A.group.d);

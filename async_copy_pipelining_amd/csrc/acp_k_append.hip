@@ -4,8 +4,8 @@
 //
 // Each row is read and written once.  A wave has one token: its sequence, its
 // position and its page are found once for all heads.  20480 new tokens of 32 + 8
-// + 8 heads of 128 bfloat16, half the channels turned: 104 us, 4.8 TB/s.  A step of 64 tokens: 5.7 us, the
-// chain of look-ups.
+// + 8 heads of 128 bfloat16, half the channels turned: 104 us, 4.8 TB/s.  A step of
+// 64 tokens: 5.7 us, the chain of look-ups.
 #include "acp_dev_cache.hpp"
 #include "acp_dev_heads.hpp"
 
@@ -91,7 +91,8 @@ __global__ __launch_bounds__(kHeadThreads) void append_kernel(const AppendArgs A
     if (static_cast<int32_t>(token) < A.batch.starts[seq]) return;
     behind = A.batch.starts[seq + 1u] - static_cast<int32_t>(token);
   }
-  const int32_t position = A.batch.lengths[seq] - behind;
+  const int32_t length = A.batch.lengths[seq];
+  const int32_t position = (length > 0 ? length : 0) - behind;
   int32_t page = -1;
   uint32_t slot = 0;
   if (position >= 0) {

@@ -553,7 +553,7 @@ typedef struct {
  *               they do not ascend, or leave the tokens, the outputs' rows are
  *               undefined, and nothing else is touched
  *   lengths     [sequences]: positions of the sequence, its tokens here, which
- *               are the last of them, included
+ *               are the last of them, included; below zero as zero
  *   pages       [sequences, max_pages], packed: position p lies in the page
  *               pages[s][p / positions of a page]
  *   max_length  no sequence is longer, where the caller knows it (0: not

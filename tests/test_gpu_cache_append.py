@@ -207,3 +207,25 @@ def test_offsets_past_32_bits():
         for t, (g, i) in enumerate(((count - 1, 63), (1 << 18, 0), (0, 4))):
             assert torch.equal(c[g, i], rows[t])
         assert int((c[:, :, 0, 0] != 0).sum()) == 3
+
+
+def test_lengths_below_zero_are_as_zero():
+    """Down to the least: no position is written or seen, queries are turned as at the positions before zero."""
+    lengths, starts = [-2 ** 31, -2 ** 31 + 2, -1, 3], [0, 3, 5, 6, 9]
+    pages = np.arange(8).reshape(4, 2)
+    cache = Cache((8, 16, 2, 64), "f16", seed=1)
+    before = [f.whole.clone() for f in cache.parts]
+    k, v = (Field((9, 2, 64), "f16", values=np.random.default_rng(i).standard_normal((9, 2, 64))) for i in range(2))
+    b = batch(lengths, pages, starts)
+    acp.acp_cache_append(cache.arg, k.desc, v.desc, b, None, None, None, torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    for f, raw, rows in zip(cache.parts, before, (k, v)):
+        assert torch.equal(f.t[6, :3], rows.t[6:9])  # the last sequence's three tokens: positions 0 to 2 of its first page
+        f.t[6, :3] = raw.as_strided(f.t.shape, f.t.stride(), 0)[6, :3]
+        assert torch.equal(f.whole.view(torch.int16), raw.view(torch.int16))
+    q, out = (Field((9, 4, 64), "f16", values=np.random.default_rng(5).standard_normal((9, 4, 64))) for _ in range(2))
+    size = acp.acp_cache_attention_workspace(q.desc, cache.arg, b)
+    work = torch.empty(size + 16, dtype=torch.uint8, device=q.t.device)
+    acp.acp_cache_attention(out.desc, q.desc, cache.arg, b, 0.125, work, size, torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    assert not bool(out.t[:6].any()) and bool(out.t[6:].any())
