@@ -134,6 +134,21 @@ __device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const Waves<V
   }
 }
 
+// A chunk of a row: one load but in rows of less than 16 bytes, which all waves
+// that have none skip.
+template <class T, bool TAIL>
+__device__ __forceinline__ rw4 load_whole(const char* p, int n, bool room) {
+  if constexpr (!TAIL) return load_chunk<T, false, false>(p, n, room);
+  constexpr int V = kChunk<T>;
+  rw4 w{0u, 0u, 0u, 0u};
+  if (n >= V || (room && n > 0)) {
+    w = __builtin_nontemporal_load(reinterpret_cast<const rw4_any*>(p - (n < V ? (V - n) * static_cast<int>(sizeof(T)) : 0)));
+  } else if (n > 0) {
+    w = load_chunk<T, false, true>(p, n, false);
+  }
+  return w;
+}
+
 // A chunk to a row.  Runs of lanes that fill whole lines of 128 bytes pass the L2s
 // by ([16384, 32 + 8, 128] bfloat16, halves: 58 us, kept 62); of shorter ones two
 // instructions fill a line, which only then is written (20480 tokens appended in
@@ -141,13 +156,53 @@ __device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const Waves<V
 // for a row, lose more by the branch (60 us, 63).
 template <class T, bool TAIL>
 __device__ __forceinline__ void store_whole(char* p, int n, const rw4& r, bool keep) {
-  if (!keep || n < kChunk<T>) {
+  constexpr int V = kChunk<T>;
+  constexpr bool kBits = TAIL && sizeof(T) == 2;
+  if (kBits && n < V) {
+    // the bits of n: at most three stores
+    uint32_t a = r[0], b = r[1];
+    if (n & 4) {
+      *reinterpret_cast<rw2_any*>(p) = rw2{a, b};
+      p += 8;
+      a = r[2];
+      b = r[3];
+    }
+    if (n & 2) {
+      *reinterpret_cast<rw1_any*>(p) = a;
+      p += 4;
+      a = b;
+    }
+    if (n & 1) *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(a);
+  } else if (!keep || n < V) {
     asm volatile("");  // keeps the branches apart: joined, the stores would lose their policy
-    store_chunk<T, TAIL>(p, n, r);
+    store_chunk<T, TAIL && !kBits>(p, n, r);
     asm volatile("");
   } else {
     *reinterpret_cast<rw4_any*>(p) = r;
   }
+}
+// V codes of a chunk, as many as n says.
+template <int V, bool TAIL>
+__device__ __forceinline__ void store_whole_codes(char* p, int n, const Codes<V>& c) {
+  if (!TAIL || n >= V) {
+    store_codes<V, false>(p, n, c);
+    return;
+  }
+  uint32_t a = c.w[0];
+  if constexpr (V == 8) {
+    if (n & 4) {
+      *reinterpret_cast<rw1_any*>(p) = a;
+      p += 4;
+      a = c.w[V / 4 - 1];
+    }
+  }
+  if (n & 2) {
+    typedef uint16_t any __attribute__((aligned(1)));
+    *reinterpret_cast<any*>(p) = static_cast<uint16_t>(a);
+    p += 2;
+    a >>= 16;
+  }
+  if (n & 1) *reinterpret_cast<uint8_t*>(p) = static_cast<uint8_t>(a);
 }
 
 // A unit of a row.
@@ -162,7 +217,7 @@ struct Piece {
   __device__ __forceinline__ void load(const char* row, const Unit<T, PAIRS>& u, bool there) {
 #pragma unroll
     for (int k = 0; k < 2; ++k)
-      raw[k] = load_chunk<T, false, !WHOLE>(row + u.at[k] * static_cast<int>(sizeof(T)), there ? u.n[k] : 0, room(u, k));
+      raw[k] = load_whole<T, !WHOLE>(row + u.at[k] * static_cast<int>(sizeof(T)), there ? u.n[k] : 0, room(u, k));
   }
   __device__ __forceinline__ void values(const Unit<T, PAIRS>& u, bool there, float (&a)[V], float (&b)[V]) {
 #pragma unroll

@@ -57,8 +57,8 @@ __device__ __forceinline__ void rows_through(const HeadsCore& A, Passes<T, PAIRS
         const float s = block_scale(format, m);
         const Codes<V> ca = encode<T, V>(format, a, s), cb = encode<T, V>(format, b, s);
         char* row = y + head * y_head;
-        store_codes<V, !WHOLE>(row + u.at[0], there ? u.n[0] : 0, ca);
-        store_codes<V, !WHOLE>(row + u.at[1], there ? u.n[1] : 0, cb);
+        store_whole_codes<V, !WHOLE>(row + u.at[0], there ? u.n[0] : 0, ca);
+        store_whole_codes<V, !WHOLE>(row + u.at[1], there ? u.n[1] : 0, cb);
         if (there && u.at[0] == 0 && u.n[0] > 0) scales[head] = s;
       }
     }
