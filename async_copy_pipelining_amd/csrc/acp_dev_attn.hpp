@@ -168,6 +168,16 @@ struct Walk {
     return n * base + n * (n + 1) / 2 * per_tile(A);
   }
 
+  // Workgroups go to the eight XCDs in turn, so one of 1, 2 or 4 heads has every
+  // P-th.  Each takes shares that follow one another, whose tiles read the same
+  // keys through its L2 (6 chunks of up to 509 tokens over up to 6001, 28 / 4 heads
+  // of 128: 191 us, in turn 195; 64 tokens over up to 4096, 32 / 8: 118, 126).
+  static __device__ __forceinline__ uint32_t together(const AttendArgs& A, uint32_t index, uint32_t shares) {
+    const uint32_t H = A.kv_heads.d;
+    const uint32_t log2 = H == 1u ? 3u : H == 2u ? 2u : H == 4u ? 1u : 0u, P = 1u << log2;
+    const uint32_t p = index & (P - 1u), rest = shares & (P - 1u);
+    return p * (shares >> log2) + (p < rest ? p : rest) + (index >> log2);
+  }
   // false: nothing to do.  All lanes of the workgroup take part.
   __device__ __forceinline__ bool begin_at(const AttendArgs& A, uint32_t index, uint64_t* lds) {
     if constexpr (!SHARES) return true;
@@ -196,8 +206,8 @@ struct Walk {
     total = uniform(total);
     const uint64_t most = (total + A.least - 1) / A.least;
     shares = static_cast<uint32_t>(most < A.shares ? most : A.shares);
-    share = index;
-    if (share >= shares) return false;
+    if (index >= shares) return false;
+    share = together(A, index, shares);
     from = total * share / shares;
     to = total * (share + 1u) / shares;
     if (from >= before_me && from < before_me + mine) {
@@ -306,7 +316,8 @@ struct Partial {
       return;
     }
     wanted = !(w.head && w.tail);
-    row = (static_cast<uint64_t>(blockIdx.x) * 2u + (w.head ? 1u : 0u)) * (static_cast<uint32_t>(M) << A.side_log2);
+    row = ((static_cast<uint64_t>(w.share) * A.kv_heads.d + kv) * 2u + (w.head ? 1u : 0u)) *
+          (static_cast<uint32_t>(M) << A.side_log2);
     if (w.head && threadIdx.x == 0) {
       uint32_t* j = A.joins + 2 * ((Tile::slot_of<M>(A, t.seq) + w.tile) * static_cast<uint64_t>(A.kv_heads.d) + kv);
       j[0] = w.share;
