@@ -204,6 +204,45 @@ __device__ __forceinline__ void put_value(char* p, float v, const bf16_t*) {
   *reinterpret_cast<__bf16*>(p) = static_cast<__bf16>(v);
 }
 
+// float16 weights that carry the scales of 8-bit values: a row's are held in
+// units of a power of two of its own, so that its largest product of a weight and
+// a scale is from 2^8 to 2^15 of them and the smallest are off by 2^-33 of that.
+// Only what the row sees counts: products are zero elsewhere.  The values' scales
+// come as kScale of themselves, which keeps products of weights of up to 2^15
+// in float32's range.
+struct WeightUnit {
+  static constexpr int kScaleLog2 = -16;
+  static constexpr float kScale = 1.0f / 65536.0f;
+  static constexpr float kLeast = 7.888609052210118e-31f;  // 2^-100: what is less is nothing in float16
+  float most = kLeast;  // the largest product so far, by the present maximum
+  float unit = 2.596148429267414e+33f;  // 2^111: a product times this is its weight
+
+  // The row's maximum rose.
+  __device__ __forceinline__ void shrink(float f) { most = __builtin_fmaxf(most * f, kLeast); }
+  // A step's largest product, before its weights are formed: whether some lane's
+  // unit no longer fits.
+  __device__ __forceinline__ bool take(float largest) {
+    most = __builtin_fmaxf(most, largest);
+    return __builtin_amdgcn_ballot_w64(away()) != 0;
+  }
+  // Gives those lanes another, and says by which power of two their sums change.
+  __device__ __forceinline__ int change() {
+    if (!away()) return 0;
+    const int before = log2();
+    unit = as_float(265u - (as_bits(most) >> 23) << 23);  // 2^11 to 2^12
+    return log2() - before;
+  }
+  // What the sums are multiplied by in the end, as a power of two.
+  __device__ __forceinline__ int back() const { return -kScaleLog2 - log2(); }
+
+ private:
+  __device__ __forceinline__ bool away() const {
+    constexpr uint32_t kLow = 135u << 23, kHigh = 142u << 23;  // 2^8, 2^15
+    return as_bits(most * unit) - kLow >= kHigh - kLow;
+  }
+  __device__ __forceinline__ int log2() const { return static_cast<int>(as_bits(unit) >> 23) - 127; }
+};
+
 // ---------------------------------------------------------------- rows that need care
 
 // A weight of zero times a value that is not finite is NaN, so a token's row

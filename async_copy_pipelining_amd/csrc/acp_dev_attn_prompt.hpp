@@ -165,7 +165,8 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
   float m = -__builtin_inff(), l = 0.0f;
-  int v_exp = -200;  // as in the form for few rows
+  constexpr bool kUnits = FMT != kCacheSame && std::is_same_v<T, _Float16>;
+  WeightUnit row_unit;  // kUnits
 
   // Each wave finds the rows of all the tile's keys: lane j has key j.
   auto entry_at = [&](uint32_t key0) { return page_entry(A, t.seq, key0 + lane, keys); };
@@ -274,7 +275,7 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
     if constexpr (FMT != kCacheSame) {
       if (thread < S::kKeys) {
         scales[b][0][thread] = ks;
-        scales[b][1][thread] = vs;
+        scales[b][1][thread] = kUnits ? vs * WeightUnit::kScale : vs;
       }
     }
   };
@@ -407,37 +408,52 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
         l *= shrink;
 #pragma unroll
         for (int d = 0; d < DP / 32; ++d) o[d] *= shrink;
+        if constexpr (kUnits) row_unit.shrink(shrink);
       }
       const float base = m == -__builtin_inff() ? 0.0f : m;
-      float unit = 1.0f;
-      if constexpr (FMT != kCacheSame && std::is_same_v<T, _Float16>) {
-        const float big = __builtin_fmaxf(scales[b][1][lane], 0.0f);
-        const uint32_t most = static_cast<uint32_t>(
-            over_lanes(static_cast<int>(as_bits(big)), 6, [](int x, int y) { return x > y ? x : y; }));
-        const int e = static_cast<int>(most >> 23) - 126;  // big < 2^e
-        const int up = __builtin_amdgcn_readfirstlane(e > v_exp ? e : v_exp);
-        if (up > v_exp) {
-          const float down = v_exp - up < -126 ? 0.0f : as_float(static_cast<uint32_t>(127 + v_exp - up) << 23);
+      // float16 over 8-bit values: all of the tile's products, and the unit that holds them
+      if constexpr (kUnits) {
+        float big = 0.0f;
 #pragma unroll
-          for (int d = 0; d < DP / 32; ++d) o[d] *= down;
-          v_exp = up;
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const af4 x = *reinterpret_cast<const af4*>(&scales[b][1][32 * h + 2 * i + 4 * half]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float p = exp2_of(__builtin_fmaf(s[h][i + e], A.scale, -base));
+              l += p;
+              s[h][i + e] = p > 0.0f ? p * x[e] : 0.0f;
+              big = __builtin_fmaxf(big, __builtin_fabsf(s[h][i + e]));
+            }
+          }
+        if (row_unit.take(max_step<5>(big))) {
+          const int by = row_unit.change();
+#pragma unroll
+          for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[d][i] = __builtin_amdgcn_ldexpf(o[d][i], by);
         }
-        unit = __builtin_amdgcn_ldexpf(1.0f, -v_exp);
       }
       unroll<4>([&](auto N) {
         constexpr uint32_t n = decltype(N)::value;
         if constexpr (!S::kVAhead) values_of(n, a);
         float p[8];
+        if constexpr (kUnits) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] = exp2_of(__builtin_fmaf(s[n / 2u][8 * (n & 1u) + i], A.scale, -base));
-        if constexpr (FMT != kCacheSame) {
+          for (int i = 0; i < 8; ++i) p[i] = s[n / 2u][8 * (n & 1u) + i] * row_unit.unit;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) p[i] = exp2_of(__builtin_fmaf(s[n / 2u][8 * (n & 1u) + i], A.scale, -base));
+        }
+        if constexpr (FMT != kCacheSame && !kUnits) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) l += p[i];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const af4 x = *reinterpret_cast<const af4*>(&scales[b][1][16u * n + 8 * e + 4 * half]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) p[4 * e + i] = p[4 * e + i] > 0.0f ? p[4 * e + i] * (x[i] * unit) : 0.0f;
+            for (int i = 0; i < 4; ++i) p[4 * e + i] = p[4 * e + i] > 0.0f ? p[4 * e + i] * x[i] : 0.0f;
           }
         }
         const rw4 weights = narrow(p, static_cast<const T*>(nullptr));
@@ -464,10 +480,12 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
     next_here = after_here;
     b ^= 1u;
   }
-  if constexpr (FMT != kCacheSame && std::is_same_v<T, _Float16>) {
-    const float unit = __builtin_amdgcn_ldexpf(1.0f, v_exp);
+  if constexpr (kUnits) {
+    const int by = row_unit.back();
 #pragma unroll
-    for (int d = 0; d < DP / 32; ++d) o[d] *= unit;
+    for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[d][i] = __builtin_amdgcn_ldexpf(o[d][i], by);
   }
   l = sum_step<5>(l);
   if (!any) return;

@@ -208,7 +208,8 @@ __device__ __forceinline__ void step_tile(const AttendArgs& A, const Tile& t, co
 #pragma unroll
   for (int d = 0; d < DP / 16; ++d) o[d] = af4{0.0f, 0.0f, 0.0f, 0.0f};
   float m = -__builtin_inff(), l = 0.0f;
-  int v_exp = -200;  // float16 with 8-bit values: o holds sums in units of 2^v_exp
+  constexpr bool kUnits = FMT != kCacheSame && std::is_same_v<T, _Float16>;
+  WeightUnit row_unit;  // kUnits
 
   // Lanes 0..31 (and again 32..63) have a key each: its page, or -1
   auto entry_at = [&](uint32_t key0) { return page_entry(A, t.seq, key0 + (lane & 31u), keys); };
@@ -313,7 +314,7 @@ __device__ __forceinline__ void step_tile(const AttendArgs& A, const Tile& t, co
     entry = entry_at(next + stride);
     const bool more = next < keys;
 
-    if constexpr (FMT != kCacheSame) my_scales[lane] = lane < 32u ? r.ks : r.vs;
+    if constexpr (FMT != kCacheSame) my_scales[lane] = lane < 32u ? r.ks : kUnits ? r.vs * WeightUnit::kScale : r.vs;
     af4 s[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -371,6 +372,7 @@ __device__ __forceinline__ void step_tile(const AttendArgs& A, const Tile& t, co
       l *= shrink;
 #pragma unroll
       for (int d = 0; d < DP / 16; ++d) o[d] *= shrink;
+      if constexpr (kUnits) row_unit.shrink(shrink);
     }
     const float base = m == -__builtin_inff() ? 0.0f : m;
     float p[8], sum = 0.0f;
@@ -381,26 +383,23 @@ __device__ __forceinline__ void step_tile(const AttendArgs& A, const Tile& t, co
     }
     l += sum;
     if constexpr (FMT != kCacheSame) {
-      // the values' scales go into the weights; float16 holds them in units of a
-      // power of two that is at least the largest scale so far
-      float unit = 1.0f;
-      if constexpr (std::is_same_v<T, _Float16>) {
-        float big = ws[0];
+      // the values' scales go into the weights
 #pragma unroll
-        for (int k = 1; k < 8; ++k) big = __builtin_fmaxf(big, ws[k]);
-        big = max_step<5>(max_step<4>(big));
-        const int e = static_cast<int>(as_bits(big) >> 23) - 126;  // big < 2^e
-        const int up = __builtin_amdgcn_readfirstlane(e > v_exp ? e : v_exp);
-        if (up > v_exp) {
-          const float down = v_exp - up < -126 ? 0.0f : as_float(static_cast<uint32_t>(127 + v_exp - up) << 23);
+      for (int k = 0; k < 8; ++k) p[k] = p[k] > 0.0f ? p[k] * ws[k] : 0.0f;
+      if constexpr (kUnits) {
+        float big = 0.0f;
 #pragma unroll
-          for (int d = 0; d < DP / 16; ++d) o[d] *= down;
-          v_exp = up;
+        for (int k = 0; k < 8; ++k) big = __builtin_fmaxf(big, __builtin_fabsf(p[k]));
+        if (row_unit.take(max_step<5>(max_step<4>(big)))) {
+          const int by = row_unit.change();
+#pragma unroll
+          for (int d = 0; d < DP / 16; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[d][i] = __builtin_amdgcn_ldexpf(o[d][i], by);
         }
-        unit = __builtin_amdgcn_ldexpf(1.0f, -v_exp);
-      }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) p[k] = p[k] > 0.0f ? p[k] * (ws[k] * unit) : 0.0f;
+        for (int k = 0; k < 8; ++k) p[k] *= row_unit.unit;
+      }
     }
     const rw4 weights = narrow(p, static_cast<const T*>(nullptr));
 
@@ -442,10 +441,12 @@ __device__ __forceinline__ void step_tile(const AttendArgs& A, const Tile& t, co
     next += stride;
     r = rn;
   }
-  if constexpr (FMT != kCacheSame && std::is_same_v<T, _Float16>) {
-    const float unit = __builtin_amdgcn_ldexpf(1.0f, v_exp);
+  if constexpr (kUnits) {
+    const int by = row_unit.back();
 #pragma unroll
-    for (int d = 0; d < DP / 16; ++d) o[d] *= unit;
+    for (int d = 0; d < DP / 16; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[d][i] = __builtin_amdgcn_ldexpf(o[d][i], by);
   }
   l = sum_step<5>(sum_step<4>(l));
 
