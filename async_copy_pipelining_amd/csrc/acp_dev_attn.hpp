@@ -204,6 +204,19 @@ __device__ __forceinline__ void put_value(char* p, float v, const bf16_t*) {
   *reinterpret_cast<__bf16*>(p) = static_cast<__bf16>(v);
 }
 
+// The running maximum is taken up only when it grows by 2^kRise or more: weights
+// of up to 2^kRise lose nothing, and most steps need no rescaling.  float16 has few
+// powers of two below one, and weights under 2^-25 of a step's largest would be
+// lost, however many they are: its weights are 2^kRoom times theirs, so that those
+// down to 2^-25 of the row's largest keep their digits and others are off by 2^-36
+// of it.  (A rise of 8 leaves a room of 7, so 2^-32, and takes as long: prompts of
+// [2 x 8192 tokens, 32 / 8 heads, 128] 802 us and 801.)
+template <class T, int FMT>
+struct Weights {
+  static constexpr bool kHalf = FMT == kCacheSame && std::is_same_v<T, _Float16>;
+  static constexpr float kRise = kHalf ? 4.0f : 8.0f, kRoom = kHalf ? 11.0f : 0.0f;
+};
+
 // float16 weights that carry the scales of 8-bit values: a row's are held in
 // units of a power of two of its own, so that its largest product of a weight and
 // a scale is from 2^8 to 2^15 of them and the smallest are off by 2^-33 of that.

@@ -400,8 +400,7 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, s[h][i]);
       top = max_step<5>(top) * A.scale;
-      // taken up only when it grows by 2^8 or more, as in the form for few rows
-      if (__builtin_amdgcn_ballot_w64(top > m + 8.0f)) {
+      if (__builtin_amdgcn_ballot_w64(top > m + Weights<T, FMT>::kRise)) {
         const float up = __builtin_fmaxf(m, top);
         const float shrink = exp2_of(m - (up == -__builtin_inff() ? 0.0f : up));
         m = up;
@@ -410,7 +409,7 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
         for (int d = 0; d < DP / 32; ++d) o[d] *= shrink;
         if constexpr (kUnits) row_unit.shrink(shrink);
       }
-      const float base = m == -__builtin_inff() ? 0.0f : m;
+      const float base = m == -__builtin_inff() ? 0.0f : m - Weights<T, FMT>::kRoom;
       // float16 over 8-bit values: all of the tile's products, and the unit that holds them
       if constexpr (kUnits) {
         float big = 0.0f;
@@ -488,6 +487,7 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
       for (int i = 0; i < 16; ++i) o[d][i] = __builtin_amdgcn_ldexpf(o[d][i], by);
   }
   l = sum_step<5>(l);
+  m -= Weights<T, FMT>::kRoom;
   if (!any) return;
   prompt_rows<T, FMT, DP>(attend_args(), t, to, begin, keys, kv, o, m, l);
 }

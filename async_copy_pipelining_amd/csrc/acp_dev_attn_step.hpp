@@ -208,6 +208,7 @@ __device__ __forceinline__ void step_tile(const AttendArgs& A, const Tile& t, co
 #pragma unroll
   for (int d = 0; d < DP / 16; ++d) o[d] = af4{0.0f, 0.0f, 0.0f, 0.0f};
   float m = -__builtin_inff(), l = 0.0f;
+  using W = Weights<T, FMT>;
   constexpr bool kUnits = FMT != kCacheSame && std::is_same_v<T, _Float16>;
   WeightUnit row_unit;  // kUnits
 
@@ -359,13 +360,11 @@ __device__ __forceinline__ void step_tile(const AttendArgs& A, const Tile& t, co
         if (j > left || !(mine & (1u << j))) x[k] = -__builtin_inff();
       }
     }
-    // The running maximum is taken up only when it grows by 2^8 or more: weights
-    // of up to 256 lose nothing, and most steps need no rescaling.
     float top = x[0];
 #pragma unroll
     for (int k = 1; k < 8; ++k) top = __builtin_fmaxf(top, x[k]);
     top = max_step<5>(max_step<4>(top));
-    if (__builtin_amdgcn_ballot_w64(top > m + 8.0f)) {
+    if (__builtin_amdgcn_ballot_w64(top > m + W::kRise)) {
       const float to = __builtin_fmaxf(m, top);
       const float shrink = exp2_of(m - (to == -__builtin_inff() ? 0.0f : to));
       m = to;
@@ -374,7 +373,7 @@ __device__ __forceinline__ void step_tile(const AttendArgs& A, const Tile& t, co
       for (int d = 0; d < DP / 16; ++d) o[d] *= shrink;
       if constexpr (kUnits) row_unit.shrink(shrink);
     }
-    const float base = m == -__builtin_inff() ? 0.0f : m;
+    const float base = m == -__builtin_inff() ? 0.0f : m - W::kRoom;
     float p[8], sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -449,6 +448,7 @@ __device__ __forceinline__ void step_tile(const AttendArgs& A, const Tile& t, co
       for (int i = 0; i < 4; ++i) o[d][i] = __builtin_amdgcn_ldexpf(o[d][i], by);
   }
   l = sum_step<5>(sum_step<4>(l));
+  m -= W::kRoom;
 
   step_rows<T, FMT, DP>(attend_args(), t, to, begin, keys, kv0, o, m, l, lds, join_stat, odd_rows);
 }

@@ -593,7 +593,8 @@ acp_status acp_cache_append(const acp_paged_cache* cache, const acp_tile_desc* k
  *   scale      finite, of the scores: 1 / sqrt(channels) mostly
  * Scores and sums are held in float32; the weights are rounded to the tensors'
  * type before they meet the values, which changes an output by half a step of
- * that type as its own rounding does.  A token that sees no position gives
+ * that type as its own rounding does (f16: weights under 2^-25 of a row's
+ * largest may be off by 2^-36 of it).  A token that sees no position gives
  * zero, scores of -infinity weigh nothing, and what no token may see (positions
  * behind it, pages past the length) changes nothing, whatever it holds.  Tokens
  * of no sequence leave out as it was.
