@@ -455,6 +455,10 @@ __device__ __forceinline__ void prompt_tile(const AttendArgs& A, const Tile& t, 
             for (int i = 0; i < 4; ++i) p[4 * e + i] = p[4 * e + i] > 0.0f ? p[4 * e + i] * x[i] : 0.0f;
           }
         }
+        // Rounded to the type: half a step of each weight, as the output's own
+        // rounding.  In two parts, as the form for few rows has them, the values'
+        // products would double (prompts of [2 x 8192 tokens, 32 / 8 heads, 128]
+        // 1035 us, so 759).
         const rw4 weights = narrow(p, static_cast<const T*>(nullptr));
         if constexpr (FMT == kCacheSame) {
           // the sum of the weights as they were rounded

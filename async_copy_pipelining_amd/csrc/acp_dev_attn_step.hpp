@@ -18,6 +18,9 @@
 // [32 tokens over up to 32768 positions, 32 / 8 heads, 128] bfloat16: 403 us,
 // 6.5 TB/s; 64 over up to 8192 in 8 bits 135 us, 5.0 TB/s, where codes and scales
 // are most of the work.  Two steps ahead, or three workgroups a CU, are no faster.
+// Weights in two 16-bit parts, which leave 2^-17 of each (float16 2^-22) where one
+// part leaves 2^-9 (2^-12), take next to no time: 401 us, with one part 401; in 8
+// bits 135, 134; 3 tokens over up to 700 positions 9.3, 9.0.
 #pragma once
 
 #include "acp_dev_attn.hpp"
@@ -400,7 +403,14 @@ __device__ __forceinline__ void step_tile(const AttendArgs& A, const Tile& t, co
         for (int k = 0; k < 8; ++k) p[k] *= row_unit.unit;
       }
     }
+    // Each weight in two parts, what rounding leaves of it for itself: the matrix
+    // instructions have time to spare.
     const rw4 weights = narrow(p, static_cast<const T*>(nullptr));
+    float kept[8];
+    widen(weights, kept, static_cast<const T*>(nullptr));
+#pragma unroll
+    for (int k = 0; k < 8; ++k) p[k] -= kept[k];
+    const rw4 rest = narrow(p, static_cast<const T*>(nullptr));
 
     // V: rows of channels to columns of keys
     {
@@ -432,7 +442,7 @@ __device__ __forceinline__ void step_tile(const AttendArgs& A, const Tile& t, co
         const ai2 w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((ACP_LDS ai2*)(mine + v_at<S, FMT>(k, d) + (col & 1u) * 8u));
         a = codes_to<T, FMT>(static_cast<uint32_t>(w[0]), static_cast<uint32_t>(w[1]));
       }
-      o[d] = mfma16<T>(a, weights, o[d]);
+      o[d] = mfma16<T>(a, rest, mfma16<T>(a, weights, o[d]));
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();

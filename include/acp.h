@@ -591,10 +591,11 @@ acp_status acp_cache_append(const acp_paged_cache* cache, const acp_tile_desc* k
  *              multiples of 8 (ACP_ERR_UNSUPPORTED else)
  *   cache      of q's type, or in 8 bits; kv heads divide q's
  *   scale      finite, of the scores: 1 / sqrt(channels) mostly
- * Scores and sums are held in float32; the weights are rounded to the tensors'
- * type before they meet the values, which changes an output by half a step of
- * that type as its own rounding does (f16: weights under 2^-25 of a row's
- * largest may be off by 2^-36 of it).  A token that sees no position gives
+ * Scores and sums are held in float32.  The weights meet the values in 16 bits:
+ * where a sequence's rows of a head are few, in two parts, which leave an output
+ * its own rounding; where they are many, rounded to the tensors' type, which
+ * changes an output by half a step of that type as its own rounding does (f16:
+ * weights under 2^-25 of a row's largest may be off by 2^-36 of it).  A token that sees no position gives
  * zero, scores of -infinity weigh nothing, and what no token may see (positions
  * behind it, pages past the length) changes nothing, whatever it holds.  Tokens
  * of no sequence leave out as it was.

@@ -9,7 +9,8 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
-from tests.heads_util import U, Cache, Field, batch  # noqa: E402
+from oracle import heads as H  # noqa: E402
+from tests.heads_util import U, Cache, Field, batch, shuffled_pages  # noqa: E402
 from tests.rows_util import DTYPES, close, out_step  # noqa: E402
 from tests.test_gpu_cache_attention import TYPES, attend  # noqa: E402
 
@@ -39,3 +40,31 @@ def test_a_long_tail_of_small_weights(dtype, score, tokens, split):
     eps = torch.finfo(DTYPES[dtype]).eps / 2
     low = length * 2.0 ** -36 if dtype == "f16" else 0.0
     close(out.values(), want, want * (eps + (4 * score + 2 + 64) * U) * 1.01 + low + out_step(dtype, want), (score, ran))
+
+
+@pytest.mark.parametrize("fmt", [None, "i8", "e4m3"])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_few_rows_hold_weights_in_two_parts(dtype, fmt):
+    """Nothing but the output's rounding shows: single tokens and short chunks, split or not."""
+    for n, (news, lengths, page, heads, kv, dim, wide) in enumerate((
+            ((1, 1, 1), (700, 33, 512), 16, 8, 2, 128, 0), ((4, 1), (90, 300), 7, 4, 2, 64, 0), ((2, 1), (400, 120), 32, 3, 1, 256, 0),
+            ((1, 1), (3000, 500), 16, 16, 4, 80, 400))):
+        pages, count = shuffled_pages(lengths, page, n)
+        if wide:
+            pages = np.concatenate([pages, np.full((len(lengths), wide), -1)], axis=1)
+        cache = Cache((count, page, kv, dim), dtype, fmt, seed=n)
+        first = np.concatenate([[0], np.cumsum(news)])
+        tokens = int(first[-1])
+        q = Field((tokens, heads, dim), dtype, values=np.random.default_rng(n).standard_normal((tokens, heads, dim)))
+        out = Field((tokens, heads, dim), dtype)
+        ran = attend(out, q, cache, batch(lengths, pages, first), 0.125)
+        assert "few rows" in ran and ("shares 0" not in ran) == bool(wide)
+        places = H.token_places(first, lengths, tokens)
+        want, size, spread = H.attend(q.values(), cache.values(0), cache.values(1), places, pages, 0.125, True)
+        # two parts of 8 bits (float16: 11) leave 2^-17 (2^-22); float16 under 2^-25 of the largest product 2^-33 of it
+        eps = 2.0 ** -17 if dtype == "bf16" else 2.0 ** -22
+        codes = {None: 1, "i8": 128, "e4m3": 448}[fmt]
+        scales = cache.scales[1].double().cpu().numpy() if fmt else np.abs(cache.values(1)).max()
+        low = max(lengths) * 2.0 ** -33 * codes * np.max(scales) if dtype == "f16" else 0.0
+        bound = size * (eps + (max(lengths) + 16) * U) + spread * (dim + 8) * U + low + out_step(dtype, want)
+        close(out.values(), want, bound, (ran, news, lengths))
