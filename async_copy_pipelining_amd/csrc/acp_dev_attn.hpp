@@ -128,6 +128,36 @@ __device__ __forceinline__ af16 mfma32(const rw4& a, const rw4& b, af16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(ab8, a), __builtin_bit_cast(ab8, b), c, 0, 0, 0);
 }
 
+// Eight weights in two parts of T.  The first is cut off towards zero, so that the
+// other is above zero too: an infinite value times both is infinite, and not the
+// difference of two.  Its least keeps it from zero where the first part is the
+// whole weight; 8-bit values are finite, and need none.
+template <class T, int FMT>
+__device__ __forceinline__ void two_parts(const float (&p)[8], rw4* first, rw4* second) {
+  constexpr bool kHalf = std::is_same_v<T, _Float16>;
+  constexpr float kLeast = FMT != kCacheSame ? 0.0f : kHalf ? 5.9604644775390625e-8f : 7.888609052210118e-31f;  // 2^-24, 2^-100
+  float rest[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float a = p[2 * k], b = p[2 * k + 1];
+    float c, d;
+    if constexpr (kHalf) {
+      const auto w = __builtin_amdgcn_cvt_pkrtz(a, b);
+      (*first)[k] = __builtin_bit_cast(uint32_t, w);
+      c = static_cast<float>(w[0]);
+      d = static_cast<float>(w[1]);
+    } else {
+      (*first)[k] = __builtin_amdgcn_perm(as_bits(b), as_bits(a), 0x07060302u);
+      c = as_float(as_bits(a) & 0xFFFF0000u);
+      d = as_float(as_bits(b) & 0xFFFF0000u);
+    }
+    // between the least and the weight: zero where that is, the least where both are infinite
+    rest[2 * k] = __builtin_amdgcn_fmed3f(a - c, kLeast, a);
+    rest[2 * k + 1] = __builtin_amdgcn_fmed3f(b - d, kLeast, b);
+  }
+  *second = narrow(rest, static_cast<const T*>(nullptr));
+}
+
 // 16 bytes for each lane from its address to LDS: lane l's come to offset + 16 l.
 // The waits are the caller's (s_nop: between the write of M0 and its use).
 __device__ __forceinline__ void to_lds(const char* from, uint32_t offset) {

@@ -18,8 +18,8 @@
 // [32 tokens over up to 32768 positions, 32 / 8 heads, 128] bfloat16: 403 us,
 // 6.5 TB/s; 64 over up to 8192 in 8 bits 135 us, 5.0 TB/s, where codes and scales
 // are most of the work.  Two steps ahead, or three workgroups a CU, are no faster.
-// Weights in two 16-bit parts, which leave 2^-17 of each (float16 2^-22) where one
-// part leaves 2^-9 (2^-12), take next to no time: 401 us, with one part 401; in 8
+// Weights in two 16-bit parts, which leave 2^-16 of each (float16 2^-22) where one
+// part leaves 2^-8 (2^-11), take next to no time: 401 us, with one part 401; in 8
 // bits 135, 134; 3 tokens over up to 700 positions 9.3, 9.0.
 #pragma once
 
@@ -403,14 +403,9 @@ __device__ __forceinline__ void step_tile(const AttendArgs& A, const Tile& t, co
         for (int k = 0; k < 8; ++k) p[k] *= row_unit.unit;
       }
     }
-    // Each weight in two parts, what rounding leaves of it for itself: the matrix
-    // instructions have time to spare.
-    const rw4 weights = narrow(p, static_cast<const T*>(nullptr));
-    float kept[8];
-    widen(weights, kept, static_cast<const T*>(nullptr));
-#pragma unroll
-    for (int k = 0; k < 8; ++k) p[k] -= kept[k];
-    const rw4 rest = narrow(p, static_cast<const T*>(nullptr));
+    // each weight in two parts: the matrix instructions have time to spare
+    rw4 weights, rest;
+    two_parts<T, FMT>(p, &weights, &rest);
 
     // V: rows of channels to columns of keys
     {

@@ -61,10 +61,56 @@ def test_few_rows_hold_weights_in_two_parts(dtype, fmt):
         assert "few rows" in ran and ("shares 0" not in ran) == bool(wide)
         places = H.token_places(first, lengths, tokens)
         want, size, spread = H.attend(q.values(), cache.values(0), cache.values(1), places, pages, 0.125, True)
-        # two parts of 8 bits (float16: 11) leave 2^-17 (2^-22); float16 under 2^-25 of the largest product 2^-33 of it
-        eps = 2.0 ** -17 if dtype == "bf16" else 2.0 ** -22
+        # the first part keeps 8 bits (float16: 11), cut off: less than 2^-7 (2^-10) of the weight's power of two is left,
+        # half a step of which is 2^-16 (2^-22).  float16 whose second part ends below 2^-24, of a largest weight of 2^11
+        # or a largest product of 2^8: 2^-33 of it
+        eps = 2.0 ** -16 if dtype == "bf16" else 2.0 ** -22
         codes = {None: 1, "i8": 128, "e4m3": 448}[fmt]
         scales = cache.scales[1].double().cpu().numpy() if fmt else np.abs(cache.values(1)).max()
         low = max(lengths) * 2.0 ** -33 * codes * np.max(scales) if dtype == "f16" else 0.0
         bound = size * (eps + (max(lengths) + 16) * U) + spread * (dim + 8) * U + low + out_step(dtype, want)
         close(out.values(), want, bound, (ran, news, lengths))
+
+
+@pytest.mark.parametrize("value", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_values_that_are_not_finite_stay_what_they_are(dtype, value):
+    """In one channel of one position that all tokens see: there the output is what the formula says, elsewhere it is
+    what it was."""
+    for n, (news, lengths, heads, kv, dim, wide) in enumerate((
+            ((1, 1), (40, 300), 4, 2, 64, 0), ((3, 2), (90, 40), 6, 3, 128, 0), ((1,), (3000,), 8, 1, 128, 300),
+            ((2,), (500,), 2, 2, 256, 0), ((70, 33), (100, 90), 4, 1, 64, 0), ((100,), (3000,), 8, 2, 128, 300))):
+        pages, count = shuffled_pages(lengths, 16, n)
+        if wide:
+            pages = np.concatenate([pages, np.full((len(lengths), wide), -1)], axis=1)
+        cache = Cache((count, 16, kv, dim), dtype, seed=n)
+        first = np.concatenate([[0], np.cumsum(news)])
+        tokens = int(first[-1])
+        q = Field((tokens, heads, dim), dtype, values=np.random.default_rng(n).standard_normal((tokens, heads, dim)))
+        got = []
+        for bad in (False, True):
+            if bad:
+                cache.parts[1].t[pages[0, 0], 2, :, 5] = value
+            out = Field((tokens, heads, dim), dtype)
+            attend(out, q, cache, batch(lengths, pages, first), 0.125)
+            got.append(out.values())
+        hit = np.zeros(got[0].shape, bool)
+        hit[:news[0], :, 5] = True
+        # rows that were computed again take their keys in another order, with weights of their own rounding
+        eps = torch.finfo(DTYPES[dtype]).eps
+        close(got[1][~hit], got[0][~hit], 2 * eps * np.abs(got[0][~hit]) + eps * 4, (value, news, lengths))
+        assert np.array_equal(got[1][hit], np.full(hit.sum(), value), equal_nan=True), (value, news, lengths)
+
+
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_scales_that_are_infinite_give_infinite_outputs(dtype, fmt):
+    for news, length in ((1, 50), (3, 50), (80, 90)):
+        cache = Cache((8, 16, 1, 64), dtype, fmt, seed=news)
+        cache.parts[1].t[1, 4] = 0x31  # a code above zero in every channel
+        cache.scales[1][1, 4] = np.inf
+        q = Field((news, 2, 64), dtype, values=np.random.default_rng(3).standard_normal((news, 2, 64)))
+        out = Field((news, 2, 64), dtype)
+        attend(out, q, cache, batch([length], np.arange(8)[None], [0, news]), 0.125)
+        sees = length - news + np.arange(news) >= 20
+        assert np.all(out.values()[sees] == np.inf) and np.isfinite(out.values()[~sees]).all()
