@@ -6,8 +6,10 @@ for gfx950).  Pointer arguments accept an ``int`` device address or any
 object with ``data_ptr()`` (a torch tensor); stream arguments accept an
 ``int`` handle or an object with ``cuda_stream`` (a torch stream).  A non-OK
 status raises ``AcpError`` carrying the status and ``acp_last_error()``.  The
-row operators' float32 arrays and workspaces, which have no descriptor, are
-checked here where they are tensors: type, length, no gaps.
+operators' arrays and workspaces, which have no descriptor, are checked here
+where they are tensors: type, length, no gaps.  ``acp_packed8``, ``acp_rotary``
+and ``acp_sequences`` keep the tensors of their arrays alive; a descriptor is an
+address, and what it describes is the caller's to keep.
 
 Importing this package fails when ``libacp.so`` has not been built: there is
 no fallback path.
@@ -105,6 +107,7 @@ class acp_packed8(ctypes.Structure):
             n = math.prod(shape[:-1]) * -(-shape[-1] // block)
         super().__init__(ctypes.pointer(codes), _floats(scales, n, "the scales"),
                          FORMATS[fmt] if isinstance(fmt, str) else int(fmt), int(block))
+        self._arrays = scales
 
 
 _PACKED_P = ctypes.POINTER(acp_packed8)
@@ -117,6 +120,7 @@ class acp_rotary(ctypes.Structure):
     def __init__(self, frequencies, rotated: int, layout="halves", scale: float = 1.0):
         super().__init__(_array(frequencies, max(0, int(rotated)) // 2, _F64, "the frequencies"), int(rotated),
                          ROTARY_LAYOUTS[layout] if isinstance(layout, str) else int(layout), scale)
+        self._arrays = frequencies
 
 
 class acp_paged_cache(ctypes.Structure):
@@ -138,6 +142,7 @@ class acp_sequences(ctypes.Structure):
     def __init__(self, lengths, pages, sequences: int, max_pages: int, starts=None, max_length: int = 0):
         super().__init__(_array(starts, sequences + 1, _I32, "starts"), _array(lengths, sequences, _I32, "lengths"),
                          _array(pages, sequences * max_pages, _I32, "pages"), sequences, max_pages, max_length)
+        self._arrays = starts, lengths, pages
 
 
 _ROTARY_P = ctypes.POINTER(acp_rotary)
