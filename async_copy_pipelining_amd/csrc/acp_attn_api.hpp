@@ -138,7 +138,8 @@ acp_status cache_attention(const acp_tile_desc* out, const acp_tile_desc* q, con
   if (st == ACP_OK) st = check_like(od, qd, true, "the output");
   if (st == ACP_OK) st = attend_plan(qd, k, b, &P);
   if (st != ACP_OK) return st;
-  if (!std::isfinite(scale)) return ret(ACP_ERR_INVALID, "the scale is not finite");
+  // times log2 e it is a number of float32 still
+  if (!(std::fabs(scale) <= 0x1p127f)) return ret(ACP_ERR_INVALID, "the scale is not finite, or past 2^127");
   if (self_overlap(od)) return ret(ACP_ERR_INVALID, "the output overlaps itself");
   if (P.workspace > 0) {
     if (!workspace || workspace_bytes < P.workspace)
@@ -168,15 +169,16 @@ acp_status cache_attention(const acp_tile_desc* out, const acp_tile_desc* q, con
   if ((st = check_stream(stream)) != ACP_OK) return st;
   set_cache(k, &A.k);
   set_cache(v, &A.v);
-  // a scale of zero becomes the least: a weight of what is hidden stays zero
   auto aligned16 = [](const CacheSide& c) {
     bool all = c.d.gbase % 16 == 0;
     for (int d = 0; d < 3; ++d) all = all && (c.d.shape[d] == 1 || c.d.strides[d] * c.d.esize % 16 == 0);
     return all;
   };
   A.direct = k.kind == acp::kCacheSame && aligned16(k) && aligned16(v);
+  // zero becomes the least there is, which leaves any score under 2^-21: a weight of
+  // what is hidden stays zero
   A.scale = std::max(static_cast<float>(std::fabs(static_cast<double>(scale)) * 1.4426950408889634),
-                     std::numeric_limits<float>::min());
+                     std::numeric_limits<float>::denorm_min());
   A.flip = scale < 0.0f ? 0x80008000u : 0u;
   A.part = static_cast<float*>(workspace);
   A.stat = reinterpret_cast<float*>(static_cast<char*>(workspace) + P.stat_at);

@@ -590,7 +590,7 @@ acp_status acp_cache_append(const acp_paged_cache* cache, const acp_tile_desc* k
  *   out, q     [tokens, heads, channels] of f16 or bf16, up to 256 channels in
  *              multiples of 8 (ACP_ERR_UNSUPPORTED else)
  *   cache      of q's type, or in 8 bits; kv heads divide q's
- *   scale      finite, of the scores: 1 / sqrt(channels) mostly
+ *   scale      of the scores, up to 2^127 in size: 1 / sqrt(channels) mostly
  * Scores and sums are held in float32.  The weights meet the values in 16 bits:
  * where a sequence's rows of a head are few, in two parts, which leave an output
  * its own rounding; where they are many, rounded to the tensors' type, which
