@@ -339,9 +339,8 @@ __device__ __forceinline__ void row_by_keys(const AttendArgs& A, const Tile& t, 
       dot = __builtin_fmaf(q[e], kc, dot);
     }
     const float s = sum_lanes(dot, 6) * A.scale;
-    if (s == -__builtin_inff()) continue;
-    const float top = __builtin_fmaxf(m, s);
-    const float shrink = exp2_of(m - top), p = exp2_of(s - top);
+    const float top = __builtin_fmaxf(m, s), base = top == -__builtin_inff() ? 0.0f : top;
+    const float shrink = exp2_of(m - base), p = exp2_of(s - base);
     l = l * shrink + p;
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = __builtin_fmaf(p, v[e], o[e] * shrink);

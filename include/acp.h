@@ -595,10 +595,11 @@ acp_status acp_cache_append(const acp_paged_cache* cache, const acp_tile_desc* k
  * where a sequence's rows of a head are few, in two parts, which leave an output
  * its own rounding; where they are many, rounded to the tensors' type, which
  * changes an output by half a step of that type as its own rounding does (f16:
- * weights under 2^-25 of a row's largest may be off by 2^-36 of it).  A token that sees no position gives
- * zero, scores of -infinity weigh nothing, and what no token may see (positions
- * behind it, pages past the length) changes nothing, whatever it holds.  Tokens
- * of no sequence leave out as it was.
+ * weights under 2^-25 of a row's largest may be off by 2^-36 of it).
+ * A token that sees no position gives zero, scores of -infinity weigh nothing
+ * (zero times a value that is not finite is NaN, as in the formula), and what no
+ * token may see (positions behind it, pages past the length) changes nothing,
+ * whatever it holds.  Tokens of no sequence leave out as it was.
  * acp_cache_attention_workspace gives the bytes of workspace that the call
  * needs at most (may be 0): partial results where few rows are split over a
  * long context.  It depends on the shapes, on sequences, max_pages and

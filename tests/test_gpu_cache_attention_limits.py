@@ -32,3 +32,31 @@ def test_scales_at_the_ends_of_float32(scale, size, tokens, fmt):
     eps = torch.finfo(DTYPES["bf16"]).eps / 2
     size = np.stack([np.abs(v[:length - tokens + t + 1]).mean(axis=0) for t in range(tokens)])[:, None]
     close(out.values(), want, size * (eps + 2.0 ** -14) + eps * np.abs(want), (scale, tokens))
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES)[:2])
+@pytest.mark.parametrize("news, lengths", [((1,), (40,)), ((4,), (40,)), ((3, 2), (2500, 40)), ((100,), (140,)), ((70,), (2500,))])
+def test_a_weight_of_zero_times_a_value_that_is_not_finite_is_nan(news, lengths, dtype):
+    """A position that all tokens see, whose score is -infinity and whose value has a NaN, and a later one of a NaN that
+    only the last token sees: rows computed again say of the first what other rows say, as the formula does."""
+    dim = 64
+    pages = np.arange(2 * 160).reshape(2, 160)[:len(news)]
+    cache = Cache((320, 16, 1, dim), dtype, seed=2)
+    first = np.concatenate([[0], np.cumsum(news)])
+    tokens = int(first[-1])
+    q = Field((tokens, 2, dim), dtype, values=np.abs(np.random.default_rng(3).standard_normal((tokens, 2, dim))) + 0.1)
+    cache.parts[0].t[0, 2] = -np.inf
+    cache.parts[1].t[0, 2, 0, 5] = np.nan
+    last = lengths[0] - 1
+    cache.parts[1].t[int(pages[0][last // 16]), last % 16, 0, 9] = np.nan
+    out = Field((tokens, 2, dim), dtype)
+    attend(out, q, cache, batch(lengths, pages, first), 0.125)
+    nan = np.isnan(out.values())
+    want = np.zeros(nan.shape, bool)
+    want[:news[0], :, 5] = True
+    want[news[0] - 1, :, 9] = True
+    assert np.array_equal(nan, want), (news, lengths, np.argwhere(nan != want)[:5])
+    # without the values' NaN it weighs nothing
+    cache.parts[1].t.nan_to_num_(nan=1.0)
+    attend(out, q, cache, batch(lengths, pages, first), 0.125)
+    assert np.isfinite(out.values()).all()
