@@ -576,8 +576,9 @@ typedef struct {
  * and the new values [tokens, kv heads, channels] into the pages of their
  * positions, and where q is given the queries, turned, to yq.  8-bit caches:
  * codes and scales as acp_pack8 has them, of the turned keys in float32.
- * Tokens of no sequence leave all outputs as they were; of two tokens with one
- * place in the cache, one is written. */
+ * Tokens of no sequence leave all outputs as they were.  Of several tokens with
+ * one place in the cache (sequences that share a page, and a length) any may be
+ * written there, or parts of them, codes and scales of different ones too. */
 acp_status acp_cache_append(const acp_paged_cache* cache, const acp_tile_desc* k, const acp_tile_desc* v,
                             const acp_sequences* sequences, const acp_rotary* rotary, const acp_tile_desc* yq,
                             const acp_tile_desc* q, void* hip_stream);
