@@ -7,9 +7,10 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
-from tests.heads_util import Cache, Field, batch  # noqa: E402
+from oracle import heads as H  # noqa: E402
+from tests.heads_util import Cache, Field, batch, shuffled_pages  # noqa: E402
 from tests.rows_util import DTYPES, close  # noqa: E402
-from tests.test_gpu_cache_attention import attend  # noqa: E402
+from tests.test_gpu_cache_attention import attend, bound_of  # noqa: E402
 
 
 @pytest.mark.parametrize("fmt", [None, "i8"])
@@ -60,3 +61,22 @@ def test_a_weight_of_zero_times_a_value_that_is_not_finite_is_nan(news, lengths,
     cache.parts[1].t.nan_to_num_(nan=1.0)
     attend(out, q, cache, batch(lengths, pages, first), 0.125)
     assert np.isfinite(out.values()).all()
+
+
+@pytest.mark.parametrize("fmt", [None, "e4m3"])
+@pytest.mark.parametrize("dtype", list(DTYPES)[:2])
+def test_scales_below_zero(dtype, fmt):
+    """The softmax of minus the scores, in every form."""
+    for n, (news, lengths, split) in enumerate((((1, 1), (40, 300), False), ((3, 2), (2500, 40), True), ((90, 60), (100, 333), False),
+                                                ((70,), (2500,), True))):
+        pages, count = shuffled_pages(lengths, 16, n)
+        first = np.concatenate([[0], np.cumsum(news)])
+        tokens = int(first[-1])
+        cache = Cache((count, 16, 2, 64), dtype, fmt, seed=n)
+        q = Field((tokens, 4, 64), dtype, values=np.random.default_rng(n).standard_normal((tokens, 4, 64)))
+        out = Field((tokens, 4, 64), dtype)
+        ran = attend(out, q, cache, batch(lengths, pages, first), -0.125)
+        assert ("shares 0" not in ran) == split, ran
+        places = H.token_places(first, lengths, tokens)
+        want, size, spread = H.attend(q.values(), cache.values(0), cache.values(1), places, pages, -0.125, True)
+        close(out.values(), want, bound_of(want, size, spread, dtype, cache, max(lengths)), ran)
