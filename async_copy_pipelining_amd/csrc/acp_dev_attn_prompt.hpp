@@ -80,6 +80,10 @@ __device__ __forceinline__ void prompt_rows(const AttendArgs& A, const Tile& t, 
 #pragma unroll
       for (int i = 0; i < 16; ++i) fine = fine && is_finite(o[d][i]);
     odd = __builtin_amdgcn_ballot_w64(!fine && real && t.position(A, row) + 1 < t.keys);
+    if (odd != 0u) {
+      const int32_t last = last_odd_value<T, FMT>(A, t, begin, keys, kv);
+      odd &= __builtin_amdgcn_ballot_w64(t.position(A, row) < last);
+    }
     odd = (odd | odd >> 32) & 0xFFFFFFFFu;
   }
   if (real && !(odd >> col & 1u)) {

@@ -128,6 +128,21 @@ __device__ __forceinline__ void step_rows(const AttendArgs& A, const Tile& t, co
   const uint32_t my_row = t.first + jr;
   const bool row_real = my_row < static_cast<uint32_t>(t.rows);
   const bool mixed = t.low + 1 < t.keys;  // rows that see less than others
+  // Of the rows that are not finite those that do not see a value that is not.
+  // The workgroup takes part.
+  auto look_again = [&] {
+    __syncthreads();
+    uint32_t any = 0;
+    for (uint32_t g = 0; g < side; ++g) any |= odd_rows[g];
+    if (any == 0u) return;
+    __syncthreads();
+    if (wave < side) {
+      const int32_t last = last_odd_value<T, FMT>(A, t, begin, keys, kv0 + wave);
+      const uint64_t m = __builtin_amdgcn_ballot_w64(lane < kStepRows && t.position(A, t.first + lane) < last);
+      if (lane == 0) odd_rows[wave] &= static_cast<uint32_t>(m);
+    }
+    __syncthreads();
+  };
 #pragma unroll
   for (int h = 0; h < kParts; ++h) {
     __syncthreads();
@@ -149,10 +164,11 @@ __device__ __forceinline__ void step_rows(const AttendArgs& A, const Tile& t, co
       }
     }
     if (kParts > 1 && mixed) continue;  // written below, once all channels were looked at
-    if (mixed) __syncthreads();
+    if (mixed) look_again();
     join_out<T, S, kWide>(A, t, to, kv0, h, stage, join_stat, odd_rows, jr, jc, row_real);
   }
   if (kParts > 1 && mixed) {
+    look_again();
 #pragma unroll
     for (int h = 0; h < kParts; ++h) {
       __syncthreads();

@@ -80,3 +80,39 @@ def test_scales_below_zero(dtype, fmt):
         places = H.token_places(first, lengths, tokens)
         want, size, spread = H.attend(q.values(), cache.values(0), cache.values(1), places, pages, -0.125, True)
         close(out.values(), want, bound_of(want, size, spread, dtype, cache, max(lengths)), ran)
+
+
+@pytest.mark.parametrize("fmt", [None, "e4m3"])
+@pytest.mark.parametrize("dtype", list(DTYPES)[:2])
+def test_rows_that_see_a_value_that_is_not_finite_are_computed_once(dtype, fmt):
+    """A NaN in one channel of the oldest position, which all rows see: every other channel keeps its bits, also in tiles
+    whose rows see different keys.  With one behind them too, the rows before it keep theirs but for the order of keys."""
+    for n, (news, lengths, heads, dim) in enumerate((((6, 3), (50, 19), 4, 128), ((3, 1, 2), (3000, 40, 1500), 6, 64),
+                                                     ((7,), (33,), 2, 256), ((130, 70), (131, 200), 4, 128),
+                                                     ((150, 64), (2900, 64), 4, 64), ((90,), (100,), 2, 256))):
+        pages, count = shuffled_pages(lengths, 16, n)
+        first = np.concatenate([[0], np.cumsum(news)])
+        tokens = int(first[-1])
+        cache = Cache((count, 16, 2, dim), dtype, fmt, seed=n)
+        q = Field((tokens, heads, dim), dtype, values=np.random.default_rng(n).standard_normal((tokens, heads, dim)))
+        bad = 0x7F if fmt else np.nan
+        got = []
+        for step in range(3):
+            if step == 1:
+                for s in range(len(news)):
+                    cache.parts[1].t[pages[s, 0], 0, :, 5] = bad
+            if step == 2:
+                at = lengths[0] - 1
+                cache.parts[1].t[pages[0, at // 16], at % 16, :, 9] = bad
+            out = Field((tokens, heads, dim), dtype)
+            attend(out, q, cache, batch(lengths, pages, first), 0.125)
+            got.append(out)
+        rest = np.arange(dim) != 5
+        assert torch.equal(got[1].t[..., rest], got[0].t[..., rest]) and bool(got[1].t[..., 5].isnan().all())
+        nan = np.zeros((tokens, heads, dim), bool)
+        nan[..., 5] = True
+        nan[news[0] - 1, :, 9] = True
+        assert np.array_equal(np.isnan(got[2].values()), nan)
+        eps = torch.finfo(DTYPES[dtype]).eps
+        a, b = got[0].values()[~nan], got[2].values()[~nan]
+        close(b, a, 2 * eps * np.abs(a) + 4 * eps * np.abs(cache.values(1)[np.isfinite(cache.values(1))]).max(), n)
