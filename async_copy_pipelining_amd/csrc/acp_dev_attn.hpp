@@ -142,7 +142,10 @@ __device__ __forceinline__ void two_parts(const float (&p)[8], rw4* first, rw4* 
     const float a = p[2 * k], b = p[2 * k + 1];
     float c, d;
     if constexpr (kHalf) {
-      const auto w = __builtin_amdgcn_cvt_pkrtz(a, b);
+      // less the least, so that small weights are rounded to nearest and not up
+      constexpr bool small = FMT == kCacheSame;
+      const auto w = __builtin_amdgcn_cvt_pkrtz(small ? __builtin_fmaxf(a - kLeast, 0.0f) : a,
+                                                small ? __builtin_fmaxf(b - kLeast, 0.0f) : b);
       (*first)[k] = __builtin_bit_cast(uint32_t, w);
       c = static_cast<float>(w[0]);
       d = static_cast<float>(w[1]);

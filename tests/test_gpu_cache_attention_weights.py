@@ -114,3 +114,26 @@ def test_scales_that_are_infinite_give_infinite_outputs(dtype, fmt):
         attend(out, q, cache, batch([length], np.arange(8)[None], [0, news]), 0.125)
         sees = length - news + np.arange(news) >= 20
         assert np.all(out.values()[sees] == np.inf) and np.isfinite(out.values()[~sees]).all()
+
+
+@pytest.mark.parametrize("score", [17.9375, 18.625])
+def test_small_weights_are_rounded_to_nearest(score):
+    """float16, few rows: a tail whose weights, 2^11 e^-score in steps of 2^-24, lie next above a whole number, under a
+    large one for each of a workgroup's waves, which take 32 keys in turn."""
+    page, dim, length = 256, 64, 1 << 17
+    cache = Cache((2, page, 1, dim), "f16", seed=1)
+    cache.parts[0].t.zero_()
+    cache.parts[1].t.fill_(1.0)
+    cache.parts[0].t[0, :128:32, 0, 0] = score / 4
+    cache.parts[1].t[0, :128:32] = 0.0
+    table = np.ones((1, length // page), np.int64)
+    table[0, 0] = 0
+    q, out = Field((1, 2, dim), "f16", values=np.full((1, 2, dim), 4.0)), Field((1, 2, dim), "f16")
+    ran = attend(out, q, cache, batch([length], table, [0, 1], 1000), 1.0)
+    assert "few rows" in ran and "shares 0" in ran
+    w = (length - 4) * math.exp(-score)
+    want = np.full((1, 2, dim), w / (4 + w))
+    # each weight is off by 2^-36 of the largest, which there are four of; the rest as above
+    bound = length * 2.0 ** -36 / 4 + want * (4 * score + 66) * U + out_step("f16", want)
+    assert 0.02 < math.exp(-score) * 2.0 ** 35 % 1 < 0.12 and length * 0.85 * 2.0 ** -35 / 4 > bound.max()
+    close(out.values(), want, bound, (score, ran))
