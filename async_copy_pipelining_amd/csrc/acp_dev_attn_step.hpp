@@ -15,7 +15,7 @@
 // while this one is computed: 16 KiB a wave for 128 channels of 16 bits, and
 // eight waves a CU keep twice the bytes in flight that its share of HBM needs.
 //
-// [32 tokens over up to 32768 positions, 32 / 8 heads, 128] bfloat16: 403 us,
+// [32 tokens over up to 32768 positions, 32 / 8 heads, 128] bfloat16: 401 us,
 // 6.5 TB/s; 64 over up to 8192 in 8 bits 135 us, 5.0 TB/s, where codes and scales
 // are most of the work.  Two steps ahead, or three workgroups a CU, are no faster.
 // Weights in two 16-bit parts, which leave 2^-16 of each (float16 2^-22) where one

@@ -459,7 +459,7 @@ acp_status acp_group_norm_backward(const acp_tile_desc* dx, float* dgamma, float
  * dims; keys may have fewer heads than queries.  Bases need only their
  * element's alignment.  What is said of the row operators holds here too:
  * overlaps (but an output may be the very tensor that it is made from: the
- * same address, shape and strides), empty tensors, workspaces, fixed order of
+ * same address, shape and strides; not attention's), empty tensors, workspaces, fixed order of
  * all sums, streams and graphs.  A head goes up to 1024 channels (f32: 512;
  * somewhat fewer where turned and other channels end inside chunks), else
  * ACP_ERR_UNSUPPORTED. */
@@ -469,8 +469,9 @@ acp_status acp_group_norm_backward(const acp_tile_desc* dx, float* dgamma, float
  *   (a, b) -> scale * (a cos - b sin, b cos + a sin)
  *   ACP_ROTARY_HALVES  a and b are channels i and i + rotated / 2
  *   ACP_ROTARY_PAIRS   a and b are channels 2 i and 2 i + 1
- * The other channels stay as they are.  Angles are formed in float64, so far
- * positions lose nothing; cos and sin are good to 2^-22. */
+ * The other channels stay as they are.  Angles are formed in float64: cos and
+ * sin are good to 2^-22 up to angles of 2^28 radians, and past them to 2^-52 of
+ * the angle more (2^-20 at the last position, 2^31 - 1). */
 typedef enum { ACP_ROTARY_HALVES = 0, ACP_ROTARY_PAIRS = 1 } acp_rotary_layout;
 
 typedef struct {
@@ -510,7 +511,8 @@ acp_status acp_rotate(const acp_tile_desc* yq, const acp_tile_desc* q, const acp
 
 /* Norm of every head of queries and keys, then the rotation, in one pass:
  *   y = R (x * rstd * w),  rstd = 1 / sqrt(mean of x^2 over the head + eps)
- *   wq, wk     device float32 [channels]; NULL: 1
+ *   wq, wk     device float32 [channels]; NULL: 1.  wk is not looked at without
+ *              k (the backward pass, which would owe its gradient, refuses it)
  *   eps        finite, >= 0
  *   rotary     NULL: no rotation; else positions as acp_rotate has them
  * A head with a NaN or an infinity, or whose squares' sum overflows float32,
@@ -600,7 +602,9 @@ acp_status acp_cache_append(const acp_paged_cache* cache, const acp_tile_desc* k
  * A token that sees no position gives zero, scores of -infinity weigh nothing
  * (zero times a value that is not finite is NaN, as in the formula), and what no
  * token may see (positions behind it, pages past the length) changes nothing,
- * whatever it holds.  Tokens of no sequence leave out as it was.
+ * whatever it holds: rows beside a value that is not finite, and that they do not
+ * see, are computed again without it, in another order and slowly.  Tokens of no
+ * sequence leave out as it was.
  * acp_cache_attention_workspace gives the bytes of workspace that the call
  * needs at most (may be 0): partial results where few rows are split over a
  * long context.  It depends on the shapes, on sequences, max_pages and
