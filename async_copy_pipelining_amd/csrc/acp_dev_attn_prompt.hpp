@@ -10,7 +10,7 @@
 // 16-bit values in registers on the way, as do rows of odd alignment.
 //
 // [2 x 8192 tokens, 32 / 8 heads, 128] bfloat16: 746 to 767 us, 975 to 1003 TFLOP/s
-// of the tokens' own scores and values (single launches under a trace 765 to 823),
+// of the tokens' own scores and values (single launches under a trace 757 to 816),
 // where a product of 8192^3 by the library reaches 1227.  With 32 rows a wave the LDS has as many cycles of reads as there
 // are of matrix instructions, and the exponentials have half as many again; two
 // waves a SIMD overlap them as they come.  Not better: one of the two half a tile
